@@ -1,0 +1,436 @@
+// Dispatch of a batch's rows to the experts and back, as operators of their
+// own: moe_permute, moe_unpermute, their gradients and the router's gradient
+// (mxfp6-sm120 page, "Execution model": indirect routing and the unpermuting
+// reduction; TokenSpeed SiTU page, "Supported contract": expert shards).
+//
+// With row p = row_of[t, j] of assignment (t, j), -1 where there is none:
+//   permute            rows[p] = x[t]
+//   its gradient       dx[t] = sum_j drows[p]
+//   unpermute          y[t] = residual[t] + sum_j w[t, j] rows[p]
+//   its gradient       drows[p] = w[t, j] dy[t],  dw[t, j] = <dy[t], rows[p]>
+// The gradient of permute is unpermute without weights or residual.  Sums are
+// held in fp32 and added in slot order, and each output is rounded once; no
+// order depends on scheduling, so results repeat bit for bit.
+//
+// All of them move rows and compute next to nothing: the bound is memory
+// traffic (or, for a few tokens, the launch).  Work is therefore laid out so
+// that each row is read once and written once: the gathers and the sums hold
+// one 16-byte piece of a token's row per thread and walk its k rows with up to
+// kSlots of them in flight.  Rows whose address or stride is not a multiple of
+// 16 bytes, or whose length is not a whole number of 16-byte pieces, go
+// element by element.
+#include <hip/hip_runtime.h>
+
+#include "internal.h"
+
+namespace moe_mx {
+
+namespace {
+
+constexpr int kSlots = 8;            // rows of a token in flight per thread
+constexpr int64_t kMaxBlocks = 1 << 20;
+constexpr int kThreadsD = 256;
+
+// Row elements: V of type T per access.
+template <typename T, int V> struct alignas(sizeof(T) * V) Pack {
+  T v[V];
+};
+__device__ __forceinline__ float to_f32(__bf16 v) { return (float)v; }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+
+// Threads of a workgroup are groups of `tpr` neighbours, one row per group;
+// thread c of a group owns piece c of the row's column block.
+struct RowMap {
+  int tpr, lg;       // threads per row (a power of two) and its logarithm
+  int pieces;        // pieces per row
+  int cblocks;       // column blocks of tpr pieces
+  int64_t nrows;     // rows
+  int64_t nblocks;   // workgroup-sized units of work
+};
+
+// The widest group of at most 256 threads that leaves at most an eighth of its
+// threads without a piece; rows shorter than 64 pieces take the next power of
+// two, so that short rows share a wave.
+RowMap row_map(int64_t nrows, int64_t pieces) {
+  RowMap m;
+  int lg = 8;
+  if (pieces < 64) {
+    lg = 0;
+    while ((1 << lg) < pieces) ++lg;
+  } else {
+    for (; lg > 6; --lg) {
+      const int64_t t = (int64_t)1 << lg, span = (pieces + t - 1) / t * t;
+      if ((span - pieces) * 8 <= span) break;
+    }
+  }
+  m.lg = lg;
+  m.tpr = 1 << lg;
+  m.pieces = (int)pieces;
+  m.cblocks = (int)((pieces + m.tpr - 1) / m.tpr);
+  m.nrows = nrows;
+  const int64_t rpb = kThreadsD >> lg;
+  m.nblocks = (nrows + rpb - 1) / rpb * m.cblocks;
+  return m;
+}
+
+// (row, piece) of this thread in unit b, or false
+__device__ __forceinline__ bool row_piece(const RowMap& m, int64_t b, int64_t& row, int& c) {
+  const int64_t rb = b / m.cblocks;
+  const int cb = (int)(b - rb * m.cblocks);
+  row = rb * (kThreadsD >> m.lg) + (threadIdx.x >> m.lg);
+  c = cb * m.tpr + (threadIdx.x & (m.tpr - 1));
+  return row < m.nrows && c < m.pieces;
+}
+
+unsigned grid_blocks(int64_t n) { return (unsigned)(n < 1 ? 1 : n > kMaxBlocks ? kMaxBlocks : n); }
+
+// Local segment [base, end) of sorted_assign, within its A entries
+__device__ __forceinline__ void local_segment(const int32_t* offsets, int lo, int n, int64_t A, int64_t& base,
+                                              int64_t& end) {
+  base = min((int64_t)max(offsets[lo], 0), A);
+  end = max(min((int64_t)max(offsets[lo + n], 0), A), base);
+}
+
+// ------------------------------------------------------------- permute ---
+
+// One row per assignment g of sorted_assign: row g - base is the row of its
+// token; thread 0 of the row notes where it went.
+template <typename P>
+__global__ __launch_bounds__(kThreadsD) void k_permute_rows(RowMap m, const P* __restrict__ x, int64_t x_ld, int k,
+                                                            const int32_t* __restrict__ offsets,
+                                                            const int32_t* __restrict__ sorted_assign, int lo, int n,
+                                                            P* __restrict__ rows, int64_t rows_ld, int64_t num_rows,
+                                                            int32_t* __restrict__ row_of) {
+  int64_t base, end;
+  local_segment(offsets, lo, n, m.nrows, base, end);
+  for (int64_t b = blockIdx.x; b < m.nblocks; b += gridDim.x) {
+    int64_t g;
+    int c;
+    if (!row_piece(m, b, g, c)) continue;
+    const int32_t a = sorted_assign[g];
+    if (a < 0 || a >= m.nrows) continue;
+    const bool here = g >= base && g < end && g - base < num_rows;
+    if (c == 0) row_of[a] = here ? (int32_t)(g - base) : -1;
+    if (here) rows[(g - base) * rows_ld + c] = x[(int64_t)(a / k) * x_ld + c];
+  }
+}
+
+// ----------------------------------------------------------- unpermute ---
+
+// y[t] = residual[t] + sum over slots j of (w[t, j]) rows[row_of[t, j]]
+template <typename T, int V, bool WEIGHTED>
+__global__ __launch_bounds__(kThreadsD) void k_gather_sum(RowMap m, const T* __restrict__ rows, int64_t rows_ld,
+                                                          int num_rows, const int32_t* __restrict__ row_of,
+                                                          const float* __restrict__ w, int k, const T* residual,
+                                                          int64_t res_ld, T* y, int64_t y_ld) {
+  using P = Pack<T, V>;
+  for (int64_t b = blockIdx.x; b < m.nblocks; b += gridDim.x) {
+    int64_t t;
+    int c;
+    if (!row_piece(m, b, t, c)) continue;
+    float s[V];
+    if (residual) {
+      const P r = *(const P*)(residual + t * res_ld + (int64_t)c * V);
+#pragma unroll
+      for (int q = 0; q < V; ++q) s[q] = to_f32(r.v[q]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < V; ++q) s[q] = 0.f;
+    }
+    for (int j0 = 0; j0 < k; j0 += kSlots) {
+      P v[kSlots];
+      float wt[kSlots];
+      bool use[kSlots];
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        const int32_t p = j0 + q < k ? row_of[t * k + j0 + q] : -1;
+        use[q] = p >= 0 && p < num_rows;
+        wt[q] = WEIGHTED && use[q] ? w[t * k + j0 + q] : 1.f;
+        if (use[q]) v[q] = *(const P*)(rows + (int64_t)p * rows_ld + (int64_t)c * V);
+      }
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q)
+        if (use[q]) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) s[i] = WEIGHTED ? fmaf(wt[q], to_f32(v[q].v[i]), s[i]) : s[i] + to_f32(v[q].v[i]);
+        }
+    }
+    P o;
+#pragma unroll
+    for (int q = 0; q < V; ++q) o.v[q] = (T)s[q];
+    *(P*)(y + t * y_ld + (int64_t)c * V) = o;
+  }
+}
+
+// drows[row_of[t, j]] = w[t, j] dy[t] and dw[t, j] = <dy[t], rows[row_of[t, j]]>:
+// one workgroup per token; the slots are taken kSlots at a time, each thread
+// holding one partial dot product per slot over its pieces of the row.
+template <typename T, int V>
+__global__ __launch_bounds__(kThreadsD) void k_unpermute_grad(int64_t tokens, int pieces, const T* __restrict__ dy,
+                                                              int64_t dy_ld, const T* __restrict__ rows,
+                                                              int64_t rows_ld, int num_rows,
+                                                              const int32_t* __restrict__ row_of,
+                                                              const float* __restrict__ w, int k,
+                                                              T* __restrict__ drows, int64_t drows_ld,
+                                                              float* __restrict__ dw) {
+  using P = Pack<T, V>;
+  __shared__ float part[kThreadsD / 64][kSlots];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+    for (int j0 = 0; j0 < k; j0 += kSlots) {
+      int32_t p[kSlots];
+      float wt[kSlots], dot[kSlots];
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        p[q] = j0 + q < k ? row_of[t * k + j0 + q] : -1;
+        if (p[q] >= num_rows) p[q] = -1;
+        wt[q] = p[q] >= 0 ? w[t * k + j0 + q] : 0.f;
+        dot[q] = 0.f;
+      }
+      for (int c = threadIdx.x; c < pieces; c += kThreadsD) {
+        const P g = *(const P*)(dy + t * dy_ld + (int64_t)c * V);
+        P v[kSlots];
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q)
+          if (p[q] >= 0) v[q] = *(const P*)(rows + (int64_t)p[q] * rows_ld + (int64_t)c * V);
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q)
+          if (p[q] >= 0) {
+            P o;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const float gi = to_f32(g.v[i]);
+              dot[q] = fmaf(gi, to_f32(v[q].v[i]), dot[q]);
+              o.v[i] = (T)(wt[q] * gi);
+            }
+            *(P*)(drows + (int64_t)p[q] * drows_ld + (int64_t)c * V) = o;
+          }
+      }
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) dot[q] += __shfl_xor(dot[q], d);
+        if (lane == 0) part[wv][q] = dot[q];
+      }
+      __syncthreads();
+      if (threadIdx.x < kSlots && j0 + (int)threadIdx.x < k) {
+        float s = part[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < kThreadsD / 64; ++i) s += part[i][threadIdx.x];
+        dw[t * k + j0 + threadIdx.x] = s;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// -------------------------------------------------------- router gradient ---
+
+// The weights of a token are the softmax of its chosen logits, so
+//   dlogits[t, e_j] = w_j (dw_j - sum_i w_i dw_i), and 0 for the others.
+// One wave per token builds the row in LDS (zeros, then the chosen entries) and
+// writes it out with neighbouring lanes on neighbouring columns.  Ids outside
+// [0, E) are left out of the row, not of the sum.
+constexpr int kRouteWaves = 4;
+__global__ __launch_bounds__(64 * kRouteWaves) void k_route_grad(const int32_t* __restrict__ ids,
+                                                                 const float* __restrict__ w,
+                                                                 const float* __restrict__ dw, int64_t tokens, int E,
+                                                                 int k, float* __restrict__ dlogits) {
+  __shared__ float row[kRouteWaves][kMaxExperts];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  float* r = row[wv];
+  // the wave's LDS accesses before it are complete for its other lanes after it
+  auto wave_sync = [] {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
+  for (int64_t t0 = (int64_t)blockIdx.x * kRouteWaves; t0 < tokens; t0 += (int64_t)gridDim.x * kRouteWaves) {
+    const int64_t t = t0 + wv;
+    if (t < tokens) {
+      float s = 0.f;
+      for (int j = lane; j < k; j += 64) s = fmaf(w[t * k + j], dw[t * k + j], s);
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+      for (int e = lane; e < E; e += 64) r[e] = 0.f;
+      wave_sync();
+      for (int j = lane; j < k; j += 64) {
+        const int32_t e = ids[t * k + j];
+        if (e >= 0 && e < E) atomicAdd(&r[e], w[t * k + j] * (dw[t * k + j] - s));
+      }
+      wave_sync();
+      for (int e = lane; e < E; e += 64) dlogits[t * E + e] = r[e];
+      wave_sync();
+    }
+  }
+}
+
+// ------------------------------------------------------------ host side ---
+
+bool src_ok(moe_src_t d) { return d == MOE_SRC_BF16 || d == MOE_SRC_FP32; }
+int64_t elem_size(moe_src_t d) { return d == MOE_SRC_BF16 ? 2 : 4; }
+bool aligned(const void* p, int64_t n) { return (uintptr_t)p % (uintptr_t)n == 0; }
+// a row matrix that 16-byte pieces can walk
+bool pieces16(const void* p, int64_t ld, int64_t es) { return aligned(p, 16) && ld * es % 16 == 0; }
+
+// Sizes every dispatch operator shares.
+moe_status_t check_sizes(moe_src_t dtype, int32_t T, int32_t H, int32_t k) {
+  if (!src_ok(dtype) || T < 0 || H < 1 || k < 1) return MOE_ERR_INVALID_ARG;
+  if ((int64_t)T * k > (int64_t)1 << 30 || H > 1 << 24) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+// a row matrix argument: present, element-aligned, rows at least H apart
+bool matrix_ok(const void* p, int64_t ld, int32_t H, moe_src_t dtype) {
+  return p && ld >= H && aligned(p, elem_size(dtype));
+}
+
+moe_status_t launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+
+template <typename T, int V>
+void launch_gather_sum(const void* rows, int64_t rows_ld, int32_t num_rows, const int32_t* row_of, const float* w,
+                       int32_t T_, int32_t H, int32_t k, const void* residual, int64_t res_ld, void* y, int64_t y_ld,
+                       hipStream_t st) {
+  const RowMap m = row_map(T_, H / V);
+  const unsigned g = grid_blocks(m.nblocks);
+  if (w)
+    k_gather_sum<T, V, true><<<g, kThreadsD, 0, st>>>(m, (const T*)rows, rows_ld, num_rows, row_of, w, k,
+                                                      (const T*)residual, res_ld, (T*)y, y_ld);
+  else
+    k_gather_sum<T, V, false><<<g, kThreadsD, 0, st>>>(m, (const T*)rows, rows_ld, num_rows, row_of, w, k,
+                                                       (const T*)residual, res_ld, (T*)y, y_ld);
+}
+
+// moe_unpermute, and with w and residual null the gradient of moe_permute
+moe_status_t gather_sum(const void* rows, moe_src_t dtype, int64_t rows_ld, int32_t num_rows, const int32_t* row_of,
+                        const float* w, int32_t T, int32_t H, int32_t k, const void* residual, int64_t res_ld,
+                        void* y, int64_t y_ld, hipStream_t stream) {
+  moe_status_t a = check_arch();
+  if (a != MOE_OK) return a;
+  const int64_t es = elem_size(dtype);
+  const bool vec = (int64_t)H * es % 16 == 0 && pieces16(y, y_ld, es) && (num_rows == 0 || pieces16(rows, rows_ld, es)) &&
+                   (!residual || pieces16(residual, res_ld, es));
+  if (dtype == MOE_SRC_BF16) {
+    if (vec) launch_gather_sum<__bf16, 8>(rows, rows_ld, num_rows, row_of, w, T, H, k, residual, res_ld, y, y_ld, stream);
+    else launch_gather_sum<__bf16, 1>(rows, rows_ld, num_rows, row_of, w, T, H, k, residual, res_ld, y, y_ld, stream);
+  } else {
+    if (vec) launch_gather_sum<float, 4>(rows, rows_ld, num_rows, row_of, w, T, H, k, residual, res_ld, y, y_ld, stream);
+    else launch_gather_sum<float, 1>(rows, rows_ld, num_rows, row_of, w, T, H, k, residual, res_ld, y, y_ld, stream);
+  }
+  return launched();
+}
+
+}  // namespace
+
+}  // namespace moe_mx
+
+using namespace moe_mx;
+
+// ------------------------------------------------------- public entry points
+
+extern "C" moe_status_t moe_permute(const void* x, moe_src_t dtype, int64_t x_ld, int32_t T, int32_t H, int32_t E,
+                                    int32_t k, const int32_t* expert_offsets, const int32_t* sorted_assign,
+                                    int32_t local_expert_offset, int32_t local_num_experts, void* rows,
+                                    int64_t rows_ld, int32_t num_rows, int32_t* row_of, hipStream_t stream) {
+  moe_status_t v = check_sizes(dtype, T, H, k);
+  if (v != MOE_OK) return v;
+  if (E < 1 || E > kMaxExperts || k > E || num_rows < 0) return MOE_ERR_INVALID_ARG;
+  const int32_t n = local_num_experts == 0 ? E : local_num_experts;
+  if (local_expert_offset < 0 || n < 0 || (int64_t)local_expert_offset + n > E) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!expert_offsets || !sorted_assign || !row_of || !matrix_ok(x, x_ld, H, dtype)) return MOE_ERR_INVALID_ARG;
+  if (num_rows > 0 && !matrix_ok(rows, rows_ld, H, dtype)) return MOE_ERR_INVALID_ARG;
+  moe_status_t a = check_arch();
+  if (a != MOE_OK) return a;
+  const int64_t es = elem_size(dtype), A = (int64_t)T * k;
+  const bool vec = (int64_t)H * es % 16 == 0 && pieces16(x, x_ld, es) && (num_rows == 0 || pieces16(rows, rows_ld, es));
+  const int V = vec ? (int)(16 / es) : 1;
+  const RowMap m = row_map(A, H / V);
+  const unsigned g = grid_blocks(m.nblocks);
+  if (vec)
+    k_permute_rows<uint4><<<g, kThreadsD, 0, stream>>>(m, (const uint4*)x, x_ld / V, k, expert_offsets, sorted_assign,
+                                                       local_expert_offset, n, (uint4*)rows, rows_ld / V, num_rows,
+                                                       row_of);
+  else if (dtype == MOE_SRC_BF16)
+    k_permute_rows<uint16_t><<<g, kThreadsD, 0, stream>>>(m, (const uint16_t*)x, x_ld, k, expert_offsets,
+                                                          sorted_assign, local_expert_offset, n, (uint16_t*)rows,
+                                                          rows_ld, num_rows, row_of);
+  else
+    k_permute_rows<uint32_t><<<g, kThreadsD, 0, stream>>>(m, (const uint32_t*)x, x_ld, k, expert_offsets,
+                                                          sorted_assign, local_expert_offset, n, (uint32_t*)rows,
+                                                          rows_ld, num_rows, row_of);
+  return launched();
+}
+
+extern "C" moe_status_t moe_permute_backward(const void* drows, moe_src_t dtype, int64_t drows_ld, int32_t num_rows,
+                                             const int32_t* row_of, int32_t T, int32_t H, int32_t k, void* dx,
+                                             int64_t dx_ld, hipStream_t stream) {
+  moe_status_t v = check_sizes(dtype, T, H, k);
+  if (v != MOE_OK) return v;
+  if (num_rows < 0) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!row_of || !matrix_ok(dx, dx_ld, H, dtype)) return MOE_ERR_INVALID_ARG;
+  if (num_rows > 0 && !matrix_ok(drows, drows_ld, H, dtype)) return MOE_ERR_INVALID_ARG;
+  return gather_sum(drows, dtype, drows_ld, num_rows, row_of, nullptr, T, H, k, nullptr, 0, dx, dx_ld, stream);
+}
+
+extern "C" moe_status_t moe_unpermute(const void* rows, moe_src_t dtype, int64_t rows_ld, int32_t num_rows,
+                                      const int32_t* row_of, const float* topk_w, int32_t T, int32_t H, int32_t k,
+                                      const void* residual, int64_t residual_ld, void* y, int64_t y_ld,
+                                      hipStream_t stream) {
+  moe_status_t v = check_sizes(dtype, T, H, k);
+  if (v != MOE_OK) return v;
+  if (num_rows < 0) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!row_of || !topk_w || !matrix_ok(y, y_ld, H, dtype)) return MOE_ERR_INVALID_ARG;
+  if (num_rows > 0 && !matrix_ok(rows, rows_ld, H, dtype)) return MOE_ERR_INVALID_ARG;
+  if (residual && !matrix_ok(residual, residual_ld, H, dtype)) return MOE_ERR_INVALID_ARG;
+  return gather_sum(rows, dtype, rows_ld, num_rows, row_of, topk_w, T, H, k, residual, residual_ld, y, y_ld, stream);
+}
+
+template <typename T, int V>
+static void launch_unpermute_grad(const void* dy, int64_t dy_ld, const void* rows, int64_t rows_ld, int32_t num_rows,
+                                  const int32_t* row_of, const float* w, int32_t tokens, int32_t H, int32_t k,
+                                  void* drows, int64_t drows_ld, float* dw, hipStream_t st) {
+  k_unpermute_grad<T, V><<<grid_blocks(tokens), kThreadsD, 0, st>>>(tokens, H / V, (const T*)dy, dy_ld, (const T*)rows,
+                                                                    rows_ld, num_rows, row_of, w, k, (T*)drows,
+                                                                    drows_ld, dw);
+}
+
+extern "C" moe_status_t moe_unpermute_backward(const void* dy, moe_src_t dtype, int64_t dy_ld, const void* rows,
+                                               int64_t rows_ld, int32_t num_rows, const int32_t* row_of,
+                                               const float* topk_w, int32_t T, int32_t H, int32_t k, void* drows,
+                                               int64_t drows_ld, float* dw, hipStream_t stream) {
+  moe_status_t v = check_sizes(dtype, T, H, k);
+  if (v != MOE_OK) return v;
+  if (num_rows < 0) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!row_of || !topk_w || !dw || !matrix_ok(dy, dy_ld, H, dtype)) return MOE_ERR_INVALID_ARG;
+  if (num_rows > 0 && (!matrix_ok(rows, rows_ld, H, dtype) || !matrix_ok(drows, drows_ld, H, dtype)))
+    return MOE_ERR_INVALID_ARG;
+  moe_status_t a = check_arch();
+  if (a != MOE_OK) return a;
+  const int64_t es = elem_size(dtype);
+  const bool vec = (int64_t)H * es % 16 == 0 && pieces16(dy, dy_ld, es) &&
+                   (num_rows == 0 || (pieces16(rows, rows_ld, es) && pieces16(drows, drows_ld, es)));
+  if (dtype == MOE_SRC_BF16) {
+    if (vec) launch_unpermute_grad<__bf16, 8>(dy, dy_ld, rows, rows_ld, num_rows, row_of, topk_w, T, H, k, drows, drows_ld, dw, stream);
+    else launch_unpermute_grad<__bf16, 1>(dy, dy_ld, rows, rows_ld, num_rows, row_of, topk_w, T, H, k, drows, drows_ld, dw, stream);
+  } else {
+    if (vec) launch_unpermute_grad<float, 4>(dy, dy_ld, rows, rows_ld, num_rows, row_of, topk_w, T, H, k, drows, drows_ld, dw, stream);
+    else launch_unpermute_grad<float, 1>(dy, dy_ld, rows, rows_ld, num_rows, row_of, topk_w, T, H, k, drows, drows_ld, dw, stream);
+  }
+  return launched();
+}
+
+extern "C" moe_status_t moe_route_backward(const int32_t* topk_ids, const float* topk_w, const float* dw, int32_t T,
+                                           int32_t E, int32_t k, float* dlogits, hipStream_t stream) {
+  if (T < 0 || E < 1 || E > kMaxExperts || k < 1 || k > E) return MOE_ERR_INVALID_ARG;
+  if ((int64_t)T * k > (int64_t)1 << 30) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!topk_ids || !topk_w || !dw || !dlogits) return MOE_ERR_INVALID_ARG;
+  moe_status_t a = check_arch();
+  if (a != MOE_OK) return a;
+  k_route_grad<<<grid_blocks(((int64_t)T + kRouteWaves - 1) / kRouteWaves), 64 * kRouteWaves, 0, stream>>>(
+      topk_ids, topk_w, dw, T, E, k, dlogits);
+  return launched();
+}

@@ -23,7 +23,8 @@ ACTS = {"bf16": 0, "mxfp8": 1}
 ACT_FNS = {"silu": 0, "relu2": 1, "swiglu_oai": 2}
 
 # Every symbol include/moe_mx.h declares.
-EXPORTS = ("mx_quantize", "moe_route_workspace_bytes", "moe_route", "mx_gemm_workspace_bytes", "mx_gemm",
+EXPORTS = ("mx_quantize", "moe_route_workspace_bytes", "moe_route", "moe_permute", "moe_permute_backward",
+           "moe_unpermute", "moe_unpermute_backward", "moe_route_backward", "mx_gemm_workspace_bytes", "mx_gemm",
            "moe_fused_workspace_bytes", "moe_fused", "moe_fused_workspace_offset", "moe_fused_noalloc",
            "moe_status_str", "moe_mx_version")
 NOALLOC_SCRATCH_BYTES = 32 << 20  # MOE_NOALLOC_SCRATCH_BYTES
@@ -79,6 +80,17 @@ def lib() -> ctypes.CDLL:
         L.mx_gemm.argtypes = [vp, vp, i64, i64, i64, ctypes.c_int, vp, vp, ctypes.c_int, ctypes.c_float, vp, vp,
                               sz, vp]
         L.mx_gemm.restype = ctypes.c_int
+        i = ctypes.c_int
+        L.moe_permute.argtypes = [vp, i, i64, i32, i32, i32, i32, vp, vp, i32, i32, vp, i64, i32, vp, vp]
+        L.moe_permute.restype = i
+        L.moe_permute_backward.argtypes = [vp, i, i64, i32, vp, i32, i32, i32, vp, i64, vp]
+        L.moe_permute_backward.restype = i
+        L.moe_unpermute.argtypes = [vp, i, i64, i32, vp, vp, i32, i32, i32, vp, i64, vp, i64, vp]
+        L.moe_unpermute.restype = i
+        L.moe_unpermute_backward.argtypes = [vp, i, i64, vp, i64, i32, vp, vp, i32, i32, i32, vp, i64, vp, vp]
+        L.moe_unpermute_backward.restype = i
+        L.moe_route_backward.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp]
+        L.moe_route_backward.restype = i
         L.moe_fused_noalloc.argtypes = [ctypes.POINTER(MoeProblem), ctypes.POINTER(MoeTensors), vp]
         L.moe_fused_noalloc.restype = ctypes.c_int
         L.moe_fused_workspace_offset.argtypes = [ctypes.POINTER(MoeProblem), ctypes.c_int]
@@ -206,6 +218,297 @@ def moe_route(logits: torch.Tensor, k: int, workspace: torch.Tensor | None = Non
     _check(lib().moe_route(_ptr(logits), T, E, k, _ptr(ids), _ptr(w), _ptr(off), _ptr(sa),
                            _ptr(workspace), workspace.numel(), _stream(stream)), "moe_route")
     return ids, w, off, sa
+
+
+# ------------------------------------------------------- operator calls --
+
+class _Plan:
+    """One checked and marshalled call of a C entry point: everything but the
+    stream, which is its last argument."""
+    __slots__ = ("name", "fn", "args", "result", "device", "keep")
+
+    def __init__(self, name, args, result, device, keep):
+        # sizes cross the ABI as 32-bit integers, strides and addresses as 64-bit
+        for v, ctype in zip(args, getattr(lib(), name).argtypes):
+            if ctype is ctypes.c_int32 and not -2 ** 31 <= v < 2 ** 31:
+                raise ValueError(f"{name}: size {v} does not fit 32 bits")
+        self.name, self.fn, self.args = name, getattr(lib(), name), args
+        self.result, self.device, self.keep = result, device, keep
+
+    def launch(self, stream):
+        if torch.cuda.current_device() != self.device.index:
+            raise ValueError(f"{self.name}: tensors on {self.device}, which is not the current device")
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        elif stream.device != self.device:
+            raise ValueError(f"{self.name}: stream on {stream.device}, tensors on {self.device}")
+        status = self.fn(*self.args, stream.cuda_stream)
+        if status != MOE_OK:
+            raise MoeError(status, self.name)
+        return self.result
+
+
+_PLANNERS = {}  # operator -> function that plans a call of it
+
+
+def _operator(planner):
+    """The operator planned by `planner` (same arguments, and `stream`)."""
+    def decorate(fn):
+        _PLANNERS[fn] = planner
+        return fn
+    return decorate
+
+
+class OpCall:
+    """One operator call (moe_permute, moe_unpermute, their gradients,
+    moe_route_backward) with its arguments checked and marshalled and its
+    outputs allocated once, for loops that call it many times on the same
+    buffers (their contents may change between calls): each call then costs the
+    host only the C call.  The stream is the current one at each call unless
+    one is given.  Calling returns the operator's outputs, the same tensors each
+    time.
+
+        combine = OpCall(moe_unpermute, rows, row_of, topk_w)
+        y = combine()
+    """
+
+    def __init__(self, op, *args, stream=None, **kw):
+        if op not in _PLANNERS:
+            raise ValueError(f"{getattr(op, '__name__', op)!r} has no prepared form")
+        self._plan = _PLANNERS[op](*args, stream=stream, **kw)
+        self._stream = stream
+
+    def __call__(self):
+        return self._plan.launch(self._stream)
+
+
+def _on_gpu(stream, *ts):
+    """The one device of the given tensors, which has to be the current one
+    (and the stream's)."""
+    _dev(*ts)
+    device = next(t.device for t in ts if t is not None)
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, which is not the current device")
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream on {stream.device}, tensors on {device}")
+    return device
+
+
+def _empty(shape, dtype, device, stream):
+    """An output or workspace of a call on `stream`: from that stream's memory,
+    and kept from reuse while the current stream may still read it."""
+    current = torch.cuda.current_stream(device)
+    if stream is None or stream == current:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
+def _require_rows(t, name: str, dtype, shape) -> int:
+    """A matrix with contiguous rows, any distance apart: its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    rows, cols = shape
+    if rows <= 1:
+        ld = cols
+    else:
+        ld = t.stride(0)
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+    return ld
+
+
+def _extent(t):
+    """Address range of a tensor with nonnegative strides."""
+    if t.numel() == 0:
+        return 0, 0
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    start = t.data_ptr()
+    return start, start + (last + 1) * t.element_size()
+
+
+def _disjoint(outputs: dict, inputs: dict):
+    """No output shares memory with an input or another output."""
+    ranges = [(n, _extent(t)) for n, t in inputs.items() if t is not None]
+    for name, t in outputs.items():
+        lo, hi = _extent(t)
+        for other, (a, b) in ranges:
+            if lo < b and a < hi:
+                raise ValueError(f"{name} overlaps {other}")
+        ranges.append((name, (lo, hi)))
+
+
+# ------------------------------------------------------------- dispatch --
+
+def _row_dtype(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a tensor")
+    if t.dtype not in SRC_DTYPES:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected bfloat16 or float32")
+    if t.dim() != 2 or t.shape[1] == 0:
+        raise ValueError(f"{name}: expected a matrix with at least one column")
+    return t.dtype
+
+
+def _tokens_slots(row_of):
+    if not isinstance(row_of, torch.Tensor) or row_of.dim() != 2 or row_of.shape[1] == 0:
+        raise ValueError("row_of: expected [T, k] with k >= 1")
+    _require(row_of, "row_of", torch.int32, row_of.shape)
+    return row_of.shape
+
+
+def _plan_permute(x, sorted_assign, expert_offsets, k, local_offset=0, local_count=0, rows=None, row_of=None,
+                  stream=None):
+    dtype = _row_dtype(x, "x")
+    T, H = x.shape
+    x_ld = _require_rows(x, "x", dtype, (T, H))
+    if not isinstance(expert_offsets, torch.Tensor) or expert_offsets.dim() != 1 or expert_offsets.numel() < 2:
+        raise ValueError("expert_offsets: expected [E + 1]")
+    E = expert_offsets.numel() - 1
+    if not 1 <= k <= E:
+        raise ValueError(f"k = {k} outside [1, E = {E}]")
+    if local_offset < 0 or local_count < 0 or local_offset + (local_count or E) > E:
+        raise ValueError(f"local experts {local_offset} + {local_count or E} outside [0, E = {E}]")
+    _require(expert_offsets, "expert_offsets", torch.int32, (E + 1,))
+    _require(sorted_assign, "sorted_assign", torch.int32, (T * k,))
+    device = _on_gpu(stream, x, sorted_assign, expert_offsets, rows, row_of)
+    if rows is None:
+        rows = _empty((T * min(k, local_count or E), H), dtype, device, stream)
+    if row_of is None:
+        row_of = _empty((T, k), torch.int32, device, stream)
+    rows_ld = _require_rows(rows, "rows", dtype, (rows.shape[0], H))
+    _require(row_of, "row_of", torch.int32, (T, k))
+    _disjoint({"rows": rows, "row_of": row_of},
+              {"x": x, "sorted_assign": sorted_assign, "expert_offsets": expert_offsets})
+    return _Plan("moe_permute", (x.data_ptr(), SRC_DTYPES[dtype], x_ld, T, H, E, k, expert_offsets.data_ptr(),
+                                 sorted_assign.data_ptr(), local_offset, local_count, rows.data_ptr(), rows_ld,
+                                 rows.shape[0], row_of.data_ptr()),
+                 (rows, row_of), device, (x, sorted_assign, expert_offsets))
+
+
+@_operator(_plan_permute)
+def moe_permute(x: torch.Tensor, sorted_assign: torch.Tensor, expert_offsets: torch.Tensor, k: int,
+                local_offset: int = 0, local_count: int = 0, rows: torch.Tensor | None = None,
+                row_of: torch.Tensor | None = None, stream=None):
+    """Rows of x [T, H] (bf16 or fp32) sorted by expert -> (rows, row_of).
+
+    sorted_assign [T*k] and expert_offsets [E+1] come from moe_route.  rows
+    [>= T*min(k, local experts), H] holds the rows of the local experts
+    [local_offset, + local_count) (0: all), the first of them at row 0; what lies
+    behind the last local row is not written.  row_of [T, k] int32 is the row of
+    each assignment, -1 where its expert is not local."""
+    return _plan_permute(x, sorted_assign, expert_offsets, k, local_offset, local_count, rows, row_of,
+                         stream).launch(stream)
+
+
+def _plan_permute_backward(drows, row_of, dx=None, stream=None):
+    dtype = _row_dtype(drows, "drows")
+    (R, H), (T, k) = drows.shape, _tokens_slots(row_of)
+    ld = _require_rows(drows, "drows", dtype, (R, H))
+    device = _on_gpu(stream, drows, row_of, dx)
+    if dx is None:
+        dx = _empty((T, H), dtype, device, stream)
+    dx_ld = _require_rows(dx, "dx", dtype, (T, H))
+    _disjoint({"dx": dx}, {"drows": drows, "row_of": row_of})
+    return _Plan("moe_permute_backward", (drows.data_ptr(), SRC_DTYPES[dtype], ld, R, row_of.data_ptr(), T, H, k,
+                                          dx.data_ptr(), dx_ld), dx, device, (drows, row_of))
+
+
+@_operator(_plan_permute_backward)
+def moe_permute_backward(drows: torch.Tensor, row_of: torch.Tensor, dx: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """Gradient of moe_permute: dx [T, H], each token the sum (fp32, slot
+    order) of its rows' gradients in drows [R, H]."""
+    return _plan_permute_backward(drows, row_of, dx, stream).launch(stream)
+
+
+def _plan_unpermute(rows, row_of, topk_w, residual=None, y=None, stream=None):
+    dtype = _row_dtype(rows, "rows")
+    (R, H), (T, k) = rows.shape, _tokens_slots(row_of)
+    ld = _require_rows(rows, "rows", dtype, (R, H))
+    _require(topk_w, "topk_w", torch.float32, (T, k))
+    res_ld = 0 if residual is None else _require_rows(residual, "residual", dtype, (T, H))
+    device = _on_gpu(stream, rows, row_of, topk_w, residual, y)
+    if y is None:
+        y = _empty((T, H), dtype, device, stream)
+    y_ld = _require_rows(y, "y", dtype, (T, H))
+    in_place = residual is not None and residual.data_ptr() == y.data_ptr() and res_ld == y_ld
+    _disjoint({"y": y}, {"rows": rows, "row_of": row_of, "topk_w": topk_w,
+                         "residual": None if in_place else residual})
+    return _Plan("moe_unpermute", (rows.data_ptr(), SRC_DTYPES[dtype], ld, R, row_of.data_ptr(), topk_w.data_ptr(),
+                                   T, H, k, None if residual is None else residual.data_ptr(), res_ld, y.data_ptr(),
+                                   y_ld), y, device, (rows, row_of, topk_w, residual))
+
+
+@_operator(_plan_unpermute)
+def moe_unpermute(rows: torch.Tensor, row_of: torch.Tensor, topk_w: torch.Tensor,
+                  residual: torch.Tensor | None = None, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y [T, H] = residual + sum over slots of topk_w [T, k] * the slot's row of
+    rows [R, H] (row_of [T, k] from moe_permute; absent rows are not read), in
+    fp32 and rounded once.  y may be residual itself."""
+    return _plan_unpermute(rows, row_of, topk_w, residual, y, stream).launch(stream)
+
+
+def _plan_unpermute_backward(dy, rows, row_of, topk_w, drows=None, dw=None, stream=None):
+    dtype = _row_dtype(rows, "rows")
+    (R, H), (T, k) = rows.shape, _tokens_slots(row_of)
+    ld = _require_rows(rows, "rows", dtype, (R, H))
+    dy_ld = _require_rows(dy, "dy", dtype, (T, H))
+    _require(topk_w, "topk_w", torch.float32, (T, k))
+    device = _on_gpu(stream, dy, rows, row_of, topk_w, drows, dw)
+    if drows is None:
+        drows = _empty((R, H), dtype, device, stream)
+    if dw is None:
+        dw = _empty((T, k), torch.float32, device, stream)
+    drows_ld = _require_rows(drows, "drows", dtype, (R, H))
+    _require(dw, "dw", torch.float32, (T, k))
+    _disjoint({"drows": drows, "dw": dw}, {"dy": dy, "rows": rows, "row_of": row_of, "topk_w": topk_w})
+    return _Plan("moe_unpermute_backward", (dy.data_ptr(), SRC_DTYPES[dtype], dy_ld, rows.data_ptr(), ld, R,
+                                            row_of.data_ptr(), topk_w.data_ptr(), T, H, k, drows.data_ptr(),
+                                            drows_ld, dw.data_ptr()),
+                 (drows, dw), device, (dy, rows, row_of, topk_w))
+
+
+@_operator(_plan_unpermute_backward)
+def moe_unpermute_backward(dy: torch.Tensor, rows: torch.Tensor, row_of: torch.Tensor, topk_w: torch.Tensor,
+                           drows: torch.Tensor | None = None, dw: torch.Tensor | None = None, stream=None):
+    """Gradients of moe_unpermute -> (drows [R, H], dw [T, k] fp32): drows holds
+    topk_w * dy in the rows that row_of names and leaves the others unwritten;
+    dw is the dot product of dy and the row, 0 for an absent one.  The gradient
+    of residual is dy."""
+    return _plan_unpermute_backward(dy, rows, row_of, topk_w, drows, dw, stream).launch(stream)
+
+
+def _plan_route_backward(topk_ids, topk_w, dw, num_experts, dlogits=None, stream=None):
+    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2 or topk_ids.shape[1] == 0:
+        raise ValueError("topk_ids: expected [T, k] with k >= 1")
+    T, k = topk_ids.shape
+    _require(topk_ids, "topk_ids", torch.int32, (T, k))
+    _require(topk_w, "topk_w", torch.float32, (T, k))
+    _require(dw, "dw", torch.float32, (T, k))
+    if k > num_experts:
+        raise ValueError(f"k = {k} outside [1, E = {num_experts}]")
+    device = _on_gpu(stream, topk_ids, topk_w, dw, dlogits)
+    if dlogits is None:
+        dlogits = _empty((T, num_experts), torch.float32, device, stream)
+    _require(dlogits, "dlogits", torch.float32, (T, num_experts))
+    _disjoint({"dlogits": dlogits}, {"topk_ids": topk_ids, "topk_w": topk_w, "dw": dw})
+    return _Plan("moe_route_backward", (topk_ids.data_ptr(), topk_w.data_ptr(), dw.data_ptr(), T, num_experts, k,
+                                        dlogits.data_ptr()), dlogits, device, (topk_ids, topk_w, dw))
+
+
+@_operator(_plan_route_backward)
+def moe_route_backward(topk_ids: torch.Tensor, topk_w: torch.Tensor, dw: torch.Tensor, num_experts: int,
+                       dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_route's weights: dlogits [T, num_experts] fp32 from dw
+    [T, k], zero for the experts a token did not choose."""
+    return _plan_route_backward(topk_ids, topk_w, dw, num_experts, dlogits, stream).launch(stream)
 
 
 # ---------------------------------------------------------------- gemm ---

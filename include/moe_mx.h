@@ -138,6 +138,62 @@ moe_status_t moe_route(const float* logits, int32_t T, int32_t E, int32_t k, int
                        void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Dispatch: the layer's steps 2 and 7 as operators of their own, with their
+ * gradients, for callers that put something of theirs between routing and the
+ * combine (experts in trainable precision, adapters, an exchange between
+ * expert shards).  `dtype` is the type of every row matrix of a call (bf16 or
+ * fp32); each matrix has contiguous rows of H elements, `*_ld` elements apart
+ * (>= H), and lies at an address that is a multiple of its element size.
+ * Outputs must not overlap inputs, but y may be residual itself.
+ * Requires 0 <= T (0: no-op), 1 <= H <= 2^24, 1 <= k, T*k <= 2^30.
+ * Sums are held in fp32 in slot order j = 0..k-1 and each output is rounded
+ * once (RNE); nothing depends on scheduling, so results repeat bit for bit.
+ *
+ * moe_permute -- rows sorted by expert: rows[row_of[t, j]] = x[t].
+ *   expert_offsets, sorted_assign  [E+1], [T*k] as moe_route writes them.  The
+ *            rows of the local experts [local_expert_offset, + local_num_experts)
+ *            (0 means all E) are entries expert_offsets[first] and following of
+ *            sorted_assign, in that order from row 0: rows of local expert i are
+ *            [o[i] - o[0], o[i+1] - o[0]) with o = expert_offsets + first.
+ *   rows     [num_rows, H] out; rows behind the last local one are left as they
+ *            were.  T * min(k, local experts) rows always suffice; with fewer,
+ *            assignments past the last row are dropped.
+ *   row_of   [T, k] int32 out: the row of each assignment, or -1 if its expert is
+ *            not local or it was dropped.
+ * moe_permute_backward -- dx[t] = sum over j with row_of[t, j] >= 0 of
+ *   drows[row_of[t, j]]; zeros for a token without a row.
+ * moe_unpermute -- y[t] = residual[t] + sum over j with row_of[t, j] >= 0 of
+ *   topk_w[t, j] * rows[row_of[t, j]]  (residual NULL: 0).  Weights and rows of
+ *   absent assignments are not read.
+ * moe_unpermute_backward -- drows[row_of[t, j]] = topk_w[t, j] * dy[t] (rows that
+ *   no assignment has are left as they were) and dw[t, j] = sum over columns of
+ *   dy[t] * rows[row_of[t, j]] in fp32 (0 for an absent assignment).  The
+ *   gradient of residual is dy itself.
+ *   In these three, entries of row_of outside [0, num_rows) count as absent; no
+ *   row may be named twice in moe_unpermute_backward (moe_permute never does).
+ * moe_route_backward -- gradient of moe_route's weights: with w the softmax of
+ *   the chosen logits, dlogits[t, ids[t, j]] = w[t,j] * (dw[t,j] - sum_i w[t,i]
+ *   dw[t,i]) and 0 elsewhere; dlogits [T, E] fp32.  Ids outside [0, E) get no
+ *   entry; requires 1 <= k <= E <= 1024.
+ */
+moe_status_t moe_permute(const void* x, moe_src_t dtype, int64_t x_ld, int32_t T, int32_t H, int32_t E, int32_t k,
+                         const int32_t* expert_offsets, const int32_t* sorted_assign, int32_t local_expert_offset,
+                         int32_t local_num_experts, void* rows, int64_t rows_ld, int32_t num_rows, int32_t* row_of,
+                         hipStream_t stream);
+moe_status_t moe_permute_backward(const void* drows, moe_src_t dtype, int64_t drows_ld, int32_t num_rows,
+                                  const int32_t* row_of, int32_t T, int32_t H, int32_t k, void* dx, int64_t dx_ld,
+                                  hipStream_t stream);
+moe_status_t moe_unpermute(const void* rows, moe_src_t dtype, int64_t rows_ld, int32_t num_rows,
+                           const int32_t* row_of, const float* topk_w, int32_t T, int32_t H, int32_t k,
+                           const void* residual, int64_t residual_ld, void* y, int64_t y_ld, hipStream_t stream);
+moe_status_t moe_unpermute_backward(const void* dy, moe_src_t dtype, int64_t dy_ld, const void* rows,
+                                    int64_t rows_ld, int32_t num_rows, const int32_t* row_of, const float* topk_w,
+                                    int32_t T, int32_t H, int32_t k, void* drows, int64_t drows_ld, float* dw,
+                                    hipStream_t stream);
+moe_status_t moe_route_backward(const int32_t* topk_ids, const float* topk_w, const float* dw, int32_t T, int32_t E,
+                                int32_t k, float* dlogits, hipStream_t stream);
+
+/*
  * mx_gemm -- dense MX GEMM with bf16 output (mxfp6-sm120 page, table of
  * paths, "Dense" row; "Execution model" figure: bf16 activations quantized
  * on the device to E4M3 with one UE8M0 scale per 32 K values, packed MX

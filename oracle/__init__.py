@@ -16,6 +16,8 @@ rather than to be fast:
 * ``oracle.moe``     -- the layer forward: activation quantization, FC1,
                         SiLU(gate)*up with its rounding/requantization point,
                         FC2, routing-weighted combine and the shared expert.
+* ``oracle.dispatch`` -- rows sorted by expert and back, with their gradients,
+                        and the gradient of the routing weights.
 
 Pins (tests/test_oracle_*.py) tie each function to something other than
 itself: hand-listed decode values, torch's own float8 codecs, brute-force
