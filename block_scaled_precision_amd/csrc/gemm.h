@@ -7,6 +7,15 @@
 
 namespace moe_mx {
 
+// Epilogue operands of mx_linear (epilogue.h); null: absent
+struct Epilogue {
+  const void* bias;          // [groups, N] fp32, or bf16 with bias_bf16
+  int bias_bf16;
+  int fn;                    // mx_fn_t
+  const uint16_t* mul;       // [M, N] bf16
+  const uint16_t* residual;  // [M, N] bf16
+};
+
 struct FcArgs {
   // M-tiles: routed mode reads `tiles[0 .. *num_tiles)`, grid sized for max_tiles;
   // dense mode (dense_rows > 0) covers rows [0, dense_rows) of a single expert.
@@ -62,6 +71,10 @@ struct FcArgs {
   float* sorted_w_out;
   Tile* tiles_out;
   int32_t* ntiles_out;
+  // mx_linear on the FC2 kernels: rows of A and of the output are permuted rows
+  // (no sorted_assign, no row weights), finished by the epilogue
+  bool linear;
+  Epilogue epi;
 };
 
 // Columns of N covered by one wave of the stream kernels.

@@ -25,6 +25,7 @@
 // MXFP4 weight; mxfp6-sm120 page: block-scaled MMA with FP32 accumulation).
 #include <hip/hip_runtime.h>
 
+#include "epilogue.h"
 #include "gemm.h"
 #include "mx_device.h"
 
@@ -249,8 +250,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
 }
 
 // FC2: obuf[a(p), n] = w(p) * (A W2^T)[p, n] for the wave's 64 columns n;
-// rows of A are rows of h in permuted order.
-template <bool MXA, int WF>
+// rows of A are rows of h in permuted order.  EPI (mx_linear): row p itself,
+// finished by the epilogue.
+template <bool MXA, int WF, bool EPI>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_fc2_stream(FcArgs p) {
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int gw = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -285,6 +287,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   for (int n = 0; n < NB; ++n) acc[n] = (v4f){0.f, 0.f, 0.f, 0.f};
   mainloop<MXA, WF>(acc, arow, asrow, brow, bsrow, K / 128, g);
 
+  if constexpr (EPI) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int col = col0 + 16 * n + r;
+      if (col >= H) continue;
+      const float bias = epi_bias(p, t.expert, col);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * g + i < t.rows) epi_store(p, (int64_t)(t.p0 + 4 * g + i) * H + col, acc[n][i] + bias);
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = 4 * g + i;
@@ -314,7 +328,8 @@ static hipError_t launch_pair(const FcArgs& p, bool fc1, hipStream_t st) {
   if (waves == 0) return hipSuccess;
   const int64_t blocks = (waves + 3) / 4;
   if (fc1) k_fc1_stream<MXA, WF><<<blocks, 256, 0, st>>>(p);
-  else k_fc2_stream<MXA, WF><<<blocks, 256, 0, st>>>(p);
+  else if (p.linear) k_fc2_stream<MXA, WF, true><<<blocks, 256, 0, st>>>(p);
+  else k_fc2_stream<MXA, WF, false><<<blocks, 256, 0, st>>>(p);
   return hipGetLastError();
 }
 

@@ -54,4 +54,10 @@ hipError_t launch_route_permute_small(const float* logits, int T, int E, int k, 
                                       int L, int32_t* offsets, int32_t* sorted_assign, float* sorted_w, Tile* tiles,
                                       int32_t* num_tiles, int bm, hipStream_t stream);
 
+// GEMM tile list of mx_linear: groups of rows [offsets[g] - offsets[0],
+// offsets[g+1] - offsets[0]), clamped to [0, M), in M-tiles of `bm` rows (empty
+// groups have none).
+hipError_t launch_group_tiles(const int32_t* offsets, int groups, int64_t M, int bm, Tile* tiles,
+                              int32_t* num_tiles, hipStream_t stream);
+
 }  // namespace moe_mx

@@ -571,6 +571,123 @@ extern "C" moe_status_t mx_gemm(const void* a, const uint8_t* a_scale, int64_t M
   return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
+// ------------------------------------------------------------- mx_linear --
+
+// Kernel, tile height and workspace layout of one mx_linear call.
+struct LinearPlan {
+  Fc kind;
+  int rows;        // M-tile height
+  int max_tiles;   // grouped: room of the tile list
+  size_t quant, tiles, ntiles, total;
+};
+
+static bool linear_sizes_ok(const mx_linear_problem_t& p) {
+  return p.M >= 0 && p.N > 0 && p.K > 0 && p.K % 32 == 0 && p.groups >= 0 && p.groups <= kMaxExperts &&
+         p.w_stride >= 0 && p.w_scale_stride >= 0;
+}
+static bool linear_supported(const mx_linear_problem_t& p) {
+  // the bounds keep tile counts and per-workgroup step counts inside 32 bits
+  return p.w_fmt != MX_E4M3 && p.N % 8 == 0 && p.K % 128 == 0 && p.M <= (int64_t)1 << 30 && p.N <= (int64_t)1 << 30 &&
+         p.K <= (int64_t)1 << 30 && (double)p.M * p.N <= 68719476736.0 &&
+         (double)p.M * p.N * p.K <= 4503599627370496.0;
+}
+
+static LinearPlan linear_plan(const mx_linear_problem_t& p, bool has_a_scale) {
+  LinearPlan f = {};
+  f.kind = Fc::kStream;
+  f.rows = kStreamRows;
+  if (p.groups > 0) f.max_tiles = (int)(p.M / f.rows + (p.M < p.groups ? p.M : p.groups));
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = o;
+    o = align_up(o + bytes, 256);
+    return r;
+  };
+  if (p.act == MOE_ACT_MXFP8 && !has_a_scale) f.quant = take(gemm_quant_bytes(p.M, p.K));
+  if (p.groups > 0) {
+    f.tiles = take((size_t)f.max_tiles * sizeof(Tile));
+    f.ntiles = take(4);
+  }
+  f.total = o;
+  return f;
+}
+
+extern "C" size_t mx_linear_workspace_bytes(const mx_linear_problem_t* p, int has_a_scale) {
+  if (!p || !linear_sizes_ok(*p) || !linear_supported(*p) || p->M == 0) return 0;
+  return linear_plan(*p, has_a_scale != 0).total;
+}
+
+extern "C" moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_tensors_t* t, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream) {
+  if (!p || !t || !linear_sizes_ok(*p)) return MOE_ERR_INVALID_ARG;
+  if (p->act != MOE_ACT_BF16 && p->act != MOE_ACT_MXFP8) return MOE_ERR_INVALID_ARG;
+  if (p->w_fmt != MX_E2M1 && p->w_fmt != MX_E3M2 && p->w_fmt != MX_E4M3) return MOE_ERR_INVALID_ARG;
+  if (p->fn != MX_FN_NONE && p->fn != MX_FN_SILU && p->fn != MX_FN_GELU && p->fn != MX_FN_RELU2)
+    return MOE_ERR_INVALID_ARG;
+  if (p->bias_dtype != MOE_SRC_BF16 && p->bias_dtype != MOE_SRC_FP32) return MOE_ERR_INVALID_ARG;
+  const bool mx = p->act == MOE_ACT_MXFP8;
+  if (!mx && t->a_scale) return MOE_ERR_INVALID_ARG;
+  const int64_t M = p->M, N = p->N, K = p->K;
+  const int64_t wbytes = N * (K / 32) * wbits(p->w_fmt) * 4, sbytes = N * (K / 32);
+  const int64_t wstride = p->w_stride ? p->w_stride : wbytes, sstride = p->w_scale_stride ? p->w_scale_stride : sbytes;
+  if (!linear_supported(*p)) return MOE_ERR_UNSUPPORTED;
+  if (p->groups > 1 && (wstride < wbytes || sstride < sbytes || wstride % 16 || sstride % 16)) return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (!t->a || !t->w || !t->w_scale || !t->out || (p->groups > 0) != (t->expert_offsets != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  for (const void* q : {t->a, (const void*)t->a_scale, (const void*)t->w, (const void*)t->w_scale, t->mul, t->residual,
+                        (const void*)t->out})
+    if (!aligned16(q)) return MOE_ERR_INVALID_ARG;
+  if (t->bias && (uintptr_t)t->bias % (p->bias_dtype == MOE_SRC_BF16 ? 2 : 4)) return MOE_ERR_INVALID_ARG;
+  const LinearPlan f = linear_plan(*p, t->a_scale != nullptr);
+  const size_t need = f.total;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (need > 0 && ((uintptr_t)workspace & 255u) != 0) return MOE_ERR_INVALID_ARG;
+  moe_status_t st = check_arch();
+  if (st != MOE_OK) return st;
+
+  char* ws = (char*)workspace;
+  FcArgs g = {};
+  g.linear = true;
+  g.epi.bias = t->bias;
+  g.epi.bias_bf16 = p->bias_dtype == MOE_SRC_BF16;
+  g.epi.fn = p->fn;
+  g.epi.mul = (const uint16_t*)t->mul;
+  g.epi.residual = (const uint16_t*)t->residual;
+  g.k = 1;
+  g.a = t->a;
+  g.a_scale = t->a_scale;
+  if (mx && !t->a_scale) {
+    uint8_t* qc = (uint8_t*)ws + f.quant;
+    uint8_t* qs = qc + align_up((size_t)(M * K), 256);
+    if (launch_quantize(t->a, MOE_SRC_BF16, M, K, K, MX_E4M3, qc, qs, stream) != hipSuccess) return MOE_ERR_HIP;
+    g.a = qc;
+    g.a_scale = qs;
+  }
+  if (p->groups > 0) {
+    Tile* tiles = (Tile*)(ws + f.tiles);
+    int32_t* ntiles = (int32_t*)(ws + f.ntiles);
+    if (launch_group_tiles(t->expert_offsets, p->groups, M, f.rows, tiles, ntiles, stream) != hipSuccess)
+      return MOE_ERR_HIP;
+    g.tiles = tiles;
+    g.num_tiles = ntiles;
+    g.max_tiles = f.max_tiles;
+  } else {
+    g.dense_rows = (int)M;
+  }
+  g.w = t->w;
+  g.w_scale = t->w_scale;
+  g.w_estride = wstride;
+  g.ws_estride = sstride;
+  g.K = (int)K;
+  g.N = (int)N;
+  const int cols = fc_cols(f.kind, false, f.rows);
+  g.nchunks = (int)((N + cols - 1) / cols);
+  g.obuf = (uint16_t*)t->out;
+  const int wf = p->w_fmt == MX_E2M1 ? 1 : 2;
+  return launch_fc_stream(g, false, mx, wf, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
 extern "C" size_t moe_fused_workspace_offset(const moe_problem_t* p, moe_ws_part_t part) {
   const size_t none = ~(size_t)0;
   if (!p || p->T < 0 || p->E < 1 || p->k < 1 || p->k > p->E || p->H <= 0 || p->I <= 0 || p->I_shared < 0)

@@ -283,6 +283,57 @@ __global__ __launch_bounds__(1024) void k_permute_small(const float* __restrict_
   }
 }
 
+// One workgroup; thread g owns group g.  Offsets are clamped so that they
+// ascend within [0, M] whatever the buffer holds, which bounds the tiles by
+// M / bm + groups.
+__global__ __launch_bounds__(1024) void k_group_tiles(const int32_t* __restrict__ offsets, int groups, int M, int bm,
+                                                      Tile* __restrict__ tiles, int32_t* __restrict__ num_tiles) {
+  __shared__ int32_t s_end[kMaxExperts];
+  __shared__ int32_t s_wave[16];
+  const int g = threadIdx.x, lane = g & 63, wv = g >> 6;
+  // running maximum of the clamped ends, so that no group starts before an
+  // earlier one ends
+  int32_t end = 0;
+  if (g < groups) end = (int32_t)min(max((int64_t)offsets[g + 1] - offsets[0], (int64_t)0), (int64_t)M);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t v = __shfl_up(end, d);
+    if (lane >= d) end = max(end, v);
+  }
+  if (lane == 63) s_wave[wv] = end;
+  __syncthreads();
+  for (int i = 0; i < wv; ++i) end = max(end, s_wave[i]);
+  s_end[g] = end;
+  __syncthreads();
+  const int32_t start = g > 0 ? s_end[g - 1] : 0;
+  const int32_t count = g < groups ? end - start : 0;
+  const int32_t ntile = (count + bm - 1) / bm;
+  int32_t inc = ntile;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t v = __shfl_up(inc, d);
+    if (lane >= d) inc += v;
+  }
+  if (lane == 63) s_wave[wv] = inc;
+  __syncthreads();
+  for (int i = 0; i < wv; ++i) inc += s_wave[i];
+  for (int i = 0; i < ntile; ++i) {
+    Tile tl;
+    tl.expert = g;
+    tl.p0 = start + i * bm;
+    tl.rows = min(bm, count - i * bm);
+    tl.pad = 0;
+    tiles[inc - ntile + i] = tl;
+  }
+  if (g == 1023) *num_tiles = inc;
+}
+
+hipError_t launch_group_tiles(const int32_t* offsets, int groups, int64_t M, int bm, Tile* tiles,
+                              int32_t* num_tiles, hipStream_t stream) {
+  k_group_tiles<<<1, 1024, 0, stream>>>(offsets, groups, (int)M, bm, tiles, num_tiles);
+  return hipGetLastError();
+}
+
 hipError_t launch_route_permute_small(const float* logits, int T, int E, int k, int32_t* ids, float* w, int off,
                                       int L, int32_t* offsets, int32_t* sorted_assign, float* sorted_w, Tile* tiles,
                                       int32_t* num_tiles, int bm, hipStream_t stream) {

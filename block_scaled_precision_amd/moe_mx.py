@@ -20,11 +20,13 @@ MX_FORMATS = {"e2m1": 1, "e3m2": 2, "e4m3": 3}
 FORMAT_BITS = {"e2m1": 4, "e3m2": 6, "e4m3": 8}
 SRC_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 ACTS = {"bf16": 0, "mxfp8": 1}
+LINEAR_FNS = {"none": 0, "silu": 1, "gelu": 2, "relu2": 3}
 ACT_FNS = {"silu": 0, "relu2": 1, "swiglu_oai": 2}
 
 # Every symbol include/moe_mx.h declares.
 EXPORTS = ("mx_quantize", "moe_route_workspace_bytes", "moe_route", "moe_permute", "moe_permute_backward",
            "moe_unpermute", "moe_unpermute_backward", "moe_route_backward", "mx_gemm_workspace_bytes", "mx_gemm",
+           "mx_linear_workspace_bytes", "mx_linear",
            "moe_fused_workspace_bytes", "moe_fused", "moe_fused_workspace_offset", "moe_fused_noalloc",
            "moe_status_str", "moe_mx_version")
 NOALLOC_SCRATCH_BYTES = 32 << 20  # MOE_NOALLOC_SCRATCH_BYTES
@@ -42,6 +44,17 @@ class MoeProblem(ctypes.Structure):
                 ("act", ctypes.c_int), ("I_shared", ctypes.c_int32), ("shared_weight", ctypes.c_float),
                 ("local_expert_offset", ctypes.c_int32), ("local_num_experts", ctypes.c_int32),
                 ("act_fn", ctypes.c_int), ("flags", ctypes.c_uint32)]
+
+
+class MxLinearProblem(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("groups", ctypes.c_int32),
+                ("act", ctypes.c_int), ("w_fmt", ctypes.c_int), ("fn", ctypes.c_int), ("bias_dtype", ctypes.c_int),
+                ("w_stride", ctypes.c_int64), ("w_scale_stride", ctypes.c_int64)]
+
+
+class MxLinearTensors(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "a", "a_scale", "w", "w_scale", "bias", "mul", "residual", "expert_offsets", "out")]
 
 
 MOE_NUM_STAGES = 7
@@ -91,6 +104,10 @@ def lib() -> ctypes.CDLL:
         L.moe_unpermute_backward.restype = i
         L.moe_route_backward.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp]
         L.moe_route_backward.restype = i
+        L.mx_linear_workspace_bytes.argtypes = [ctypes.POINTER(MxLinearProblem), i]
+        L.mx_linear_workspace_bytes.restype = sz
+        L.mx_linear.argtypes = [ctypes.POINTER(MxLinearProblem), ctypes.POINTER(MxLinearTensors), vp, sz, vp]
+        L.mx_linear.restype = i
         L.moe_fused_noalloc.argtypes = [ctypes.POINTER(MoeProblem), ctypes.POINTER(MoeTensors), vp]
         L.moe_fused_noalloc.restype = ctypes.c_int
         L.moe_fused_workspace_offset.argtypes = [ctypes.POINTER(MoeProblem), ctypes.c_int]
@@ -261,7 +278,7 @@ def _operator(planner):
 
 class OpCall:
     """One operator call (moe_permute, moe_unpermute, their gradients,
-    moe_route_backward) with its arguments checked and marshalled and its
+    moe_route_backward, mx_linear) with its arguments checked and marshalled and its
     outputs allocated once, for loops that call it many times on the same
     buffers (their contents may change between calls): each call then costs the
     host only the C call.  The stream is the current one at each call unless
@@ -555,6 +572,110 @@ def mx_gemm(a: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, fmt: str, a
                          alpha, _ptr(c), _ptr(workspace), 0 if workspace is None else workspace.numel(),
                          _stream(stream)), "mx_gemm")
     return c
+
+
+# --------------------------------------------------------------- linear --
+
+def _group_stride(t, name, shape, groups):
+    """Bytes between the groups' matrices of t, each of them contiguous."""
+    full = (groups, *shape) if groups else shape
+    if groups == 0:
+        _require(t, name, torch.uint8, full)
+        return 0
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a tensor")
+    if t.dtype != torch.uint8:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {torch.uint8}")
+    if tuple(t.shape) != full:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {full}")
+    if not t[0].is_contiguous():
+        raise ValueError(f"{name}: each group's matrix must be contiguous")
+    if groups > 1 and (t.stride(0) < t[0].numel() or t.stride(0) % 16):
+        raise ValueError(f"{name}: groups must not overlap and lie a multiple of 16 bytes apart")
+    return t.stride(0) if groups > 1 else 0
+
+
+def _plan_linear(a, w, w_scale, fmt, act="mxfp8", a_scale=None, bias=None, fn="none", mul=None, residual=None,
+                 expert_offsets=None, out=None, workspace=None, stream=None):
+    if fmt not in ("e2m1", "e3m2"):
+        raise ValueError(f"weight format {fmt!r} is not e2m1 or e3m2")
+    if act not in ACTS:
+        raise ValueError(f"unknown activation precision {act!r}")
+    if fn not in LINEAR_FNS:
+        raise ValueError(f"unknown activation function {fn!r}")
+    grouped = expert_offsets is not None
+    if not isinstance(a, torch.Tensor) or a.dim() != 2:
+        raise ValueError("a: expected [M, K]")
+    if not isinstance(w, torch.Tensor) or w.dim() != (3 if grouped else 2):
+        raise ValueError("w: expected [groups, N, K*b/8] with expert_offsets, [N, K*b/8] without")
+    M, K = a.shape
+    N, G = w.shape[-2], w.shape[0] if grouped else 0
+    if N == 0 or N % 8 or K == 0 or K % 128:
+        raise ValueError(f"N = {N} must be a positive multiple of 8, K = {K} of 128")
+    if grouped and not 1 <= G <= 1024:
+        raise ValueError(f"{G} groups outside [1, 1024]")
+    if a_scale is None:
+        _require(a, "a", torch.bfloat16, (M, K))
+    else:
+        if act != "mxfp8":
+            raise ValueError("a_scale goes with act='mxfp8'")
+        _require(a, "a", torch.uint8, (M, K))
+        _require(a_scale, "a_scale", torch.uint8, (M, K // 32))
+    w_stride = _group_stride(w, "w", (N, K * FORMAT_BITS[fmt] // 8), G)
+    s_stride = _group_stride(w_scale, "w_scale", (N, K // 32), G)
+    if grouped:
+        _require(expert_offsets, "expert_offsets", torch.int32, (G + 1,))
+    if bias is not None:
+        if not isinstance(bias, torch.Tensor) or bias.dtype not in SRC_DTYPES:
+            raise ValueError("bias: expected a bfloat16 or float32 tensor")
+        _require(bias, "bias", bias.dtype, (G, N) if grouped else (N,))
+    for name, t in (("mul", mul), ("residual", residual)):
+        if t is not None:
+            _require(t, name, torch.bfloat16, (M, N))
+    device = _on_gpu(stream, a, a_scale, w, w_scale, bias, mul, residual, expert_offsets, out, workspace)
+    if out is None:
+        out = _empty((M, N), torch.bfloat16, device, stream)
+    _require(out, "out", torch.bfloat16, (M, N))
+    problem = MxLinearProblem(M, N, K, G, ACTS[act], MX_FORMATS[fmt], LINEAR_FNS[fn],
+                              0 if bias is None else SRC_DTYPES[bias.dtype], w_stride, s_stride)
+    need = lib().mx_linear_workspace_bytes(ctypes.byref(problem), a_scale is not None)
+    if workspace is None and need:
+        workspace = _empty((need,), torch.uint8, device, stream)
+    if workspace is not None:
+        _require_workspace(workspace, need)
+    same = [t for t in (mul, residual) if t is not None and t.data_ptr() == out.data_ptr()]
+    _disjoint({"out": out, **({} if workspace is None else {"workspace": workspace})},
+              {"a": a, "a_scale": a_scale, "w": w, "w_scale": w_scale, "bias": bias, "expert_offsets": expert_offsets,
+               "mul": None if any(t is mul for t in same) else mul,
+               "residual": None if any(t is residual for t in same) else residual})
+    if workspace is not None:
+        _disjoint({"workspace": workspace}, {"mul": mul, "residual": residual})
+    tensors = MxLinearTensors(*(None if t is None else t.data_ptr() for t in (
+        a, a_scale, w, w_scale, bias, mul, residual, expert_offsets, out)))
+    return _Plan("mx_linear", (ctypes.byref(problem), ctypes.byref(tensors),
+                               None if workspace is None else workspace.data_ptr(),
+                               0 if workspace is None else workspace.numel()),
+                 out, device, (a, a_scale, w, w_scale, bias, mul, residual, expert_offsets, workspace))
+
+
+@_operator(_plan_linear)
+def mx_linear(a: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, fmt: str, act: str = "mxfp8",
+              a_scale: torch.Tensor | None = None, bias: torch.Tensor | None = None, fn: str = "none",
+              mul: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+              expert_offsets: torch.Tensor | None = None, out: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out [M, N] bf16 = fn(A W^T + bias) * mul + residual, in fp32 and rounded once.
+
+    a: [M, K] bf16 (act "bf16", or "mxfp8" quantized on the device), or E4M3
+    codes [M, K] uint8 with a_scale [M, K/32].  w [N, K*b/8] + w_scale [N, K/32]
+    packed MX weights; bias [N] bf16 or fp32; mul, residual [M, N] bf16 (out may
+    be either); fn "none", "silu", "gelu" or "relu2".  With expert_offsets [G+1]
+    int32 the rows of a are sorted by group (moe_permute) and w, w_scale and bias
+    have a leading axis of G, one matrix per group; rows behind the last group
+    are not written.  A shard of the experts passes its slice of moe_route's
+    offsets."""
+    return _plan_linear(a, w, w_scale, fmt, act, a_scale, bias, fn, mul, residual, expert_offsets, out, workspace,
+                        stream).launch(stream)
 
 
 # ---------------------------------------------------------------- fused --

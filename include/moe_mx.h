@@ -229,6 +229,71 @@ moe_status_t mx_gemm(const void* a, const uint8_t* a_scale, int64_t M, int64_t N
                      const uint8_t* w, const uint8_t* w_scale, mx_elem_t w_fmt, float alpha, void* c,
                      void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * mx_linear -- matrix product with packed MX weights and a fused epilogue, for
+ * one weight matrix or for one per group of rows (experts):
+ *
+ *   v[m, n]   = sum_k A'[m, k] * W'[g, n, k] + bias[g, n]     (fp32 accumulation)
+ *   out[m, n] = bf16_RNE(fn(v[m, n]) * mul[m, n] + residual[m, n])
+ *
+ * with g the group of row m (one group: 0), the epilogue in fp32 and one rounding.
+ * A' and W' are as in mx_gemm: bf16 A as given, or its MXFP8 values (quantized
+ * on the device as mx_quantize does, or given as codes and scales); MX_E2M1 or
+ * MX_E3M2 weights.  mul serves gated activations: with up = mx_linear(...) of
+ * the up half, mx_linear of the gate half with fn = MX_FN_SILU and mul = up is
+ * SiLU(gate) * up.
+ *
+ * fn: MX_FN_NONE v; MX_FN_SILU v / (1 + exp(-v)); MX_FN_GELU v * Phi(v) with the
+ * normal distribution function Phi (the erf form); MX_FN_RELU2 max(v, 0)^2.
+ *
+ * Groups: with groups = 0 every row uses w [N, K*b/8].  With groups = G >= 1,
+ * w is [G, N, K*b/8] and row m belongs to the group g with offsets[g] -
+ * offsets[0] <= m < offsets[g+1] - offsets[0], offsets = expert_offsets [G+1] on
+ * the device, ascending: rows sorted by moe_permute with the offsets of
+ * moe_route, or a slice of them for an expert shard.  M is the number of rows
+ * of a and out; rows from offsets[G] - offsets[0] on are neither read nor
+ * written (with MXFP8 from bf16 they are read: any values, NaN included).
+ * Offsets beyond M or out of order give unspecified rows, never an access out
+ * of bounds.
+ */
+typedef enum { MX_FN_NONE = 0, MX_FN_SILU = 1, MX_FN_GELU = 2, MX_FN_RELU2 = 3 } mx_fn_t;
+
+typedef struct {
+  int64_t M, N, K;        /* rows, output columns (% 8 == 0), contraction (% 128 == 0) */
+  int32_t groups;         /* 0: one weight matrix; else matrices w holds (<= 1024)      */
+  moe_act_t act;          /* MOE_ACT_BF16 or MOE_ACT_MXFP8                              */
+  mx_elem_t w_fmt;        /* MX_E2M1 or MX_E3M2                                         */
+  mx_fn_t fn;
+  moe_src_t bias_dtype;   /* type of bias, where there is one                           */
+  int64_t w_stride;       /* bytes between the groups' matrices in w (% 16 == 0;        */
+  int64_t w_scale_stride; /* and in w_scale); 0: one right behind the other             */
+} mx_linear_problem_t;
+
+typedef struct {
+  const void* a;                 /* [M, K] bf16, or E4M3 codes with a_scale             */
+  const uint8_t* a_scale;        /* [M, K/32] with MOE_ACT_MXFP8, or NULL: quantize a   */
+  const uint8_t* w;              /* [groups or 1, N, K*b/8]                             */
+  const uint8_t* w_scale;        /* [groups or 1, N, K/32]                              */
+  const void* bias;              /* [groups or 1, N] of bias_dtype, or NULL             */
+  const void* mul;               /* [M, N] bf16, or NULL                                */
+  const void* residual;          /* [M, N] bf16, or NULL                                */
+  const int32_t* expert_offsets; /* [groups + 1] (groups > 0 only)                      */
+  void* out;                     /* [M, N] bf16; may be mul or residual itself          */
+} mx_linear_tensors_t;
+
+/* Workspace of mx_linear: mx_linear_workspace_bytes(p, has_a_scale) bytes,
+ * 256-byte aligned, contents need not be set; 0 for a problem that needs none or
+ * is invalid.  It holds the tile list of grouped calls, the partial sums of
+ * split ones and, unless a_scale is given, the quantized A of MXFP8 from bf16, so
+ * calls that may run at the same time need one each.
+ * Requires M >= 0 (0: no-op), M <= 2^30, M*N <= 2^36, M*N*K <= 2^52 and 16-byte
+ * aligned a, a_scale, w, w_scale, mul, residual and out (bias: its element size); N % 8
+ * != 0, K % 128 != 0, larger sizes or E4M3 weights give MOE_ERR_UNSUPPORTED.
+ * Deterministic: the summation order depends on the problem alone. */
+size_t mx_linear_workspace_bytes(const mx_linear_problem_t* p, int has_a_scale);
+moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_tensors_t* t, void* workspace,
+                       size_t workspace_bytes, hipStream_t stream);
+
 /* Problem description of one fused MoE layer call. */
 typedef struct {
   int32_t T;                   /* tokens (>= 0)                                      */

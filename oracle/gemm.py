@@ -22,8 +22,13 @@ given already quantized (E4M3 codes + E8M0 scales).  The result is float64;
 the device returns one bf16 rounding (round half to even) of its fp32
 accumulation, so wherever that accumulation is exact the two agree bit for
 bit after rounding this result to bf16.
+
+``mx_linear`` adds the epilogue of a linear layer (bias, activation, product
+with a second operand, residual) and groups of rows with a matrix each.
 """
 from __future__ import annotations
+
+import math
 
 import numpy as np
 
@@ -45,3 +50,43 @@ def mx_gemm(a, w_packed, w_scale, *, wfmt: str, act: str, alpha: float = 1.0, a_
     K = A.shape[1]
     W = decode_weight(w_packed, w_scale, wfmt, K)
     return alpha * (A @ W.T)
+
+
+def linear_fn(v: np.ndarray, fn: str) -> np.ndarray:
+    if fn == "none":
+        return v
+    if fn == "silu":
+        return v / (1.0 + np.exp(-v))
+    if fn == "gelu":  # v times the normal distribution function at v
+        return v * np.vectorize(lambda z: 0.5 * math.erfc(-z / math.sqrt(2.0)), otypes=[np.float64])(v)
+    if fn == "relu2":
+        return np.maximum(v, 0.0) ** 2
+    raise ValueError(fn)
+
+
+def mx_linear(a, w_packed, w_scale, *, wfmt: str, act: str, bias=None, fn: str = "none", mul=None, residual=None,
+              offsets=None, a_scale=None):
+    """(out, sum over k of |a w|, v) in float64 [M, N]; with offsets [G + 1], w,
+    w_scale and bias have a leading axis of G and rows [offsets[g] - offsets[0],
+    offsets[g+1] - offsets[0]) take entry g; rows of no group are NaN."""
+    M = a.shape[0]
+    if offsets is None:
+        w_packed, w_scale = w_packed[None], w_scale[None]
+        bias = None if bias is None else bias[None]
+        offsets = [0, M]
+    N = w_packed.shape[1]
+    out, size, v_all = (np.full((M, N), np.nan) for _ in range(3))
+    if a_scale is not None:
+        A = mx.dequantize(np.asarray(a, dtype=np.uint8), a_scale, "e4m3")
+    else:
+        A = activations(np.asarray(a, dtype=np.float64), act)
+    for g in range(len(offsets) - 1):
+        rows = slice(int(offsets[g] - offsets[0]), int(offsets[g + 1] - offsets[0]))
+        if rows.start == rows.stop:
+            continue
+        W = decode_weight(w_packed[g], w_scale[g], wfmt, A.shape[1])
+        v = A[rows] @ W.T + (0.0 if bias is None else bias[g])
+        size[rows] = np.abs(A[rows]) @ np.abs(W).T
+        v_all[rows] = v
+        out[rows] = linear_fn(v, fn) * (1.0 if mul is None else mul[rows]) + (0.0 if residual is None else residual[rows])
+    return out, size, v_all

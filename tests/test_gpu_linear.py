@@ -1,0 +1,384 @@
+"""mx_linear on the GPU against the float64 oracle.
+
+Exact cases: A of small integers, weights with scale code 127, integer biases
+and residuals.  Every product and partial sum is a multiple of 1/16 within
+fp32's 24 bits, so v + residual is exact and its one rounding has to agree bit
+for bit with the oracle's.
+
+Bounded cases, with e = 2^-24 and u = 2^-8 (half a step of bf16): an fp32
+accumulation of K products and the bias, in any order and with truncating
+additions, puts dv <= 2 (K + 1) e (sum |a w| + |bias|) on v.  fn moves by at
+most L dv + its own error: |silu'| <= 1.1, |gelu'| <= 1.13, (max(v,0)^2)' <= 2
+|v| + dv, and expf, erfcf and the operations around them stay within 16 e
+relative, with an argument rounding of erfc (e |v| each in the scaled argument)
+worth at most 2 v^2 e relative where the result is not negligible against v e.
+mul, residual and the output rounding follow term by term.
+"""
+import numpy as np
+import pytest
+import torch
+
+from block_scaled_precision_amd import inputs as gen
+from oracle import gemm as og
+from oracle import mx
+from tests.conftest import has_gpu
+from tests.helpers import RMS_REL, assert_y_close, print_flush, y_error
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not has_gpu(), reason="needs a GPU")]
+
+BITS = {"e2m1": 4, "e3m2": 6}
+E32, U = 2.0 ** -24, 2.0 ** -8
+BF16 = torch.bfloat16
+
+
+def _np(t):
+    return t.detach().to(torch.float64).cpu().numpy()
+
+
+def _weights(shape, K, fmt, seed, scales=None):
+    w = gen.random_bytes((*shape, K * BITS[fmt] // 8), seed, 21)
+    if scales is None:
+        return w, torch.full((*shape, K // 32), 127, dtype=torch.uint8)
+    g = torch.Generator().manual_seed(seed)
+    return w, torch.randint(*scales, (*shape, K // 32), generator=g, dtype=torch.uint8)
+
+
+def _ints(shape, seed, tensor, dtype=BF16):
+    return gen.small_integers(shape, seed, tensor).to(dtype)
+
+
+def _same_bits(got, ref, what):
+    """got bf16 equals ref (float64) rounded to bf16; NaN rows of ref: not compared."""
+    rows = ~np.isnan(ref).any(1)
+    g, r = _np(got)[rows], mx.round_to_bf16(ref[rows])
+    bad = np.argwhere(g != r)
+    assert bad.size == 0, f"{what}: {len(bad)} of {g.size} differ, first at {bad[0]}"
+
+
+# (M, N, K, fmt, act): one row, tile edges, sizes that fit each kernel and sizes
+# next to them (N off the column blocks, K off the stage groups)
+DENSE = [
+    (1, 8, 128, "e2m1", "bf16"), (1, 8, 128, "e3m2", "mxfp8"), (1, 512, 1024, "e2m1", "bf16"),
+    (8, 256, 2048, "e2m1", "bf16"), (17, 256, 1536, "e2m1", "bf16"), (16, 520, 768, "e2m1", "bf16"),
+    (100, 512, 512, "e2m1", "bf16"), (130, 256, 1024, "e2m1", "bf16"), (70, 264, 512, "e2m1", "bf16"),
+    (65, 248, 1536, "e2m1", "bf16"), (129, 1000, 384, "e2m1", "bf16"),
+    (33, 72, 640, "e3m2", "bf16"), (200, 320, 1024, "e3m2", "bf16"), (3, 136, 256, "e3m2", "bf16"),
+    (300, 512, 1024, "e2m1", "mxfp8"), (193, 256, 2048, "e2m1", "mxfp8"), (200, 384, 512, "e2m1", "mxfp8"),
+    (260, 264, 1024, "e2m1", "mxfp8"), (10, 200, 384, "e2m1", "mxfp8"), (150, 1000, 1152, "e2m1", "mxfp8"),
+    (300, 256, 512, "e3m2", "mxfp8"), (192, 128, 1536, "e3m2", "mxfp8"), (40, 136, 256, "e3m2", "mxfp8"),
+    (129, 504, 896, "e3m2", "mxfp8"), (16, 256, 512, "e3m2", "mxfp8"), (2, 640, 3584, "e2m1", "mxfp8"),
+]
+IDS = [f"{M}x{N}x{K}_{f}_{a}" for M, N, K, f, a in DENSE]
+
+
+@pytest.mark.parametrize("M,N,K,fmt,act", DENSE, ids=IDS)
+def test_exact_products_are_bit_identical(M, N, K, fmt, act):
+    from block_scaled_precision_amd import moe_mx as m
+    print_flush(f"mx_linear exact M={M} N={N} K={K} {fmt}/{act}")
+    a, (w, s) = _ints((M, K), 0, 20), _weights((N,), K, fmt, 0)
+    bias, res = _ints((N,), 1, 22, torch.float32), _ints((M, N), 2, 23)
+    mul = 2.0 ** gen.small_integers((M, N), 3, 24, -2, 2).float()
+    args = (a.cuda(), w.cuda(), s.cuda(), fmt, act)
+    kw = dict(wfmt=fmt, act=act)
+    ref, _, _ = og.mx_linear(_np(a), w.numpy(), s.numpy(), **kw)
+    _same_bits(m.mx_linear(*args), ref, "plain")
+    for b in (bias, bias.to(BF16)):
+        ref, _, _ = og.mx_linear(_np(a), w.numpy(), s.numpy(), bias=_np(b), residual=_np(res), **kw)
+        _same_bits(m.mx_linear(*args, bias=b.cuda(), residual=res.cuda()), ref, "bias, residual")
+    ref, _, _ = og.mx_linear(_np(a), w.numpy(), s.numpy(), bias=_np(bias), mul=_np(mul), **kw)
+    out = mul.to(BF16).cuda()
+    assert m.mx_linear(*args, bias=bias.cuda(), mul=out, out=out) is out
+    _same_bits(out, ref, "bias, mul in place")
+
+
+def _bound(fn, K, v, size, bias, mul, res, out):
+    dv = 2 * (K + 1) * E32 * (size + np.abs(bias))
+    f = np.abs(og.linear_fn(v, fn))
+    if fn == "none":
+        df = dv
+    elif fn == "silu":
+        df = 1.1 * dv + 16 * E32 * (f + dv)
+    elif fn == "gelu":
+        df = 1.13 * dv + (16 + 2 * v * v) * E32 * (f + dv) + E32 * np.abs(v) * 2.0 ** -24
+    else:
+        df = (2 * np.abs(v) + dv) * dv + 4 * E32 * (f + dv)
+    d = df * np.abs(mul) * (1 + 2 * E32) + 2 * E32 * (f * np.abs(mul) + np.abs(res))
+    return U * np.abs(out) + (1 + U) * d
+
+
+@pytest.mark.parametrize("fn", ["none", "silu", "gelu", "relu2"])
+@pytest.mark.parametrize("M,N,K,fmt,act", [
+    (1, 512, 1024, "e2m1", "bf16"), (9, 264, 384, "e2m1", "bf16"), (100, 512, 512, "e2m1", "bf16"),
+    (130, 256, 512, "e2m1", "bf16"), (40, 136, 256, "e3m2", "bf16"), (300, 512, 1024, "e2m1", "mxfp8"),
+    (200, 384, 512, "e2m1", "mxfp8"), (300, 256, 512, "e3m2", "mxfp8"), (129, 504, 384, "e3m2", "mxfp8"),
+    (70, 1000, 640, "e2m1", "mxfp8"),
+])
+def test_activations_within_their_bound(M, N, K, fmt, act, fn):
+    from block_scaled_precision_amd import moe_mx as m
+    print_flush(f"mx_linear {fn} M={M} N={N} K={K} {fmt}/{act}")
+    a = gen.normal((M, K), 4, 25).to(BF16)
+    w, s = _weights((N,), K, fmt, 4, scales=(118, 123))
+    bias = gen.normal((N,), 4, 26)
+    mul, res = gen.normal((M, N), 4, 27).to(BF16), gen.normal((M, N), 4, 28).to(BF16)
+    for mu, re in ((None, None), (mul, res)):
+        got = m.mx_linear(a.cuda(), w.cuda(), s.cuda(), fmt, act, bias=bias.cuda(), fn=fn,
+                          mul=None if mu is None else mu.cuda(), residual=None if re is None else re.cuda())
+        mu64, re64 = (1.0 if mu is None else _np(mu)), (0.0 if re is None else _np(re))
+        ref, size, v = og.mx_linear(_np(a), w.numpy(), s.numpy(), wfmt=fmt, act=act, bias=_np(bias), fn=fn, mul=mu64 *
+                                    np.ones((M, N)), residual=re64 * np.ones((M, N)))
+        d = np.abs(_np(got) - ref)
+        bound = _bound(fn, K, v, size, _np(bias), mu64, re64, ref)
+        assert (d <= bound).all(), f"{(d > bound).sum()} out of bounds, worst ratio {(d / bound).max():.2f}"
+
+
+def test_activations_over_the_whole_range():
+    """One product per output (K = 128, one nonzero weight of 1), so v = a over
+    the range where exp overflows and erfc vanishes."""
+    from block_scaled_precision_amd import moe_mx as m
+    vals = torch.cat([torch.linspace(-12, 12, 400), torch.tensor([-300.0, -100.0, -89.0, -0.0, 0.0, 89.0, 300.0])]).to(BF16)
+    a = torch.zeros((len(vals), 128), dtype=BF16)
+    a[:, 5] = vals
+    w = torch.zeros((8, 64), dtype=torch.uint8)
+    w[:, 2] = 0x20  # element 5: code 2 = 1.0
+    s = torch.full((8, 4), 127, dtype=torch.uint8)
+    for fn in ("none", "silu", "gelu", "relu2"):
+        got = _np(m.mx_linear(a.cuda(), w.cuda(), s.cuda(), "e2m1", "bf16", fn=fn))
+        v = _np(vals)[:, None] * np.ones((1, 8))
+        with np.errstate(over="ignore"):
+            ref = og.linear_fn(v, fn)
+        bound = U * np.abs(ref) + (16 + 2 * v * v) * E32 * np.abs(ref) + 2.0 ** -126
+        assert (np.abs(got - ref) <= bound).all(), fn
+
+
+# rows per group around the tile heights of every kernel; empty groups first,
+# last and between; a single group; a group with every row
+SIZES = {
+    "mixed": [0, 1, 15, 0, 16, 17, 33, 0], "tiles": [64, 65, 128, 129, 0, 192, 193, 10], "one": [37], "last": [0, 0, 0, 50],
+    "first": [50, 0, 0], "none": [0, 0],
+}
+GROUPED = [
+    (N, K, fmt, act) for N, K, fmt, act in [
+        (512, 1024, "e2m1", "bf16"), (256, 512, "e2m1", "bf16"), (72, 384, "e2m1", "bf16"), (136, 256, "e3m2", "bf16"),
+        (256, 1024, "e2m1", "mxfp8"), (384, 512, "e2m1", "mxfp8"), (256, 512, "e3m2", "mxfp8"), (200, 640, "e3m2", "mxfp8"),
+    ]]
+
+
+@pytest.mark.parametrize("name", sorted(SIZES))
+@pytest.mark.parametrize("N,K,fmt,act", GROUPED, ids=[f"{n}x{k}_{f}_{a}" for n, k, f, a in GROUPED])
+def test_groups_are_bit_identical(N, K, fmt, act, name):
+    """Rows sorted by group; offsets that do not start at 0, rows behind the last
+    group (NaN in A) left as they were, weights at a stride (the gate half of
+    [gate; up])."""
+    from block_scaled_precision_amd import moe_mx as m
+    counts = SIZES[name]
+    G, P, tail = len(counts), sum(counts), 5
+    M = P + tail
+    print_flush(f"mx_linear groups {name} N={N} K={K} {fmt}/{act}")
+    offsets = np.concatenate([[0], np.cumsum(counts)]) + 11
+    a, (w, s) = _ints((M, K), 5, 20), _weights((G, 2 * N), K, fmt, 5)
+    bias, res = _ints((G, N), 6, 22, torch.float32), _ints((M, N), 7, 23)
+    ref, _, _ = og.mx_linear(_np(a), w.numpy()[:, :N], s.numpy()[:, :N], wfmt=fmt, act=act, bias=_np(bias),
+                             residual=_np(res), offsets=offsets)
+    a[P:] = float("nan")
+    out = torch.full((M, N), 33.0, dtype=BF16, device="cuda")
+    off = torch.from_numpy(offsets).int().cuda()
+    m.mx_linear(a.cuda(), w.cuda()[:, :N], s.cuda()[:, :N], fmt, act, bias=bias.cuda(), residual=res.cuda(),
+                expert_offsets=off, out=out)
+    torch.cuda.synchronize()
+    assert (out[P:] == 33.0).all()
+    _same_bits(out, ref, name)
+    if act == "mxfp8":
+        codes, scales = m.mx_quantize(a.cuda(), "e4m3")
+        out2 = m.mx_linear(codes, w.cuda()[:, :N], s.cuda()[:, :N], fmt, act, a_scale=scales, bias=bias.cuda(),
+                           residual=res.cuda(), expert_offsets=off)
+        assert torch.equal(out2[:P], out[:P])
+
+
+def test_offsets_out_of_order_or_range_stay_in_bounds():
+    """Whatever the offsets hold, nothing outside [M, N] is written: out lies
+    between two guard areas."""
+    from block_scaled_precision_amd import moe_mx as m
+    M, N, K, G = 40, 64, 256, 4
+    a, (w, s) = _ints((M, K), 8, 20), _weights((G, N), K, "e2m1", 8)
+    buf = torch.full((3 * M, N), 9.0, dtype=BF16, device="cuda")
+    for off in ([0, 1000, 5, 60, 80], [7, 3, 2, 1, 0], [-2 ** 31, 2 ** 31 - 1, 0, 5, 9], [0, 10, 10, 2, 30]):
+        m.mx_linear(a.cuda(), w.cuda(), s.cuda(), "e2m1", "bf16", expert_offsets=torch.tensor(off, dtype=torch.int32).cuda(),
+                    out=buf[M:2 * M])
+        torch.cuda.synchronize()
+        assert (buf[:M] == 9.0).all() and (buf[2 * M:] == 9.0).all()
+
+
+def test_no_rows_and_aliases():
+    from block_scaled_precision_amd import moe_mx as m
+    a, (w, s) = _ints((0, 256), 9, 20), _weights((64,), 256, "e2m1", 9)
+    assert m.mx_linear(a.cuda(), w.cuda(), s.cuda(), "e2m1", "mxfp8").shape == (0, 64)
+    a = _ints((20, 256), 9, 20).cuda()
+    res = _ints((20, 64), 9, 23).cuda()
+    want = m.mx_linear(a, w.cuda(), s.cuda(), "e2m1", "bf16", residual=res)
+    buf = res.clone()
+    m.mx_linear(a, w.cuda(), s.cuda(), "e2m1", "bf16", residual=buf, out=buf)
+    assert torch.equal(buf, want)
+    with pytest.raises(ValueError, match="out overlaps residual"):
+        big = torch.zeros((21, 64), dtype=BF16, device="cuda")
+        m.mx_linear(a, w.cuda(), s.cuda(), "e2m1", "bf16", residual=big[1:], out=big[:20])
+    with pytest.raises(ValueError, match="out overlaps a"):
+        m.mx_linear(a, w.cuda(), s.cuda(), "e2m1", "bf16", out=a.view(-1)[:1280].view(20, 64))
+
+
+def _experts(m, x, logits, k, wg, wu, wd, bg, bu, bd, residual):
+    """The layer from its parts: route, sort, gated product, down product,
+    combine onto the residual."""
+    ids, w, off, order = m.moe_route(logits, k)
+    rows, row_of = m.moe_permute(x, order, off, k)
+    up = m.mx_linear(rows, *wu, bias=bu, expert_offsets=off)
+    h = m.mx_linear(rows, *wg, bias=bg, fn="silu", mul=up, expert_offsets=off)
+    return m.moe_unpermute(m.mx_linear(h, *wd, bias=bd, expert_offsets=off), row_of, w, residual=residual)
+
+
+@pytest.mark.parametrize("T,fmt,act", [(1, "e2m1", "bf16"), (48, "e2m1", "bf16"), (300, "e2m1", "mxfp8"),
+                                       (120, "e3m2", "mxfp8"), (500, "e2m1", "bf16")])
+def test_parts_make_the_fused_layer(T, fmt, act):
+    """Without biases and residual the parts are the layer moe_fused computes.
+
+    Against the oracle, with bf16 roundings where the parts have them (up, h and
+    the down product): within the layer's output bar.  Against moe_fused: the
+    same bar with bf16 activations.  With MXFP8 activations moe_fused quantizes
+    h from fp32 and the parts from bf16, after a rounding of up and one of h: h
+    moves by |d| <= 2 * 2^-8 |h| in front of a rounding with steps s <= 2^-3 |h|,
+    which changes its result by s with probability |d| / s: E[change^2] = |d| s <=
+    2^-10 h^2, so the relative rms of the change of h, and of y, which is linear in
+    h, stays below 2^-5 on top of the bar."""
+    from block_scaled_precision_amd import moe_mx as m
+    H, I, E, k = 512, 1024, 8, 3
+    print_flush(f"layer from parts T={T} {fmt}/{act}")
+    x, logits = gen.normal((T, H), 10, 1).to(BF16).cuda(), gen.normal((T, E), 10, 0).cuda()
+    w1, s1 = m.mx_quantize(gen.normal((E, 2 * I, H), 10, 2, std=0.02).cuda(), fmt)
+    w2, s2 = m.mx_quantize(gen.normal((E, H, I), 10, 3, std=0.02).cuda(), fmt)
+    parts = _experts(m, x, logits, k, (w1[:, :I], s1[:, :I], fmt, act), (w1[:, I:], s1[:, I:], fmt, act),
+                     (w2, s2, fmt, act), None, None, None, None)
+    fused = m.moe_fused(m.make_problem(T, H, I, E, k, fmt, act), x, m.MoeWeights(w1, s1, w2, s2, fmt), logits)
+    ids, wt, off, order = m.moe_route(logits, k)
+    n1, n2, q1, q2 = (t.cpu().numpy() for t in (w1, w2, s1, s2))
+    kw = dict(wfmt=fmt, act=act, offsets=off.cpu().numpy())
+    rows = _np(x)[order.cpu().numpy() // k]
+    up = mx.round_to_bf16(og.mx_linear(rows, n1[:, I:], q1[:, I:], **kw)[0])
+    h = mx.round_to_bf16(og.mx_linear(rows, n1[:, :I], q1[:, :I], fn="silu", mul=up, **kw)[0])
+    down = mx.round_to_bf16(og.mx_linear(h, n2, q2, **kw)[0])
+    y = np.zeros((T, H))
+    np.add.at(y, order.cpu().numpy() // k, down * _np(wt).ravel()[order.cpu().numpy()][:, None])
+    assert_y_close(_np(parts), y, f"parts against the oracle T={T} {fmt}/{act}")
+    if act == "bf16":
+        assert_y_close(_np(parts), _np(fused), f"parts against the fused layer T={T} {fmt}/{act}")
+    else:
+        assert y_error(_np(parts), _np(fused))[1] <= RMS_REL + 2.0 ** -5
+    # shards of the experts add up to the layer: rows, products and combine per shard
+    total = torch.zeros((T, H), device="cuda")
+    for lo, n in ((0, 3), (3, 5)):
+        rows, row_of = m.moe_permute(x, order, off, k, local_offset=lo, local_count=n)
+        loc, sl = off[lo:lo + n + 1], slice(lo, lo + n)
+        up = m.mx_linear(rows, w1[sl, I:], s1[sl, I:], fmt, act, expert_offsets=loc)
+        h = m.mx_linear(rows, w1[sl, :I], s1[sl, :I], fmt, act, fn="silu", mul=up, expert_offsets=loc)
+        down = m.mx_linear(h, w2[sl], s2[sl], fmt, act, expert_offsets=loc)
+        total += m.moe_unpermute(down, row_of, wt).float()
+    assert_y_close(_np(total), _np(parts), f"shards against the whole T={T} {fmt}/{act}")
+
+
+def test_layer_from_parts_repeats_on_streams_and_in_replayed_graphs():
+    """Two graphs captured from the same function, replayed in turn with other
+    inputs and eager work between them: each owns its workspaces."""
+    from block_scaled_precision_amd import moe_mx as m
+    T, H, I, E, k = 40, 256, 512, 8, 2
+    print_flush("layer from parts: streams and graphs")
+    q = [m.mx_quantize(gen.normal((E, n, kk), 11, 50 + i, std=0.05).cuda(), "e2m1")
+         for i, (n, kk) in enumerate(((I, H), (I, H), (H, I)))]
+    biases = [gen.normal((E, n), 11, 60 + i).cuda() for i, n in enumerate((I, I, H))]
+    for act in ("bf16", "mxfp8"):
+        ws = [(*p, "e2m1", act) for p in q]
+        sets = [(gen.normal((T, H), 11, 70 + i).to(BF16).cuda(), gen.normal((T, E), 11, 80 + i).cuda()) for i in range(3)]
+
+        def layer(x, lg):
+            return _experts(m, x, lg, k, *ws, *biases, x)
+
+        want = [layer(*s) for s in sets]
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            other = layer(*sets[1])
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(other, want[1]) and torch.equal(layer(*sets[0]), want[0])
+        graphs = []
+        for _ in range(2):
+            bufs = [t.clone() for t in sets[0]]
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                out = layer(*bufs)
+            graphs.append((g, bufs, out))
+        for i, which in ((1, 0), (2, 1), (0, 0), (1, 1), (2, 0)):
+            g, bufs, out = graphs[which]
+            for b, t in zip(bufs, sets[i]):
+                b.copy_(t)
+            g.replay()
+            torch.cuda.synchronize()
+            layer(*sets[0])
+            assert torch.equal(out, want[i]), f"{act}: graph {which}, set {i}"
+
+
+def test_prepared_call_and_stream_argument():
+    from block_scaled_precision_amd import moe_mx as m
+    M, N, K = 24, 256, 512
+    a, (w, s) = _ints((M, K), 12, 20).cuda(), _weights((N,), K, "e2m1", 12)
+    w, s = w.cuda(), s.cuda()
+    for act in ("bf16", "mxfp8"):
+        call = m.OpCall(m.mx_linear, a, w, s, "e2m1", act, fn="relu2")
+        y = call()
+        assert torch.equal(y, m.mx_linear(a, w, s, "e2m1", act, fn="relu2"))
+        a.neg_()
+        assert call() is y and torch.equal(y, m.mx_linear(a, w, s, "e2m1", act, fn="relu2"))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        y2 = m.mx_linear(a, w, s, "e2m1", act, fn="relu2", stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(y2, y)
+
+
+def test_rows_past_32_bit_offsets():
+    """Output and operand offsets beyond 2^32 bytes and elements: the last rows
+    of a long batch against the same rows alone."""
+    from block_scaled_precision_amd import moe_mx as m
+    K, N = 128, 4096
+    M = (1 << 32) // N + 1000
+    print_flush(f"mx_linear 64-bit offsets M={M}")
+    (w, s) = _weights((N,), K, "e2m1", 13)
+    w, s = w.cuda(), s.cuda()
+    a = torch.ones((M, K), dtype=BF16, device="cuda")
+    a[-40:] = _ints((40, K), 13, 20).cuda()
+    for act in ("bf16", "mxfp8"):
+        out = m.mx_linear(a, w, s, "e2m1", act)
+        assert torch.equal(out[-40:], m.mx_linear(a[-40:].contiguous(), w, s, "e2m1", act))
+        assert torch.equal(out[0], out[M - 41])
+
+
+def _draw(n, seed=20261207):
+    rng = np.random.default_rng(seed)
+    out = []
+    for i in range(n):
+        G = int(rng.choice([0, 0, 1, 3, 9]))
+        M, N, K = int(rng.integers(1, 400)), 8 * int(rng.integers(1, 100)), 128 * int(rng.integers(1, 17))
+        out.append(pytest.param(M, N, K, G, str(rng.choice(["e2m1", "e3m2"])), str(rng.choice(["bf16", "mxfp8"])), i))
+    return out
+
+
+@pytest.mark.parametrize("M,N,K,G,fmt,act,i", _draw(32))
+def test_drawn_shapes_are_bit_identical(M, N, K, G, fmt, act, i):
+    from block_scaled_precision_amd import moe_mx as m
+    print_flush(f"mx_linear drawn M={M} N={N} K={K} G={G} {fmt}/{act}")
+    rng = np.random.default_rng(i)
+    a, (w, s) = _ints((M, K), 14 + i, 20), _weights((G, N) if G else (N,), K, fmt, 14 + i)
+    bias, res = _ints((G, N) if G else (N,), 15 + i, 22, torch.float32), _ints((M, N), 16 + i, 23)
+    offsets = np.concatenate([[0], np.sort(rng.integers(0, M + 1, G))]) if G else None
+    ref, _, _ = og.mx_linear(_np(a), w.numpy(), s.numpy(), wfmt=fmt, act=act, bias=_np(bias), residual=_np(res),
+                             offsets=offsets)
+    off = None if offsets is None else torch.from_numpy(offsets).int().cuda()
+    got = m.mx_linear(a.cuda(), w.cuda(), s.cuda(), fmt, act, bias=bias.cuda(), residual=res.cuda(), expert_offsets=off)
+    _same_bits(got, ref, "drawn")

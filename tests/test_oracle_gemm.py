@@ -109,3 +109,35 @@ def test_prequantized_activations_and_the_layer_fc1():
     d1 = om.decode_weight(p, s, "e3m2", K)
     z = om.activations(a, "mxfp8") @ d1.T
     assert np.array_equal(og.mx_gemm(a, p, s, wfmt="e3m2", act="mxfp8"), z)
+
+
+@pytest.mark.parametrize("fn", ["none", "silu", "gelu", "relu2"])
+def test_linear_epilogue_matches_torch_float64(fn):
+    rng = np.random.default_rng(21)
+    M, N, K = 5, 8, 64
+    a = _bf16(rng, (M, K))
+    p, s = om.quantize_weight(rng.standard_normal((N, K)) * 0.3, "e3m2")
+    bias, mul, res = rng.standard_normal(N), rng.standard_normal((M, N)), rng.standard_normal((M, N))
+    out, size, v = og.mx_linear(a, p, s, wfmt="e3m2", act="bf16", bias=bias, fn=fn, mul=mul, residual=res)
+    z = torch.from_numpy(og.mx_gemm(a, p, s, wfmt="e3m2", act="bf16")) + torch.from_numpy(bias)
+    f = {"none": lambda t: t, "silu": torch.nn.functional.silu, "gelu": torch.nn.functional.gelu,
+         "relu2": lambda t: torch.relu(t) ** 2}[fn]
+    ref = f(z) * torch.from_numpy(mul) + torch.from_numpy(res)
+    np.testing.assert_allclose(out, ref.numpy(), rtol=1e-12, atol=1e-12)
+    np.testing.assert_allclose(v, z.numpy(), rtol=1e-14)
+    assert (size >= np.abs(v - bias) - 1e-12).all()
+
+
+def test_linear_groups_are_separate_products():
+    rng = np.random.default_rng(22)
+    G, N, K = 4, 8, 32
+    offsets = np.array([3, 5, 5, 6, 9])  # group 1 empty, offsets not from 0
+    a = _bf16(rng, (8, K))
+    packed = [om.quantize_weight(rng.standard_normal((N, K)), "e2m1") for _ in range(G)]
+    p, s = (np.stack([q[i] for q in packed]) for i in range(2))
+    bias = rng.standard_normal((G, N))
+    out, _, _ = og.mx_linear(a, p, s, wfmt="e2m1", act="mxfp8", bias=bias, offsets=offsets)
+    for g, rows in ((0, slice(0, 2)), (2, slice(2, 3)), (3, slice(3, 6))):
+        ref = og.mx_gemm(a[rows], p[g], s[g], wfmt="e2m1", act="mxfp8") + bias[g]
+        np.testing.assert_allclose(out[rows], ref, rtol=1e-13)
+    assert np.isnan(out[6:]).all()
