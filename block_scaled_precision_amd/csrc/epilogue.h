@@ -47,4 +47,39 @@ __device__ __forceinline__ void epi_store(const FcArgs& p, int64_t o, float v) {
   ((__bf16*)p.obuf)[o] = (__bf16)v;
 }
 
+// R rows from row0 (rows from row_end on: none) by C columns col0, col0 +
+// cstep, ... of out, v(i, n) their accumulators.  The block's second factors and
+// residuals are loaded before its first store: a store may alias them, so the
+// loads of a row could not pass the stores of the row before, and each would
+// cost a memory latency.  FN: the function, or -1 to take it from p.
+template <int R, int C, int FN = -1, class V>
+__device__ __forceinline__ void epi_block(const FcArgs& p, int group, int64_t row0, int64_t row_end, int col0,
+                                          int cstep, V v) {
+  float bias[C];
+  uint16_t mu[R][C], re[R][C];
+#pragma unroll
+  for (int n = 0; n < C; ++n) bias[n] = col0 + n * cstep < p.N ? epi_bias(p, group, col0 + n * cstep) : 0.f;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int n = 0; n < C; ++n) {
+      const int col = col0 + n * cstep;
+      const bool in = row0 + i < row_end && col < p.N;
+      const int64_t o = (row0 + i) * p.N + col;
+      mu[i][n] = p.epi.mul && in ? p.epi.mul[o] : 0;
+      re[i][n] = p.epi.residual && in ? p.epi.residual[o] : 0;
+    }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int n = 0; n < C; ++n) {
+      const int col = col0 + n * cstep;
+      if (row0 + i >= row_end || col >= p.N) continue;
+      float x = epi_fn(FN < 0 ? p.epi.fn : FN, v(i, n) + bias[n]);
+      if (p.epi.mul) x *= bf16_bits_to_f32(mu[i][n]);
+      if (p.epi.residual) x += bf16_bits_to_f32(re[i][n]);
+      ((__bf16*)p.obuf)[(row0 + i) * p.N + col] = (__bf16)x;
+    }
+}
+
 }  // namespace moe_mx

@@ -127,6 +127,9 @@ hipError_t launch_fc_small_routed(const FcArgs& p, int grid, hipStream_t st);
 hipError_t launch_splitk_reduce(const float* part, int ksplit, int64_t n4, float alpha, uint16_t* y,
                                 hipStream_t st);
 
+// mx_linear: out = epilogue of the sum over s of p.part[s] (N % 4 == 0, dense)
+hipError_t launch_splitk_epilogue(const FcArgs& p, hipStream_t st);
+
 // Mid-M variant for bf16 activations and E2M1 weights when experts see many
 // rows: M-tiles of up to `rows` rows (kMidRows or kMidRowsHigh), N-blocks of
 // kWideCols weight rows, i.e. 128 h columns (FC1: nchunks = I / 128) or 256

@@ -33,6 +33,7 @@
 #include <hip/hip_runtime.h>
 
 #include "copy_ring.h"
+#include "epilogue.h"
 #include "gemm.h"
 #include "mx_device.h"
 
@@ -124,9 +125,11 @@ __device__ __forceinline__ MGeom m_geom(const FcArgs& p, const MSched& sc, int l
   return g;
 }
 
-// weight row (within the expert's matrix) of row jr of N-block nb
-template <bool FC1>
+// weight row (within the expert's matrix) of row jr of N-block nb; EPI: rows
+// past N repeat the last one (their columns are not stored)
+template <bool FC1, bool EPI>
 __device__ __forceinline__ int64_t m_wrow(const FcArgs& p, int nb, int jr) {
+  if (EPI) return min(nb * MBN + jr, p.N - 1);
   if (FC1) return jr < MBN / 2 ? (int64_t)nb * (MBN / 2) + jr : (int64_t)p.N + nb * (MBN / 2) + jr - MBN / 2;
   return (int64_t)nb * MBN + jr;
 }
@@ -189,7 +192,7 @@ __device__ __forceinline__ void m_stage(const uint8_t* st, const uint8_t* sg, in
   }
 }
 
-template <bool FC1, int TM>
+template <bool FC1, int TM, bool EPI>
 __device__ __forceinline__ void mid_multiply(const FcArgs& p, const MSched& sc, uint8_t* smem, int w) {
   using L = ML<TM>;
   const int lane = threadIdx.x & 63;
@@ -208,7 +211,7 @@ __device__ __forceinline__ void mid_multiply(const FcArgs& p, const MSched& sc, 
   int m_row[2][4];
   float m_wt[2][4];
   auto load_meta = [&]() {
-    if (!FC1 && p.dense_rows == 0) {
+    if (!FC1 && !EPI && p.dense_rows == 0) {
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -247,6 +250,16 @@ __device__ __forceinline__ void mid_multiply(const FcArgs& p, const MSched& sc, 
               for (int n = 0; n < 4; ++n) o[16 * n] = f32_to_bf16_rne(gated_act(p.act_fn, acc[m][n][i], acc[m][n + 4][i]));
             }
           }
+      } else if (EPI) {
+        // two 16-row sub-tiles, four columns at a time: their factors and
+        // residuals are all requested before the first is used
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int n0 = 0; n0 < 8; n0 += 4)
+            epi_block<4, 4>(p, it.expert, it.p0 + 32 * wr + 16 * m + 4 * g, it.p0 + it.rows,
+                            it.nb * MBN + 128 * wc + 16 * n0 + r16, 16,
+                            [&](int i, int n) { return acc[m][n0 + n][i]; });
       } else {
         // row metadata by plain per-lane loads (the multiply waves issue no
         // copies, so their memory counter holds nothing else)
@@ -283,7 +296,7 @@ __device__ __forceinline__ void mid_multiply(const FcArgs& p, const MSched& sc, 
 
 // -------------------------------------------------------- weight copies ---
 
-template <bool FC1, int TM>
+template <bool FC1, int TM, bool EPI>
 __device__ __forceinline__ void mid_weights(const FcArgs& p, const MSched& sc, uint8_t* smem, int bw) {
   using L = ML<TM>;
   const int lane = threadIdx.x & 63;
@@ -302,13 +315,13 @@ __device__ __forceinline__ void mid_weights(const FcArgs& p, const MSched& sc, u
       const int t = kBCopies * bw + i;
       const int jr = 16 * t + lane / 4;
       const int ch = (lane % 4) ^ ((jr >> 1) & 3);
-      src[i] = wb + m_wrow<FC1>(p, it.nb, jr) * wrow + 16 * ch;
+      src[i] = wb + m_wrow<FC1, EPI>(p, it.nb, jr) * wrow + 16 * ch;
     }
 #pragma unroll
     for (int i = 0; i < kGCopies; ++i) {
       // scale copy s lands rows 64s .. 64s + 63, 16 B (4 stages) per row
       const int jr = 64 * (kGCopies * bw + i) + lane;
-      ssrc[i] = sb + m_wrow<FC1>(p, it.nb, jr) * (K / 32);
+      ssrc[i] = sb + m_wrow<FC1, EPI>(p, it.nb, jr) * (K / 32);
     }
   };
   int li = 0, ls = 0, issued = 0;
@@ -402,7 +415,9 @@ __device__ __forceinline__ void mid_activations(const FcArgs& p, const MSched& s
   }
 }
 
-template <bool FC1, int TM>
+// EPI (mx_linear on FC2): rows of A and out are permuted rows, finished by the
+// epilogue
+template <bool FC1, int TM, bool EPI>
 __global__ __launch_bounds__(ML<TM>::THREADS, 1) void k_fc_mid(FcArgs p) {
   using L = ML<TM>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[L::L_TOTAL];
@@ -422,8 +437,8 @@ __global__ __launch_bounds__(ML<TM>::THREADS, 1) void k_fc_mid(FcArgs p) {
   sc.total = sc.my_items * sc.nk;
   if (sc.total == 0) return;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (w < L::MUL_WAVES) mid_multiply<FC1, TM>(p, sc, smem, w);
-  else if (w < L::MUL_WAVES + 2) mid_weights<FC1, TM>(p, sc, smem, w - L::MUL_WAVES);
+  if (w < L::MUL_WAVES) mid_multiply<FC1, TM, EPI>(p, sc, smem, w);
+  else if (w < L::MUL_WAVES + 2) mid_weights<FC1, TM, EPI>(p, sc, smem, w - L::MUL_WAVES);
   else mid_activations<FC1, TM>(p, sc, smem, w - L::MUL_WAVES - 2);
 }
 
@@ -431,8 +446,9 @@ __global__ __launch_bounds__(ML<TM>::THREADS, 1) void k_fc_mid(FcArgs p) {
 
 template <int TM>
 static hipError_t launch_mid_t(const FcArgs& p, bool fc1, int grid, hipStream_t st) {
-  if (fc1) k_fc_mid<true, TM><<<grid, ML<TM>::THREADS, 0, st>>>(p);
-  else k_fc_mid<false, TM><<<grid, ML<TM>::THREADS, 0, st>>>(p);
+  if (p.linear) k_fc_mid<false, TM, true><<<grid, ML<TM>::THREADS, 0, st>>>(p);
+  else if (fc1) k_fc_mid<true, TM, false><<<grid, ML<TM>::THREADS, 0, st>>>(p);
+  else k_fc_mid<false, TM, false><<<grid, ML<TM>::THREADS, 0, st>>>(p);
   return hipGetLastError();
 }
 

@@ -37,6 +37,7 @@
 #include <hip/hip_runtime.h>
 
 #include "copy_ring.h"
+#include "epilogue.h"
 #include "gemm.h"
 #include "mx_device.h"
 #include "batch_route.h"
@@ -132,8 +133,11 @@ __device__ __forceinline__ SGeom s_geom(const FcArgs& p, const SSched& sc, int l
   return g;
 }
 
-template <bool FC1>
+// weight row of row jr of N-block nb; EPI: rows past N repeat the last one (their
+// columns are not stored)
+template <bool FC1, bool EPI>
 __device__ __forceinline__ int64_t s_wrow(const FcArgs& p, int nb, int jr) {
+  if (EPI) return min(nb * SBN + jr, p.N - 1);
   if (FC1) return jr < SBN / 2 ? (int64_t)nb * (SBN / 2) + jr : (int64_t)p.N + nb * (SBN / 2) + jr - SBN / 2;
   return (int64_t)nb * SBN + jr;
 }
@@ -167,7 +171,7 @@ __device__ __forceinline__ void wait_ops(int n) {
 
 // ------------------------------------------------------------ multiply ---
 
-template <bool FC1, int GS, bool RT>
+template <bool FC1, int GS, bool RT, bool EPI>
 __device__ __forceinline__ void small_multiply(const FcArgs& p, const SSched& sc, uint8_t* smem) {
   using SG = SGroup<GS>;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -180,7 +184,7 @@ __device__ __forceinline__ void small_multiply(const FcArgs& p, const SSched& sc
   SGeom it = s_geom<RT>(p, sc, 0, smem);
   // routed FC2: the item's row metadata, loaded when the item starts (scalar
   // cache) so that its epilogue does not wait for it
-  const bool routed2 = !FC1 && p.dense_rows == 0;
+  const bool routed2 = !FC1 && !EPI && p.dense_rows == 0;
   Dw16 m_ids = {}, m_wts = {};
   if (routed2) {
     m_ids = load_dw16(p.sorted_assign + it.p0);
@@ -237,13 +241,24 @@ __device__ __forceinline__ void small_multiply(const FcArgs& p, const SSched& sc
       float wt[4];
       if (sc.S > 1) {
         // split dense GEMM: this K range's unscaled fp32 sums
-        float* o = p.part + ((int64_t)it.ks * p.dense_rows + it.p0) * p.N + it.nb * SBN + 32 * w + r16;
+        const int col = it.nb * SBN + 32 * w + r16;
+        float* o = p.part + ((int64_t)it.ks * p.dense_rows + it.p0) * p.N + col;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (4 * g + i < it.rows) {
-            o[(int64_t)(4 * g + i) * p.N] = acc[0][i];
-            o[(int64_t)(4 * g + i) * p.N + 16] = acc[1][i];
+            if (!EPI || col < p.N) o[(int64_t)(4 * g + i) * p.N] = acc[0][i];
+            if (!EPI || col + 16 < p.N) o[(int64_t)(4 * g + i) * p.N + 16] = acc[1][i];
           }
+        }
+      } else if (EPI) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int col = it.nb * SBN + 32 * w + 16 * n + r16;
+          if (col >= p.N) continue;
+          const float bias = epi_bias(p, it.expert, col);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (4 * g + i < it.rows) epi_store(p, (int64_t)(it.p0 + 4 * g + i) * p.N + col, acc[n][i] + bias);
         }
       } else if (p.dense_rows > 0) {
 #pragma unroll
@@ -270,7 +285,7 @@ __device__ __forceinline__ void small_multiply(const FcArgs& p, const SSched& sc
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (sc.S == 1 && 4 * g + i < it.rows) {
+        if (!EPI && sc.S == 1 && 4 * g + i < it.rows) {
           uint16_t* o = p.obuf + (int64_t)orow[i] * p.N + it.nb * SBN + 32 * w + r16;
           o[0] = f32_to_bf16_rne(wt[i] * acc[0][i]);
           o[16] = f32_to_bf16_rne(wt[i] * acc[1][i]);
@@ -292,7 +307,7 @@ __device__ __forceinline__ void small_multiply(const FcArgs& p, const SSched& sc
 
 // -------------------------------------------------------- weight copies ---
 
-template <bool FC1, int GS, bool RT>
+template <bool FC1, int GS, bool RT, bool EPI>
 __device__ __forceinline__ void small_weights(const FcArgs& p, const SSched& sc, uint8_t* smem) {
   using SG = SGroup<GS>;
   const int lane = threadIdx.x & 63, bw = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) - kWaveB);
@@ -313,7 +328,7 @@ __device__ __forceinline__ void small_weights(const FcArgs& p, const SSched& sc,
       const int t = kBData * bw + i;  // 1-KB copy index within the stage
       const int jr = (64 / CPR) * t + lane / CPR;
       const int ch = (lane % CPR) ^ wb_swz(jr);
-      src[i] = wb + s_wrow<FC1>(p, it.nb, jr) * wrow + 16 * ch;
+      src[i] = wb + s_wrow<FC1, EPI>(p, it.nb, jr) * wrow + 16 * ch;
     }
     // scale group: GROW bytes per row, SG::LW per lane; copy t covers bytes
     // [64 LW t, 64 LW (t+1)) of the group buffer (row-major)
@@ -321,7 +336,7 @@ __device__ __forceinline__ void small_weights(const FcArgs& p, const SSched& sc,
     for (int i = 0; i < SG::COPIES; ++i) {
       const int byte = SG::LW * (64 * (SG::COPIES * bw + i) + lane);
       const int jr = byte / GROW, within = byte % GROW;
-      ssrc[i] = sb + s_wrow<FC1>(p, it.nb, jr) * (K / 32) + within;
+      ssrc[i] = sb + s_wrow<FC1, EPI>(p, it.nb, jr) * (K / 32) + within;
     }
   };
   int li = 0, ls = 0, issued = 0;
@@ -419,7 +434,9 @@ __device__ __forceinline__ void small_activations(const FcArgs& p, const SSched&
 
 }  // namespace
 
-template <bool FC1, int GS>
+// EPI (mx_linear on FC2): rows of A and out are permuted rows, finished by the
+// epilogue
+template <bool FC1, int GS, bool EPI>
 __global__ __launch_bounds__(kThreadsS, 1) void k_fc_small(FcArgs p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[L_SG + L_SG_SIZE];
   SSched sc;
@@ -434,8 +451,8 @@ __global__ __launch_bounds__(kThreadsS, 1) void k_fc_small(FcArgs p) {
   sc.total = sc.my_items * sc.nk;
   if (sc.total == 0) return;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (w < kMulW) small_multiply<FC1, GS, false>(p, sc, smem);
-  else if (w < kWaveA) small_weights<FC1, GS, false>(p, sc, smem);
+  if (w < kMulW) small_multiply<FC1, GS, false, EPI>(p, sc, smem);
+  else if (w < kWaveA) small_weights<FC1, GS, false, EPI>(p, sc, smem);
   else small_activations<FC1, false>(p, sc, smem);
 }
 
@@ -505,18 +522,18 @@ __global__ __launch_bounds__(kThreadsS, 1) void k_fc_small_routed(FcArgs p) {
   sc.total = sc.my_items * sc.nk;
   if (sc.total == 0) return;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (w < kMulW) small_multiply<true, GS, true>(p, sc, smem);
-  else if (w < kWaveA) small_weights<true, GS, true>(p, sc, smem);
+  if (w < kMulW) small_multiply<true, GS, true, false>(p, sc, smem);
+  else if (w < kWaveA) small_weights<true, GS, true, false>(p, sc, smem);
   else small_activations<true, true>(p, sc, smem);
 }
 
-template <bool FC1>
+template <bool FC1, bool EPI>
 static hipError_t launch_small_t(const FcArgs& p, int grid, hipStream_t st) {
   // scale groups: the largest of 4, 2, 1 stages that divides the stages of an item
   const int nk = p.K / SBK / (p.ksplit > 1 ? p.ksplit : 1);
-  if (nk % 4 == 0) k_fc_small<FC1, 4><<<grid, kThreadsS, 0, st>>>(p);
-  else if (nk % 2 == 0) k_fc_small<FC1, 2><<<grid, kThreadsS, 0, st>>>(p);
-  else k_fc_small<FC1, 1><<<grid, kThreadsS, 0, st>>>(p);
+  if (nk % 4 == 0) k_fc_small<FC1, 4, EPI><<<grid, kThreadsS, 0, st>>>(p);
+  else if (nk % 2 == 0) k_fc_small<FC1, 2, EPI><<<grid, kThreadsS, 0, st>>>(p);
+  else k_fc_small<FC1, 1, EPI><<<grid, kThreadsS, 0, st>>>(p);
   return hipGetLastError();
 }
 
@@ -540,6 +557,31 @@ __global__ void k_splitk_reduce(const float4* __restrict__ part, int ksplit, int
   y[i] = o;
 }
 
+// The same sums finished by mx_linear's epilogue: 4 neighbouring columns per thread.
+__global__ void k_splitk_epilogue(FcArgs p, int64_t n4) {
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n4) return;
+  const float4* part = (const float4*)p.part;
+  float4 s = part[i];
+  for (int k = 1; k < p.ksplit; ++k) {
+    const float4 v = part[(int64_t)k * n4 + i];
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  const int col = (int)(4 * i % p.N);
+  const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) epi_store(p, 4 * i + q, v[q] + epi_bias(p, 0, col + q));
+}
+
+hipError_t launch_splitk_epilogue(const FcArgs& p, hipStream_t st) {
+  const int64_t n4 = (int64_t)p.dense_rows * p.N / 4;
+  k_splitk_epilogue<<<(unsigned)((n4 + 255) / 256), 256, 0, st>>>(p, n4);
+  return hipGetLastError();
+}
+
 hipError_t launch_splitk_reduce(const float* part, int ksplit, int64_t n4, float alpha, uint16_t* y,
                                 hipStream_t st) {
   if (n4 <= 0) return hipSuccess;
@@ -549,7 +591,8 @@ hipError_t launch_splitk_reduce(const float* part, int ksplit, int64_t n4, float
 
 hipError_t launch_fc_small(const FcArgs& p, bool fc1, int grid, hipStream_t st) {
   if (grid < 1) grid = 1;
-  return fc1 ? launch_small_t<true>(p, grid, st) : launch_small_t<false>(p, grid, st);
+  if (p.linear) return launch_small_t<false, true>(p, grid, st);
+  return fc1 ? launch_small_t<true, false>(p, grid, st) : launch_small_t<false, false>(p, grid, st);
 }
 
 template <int GS>

@@ -55,6 +55,7 @@
 #include <hip/hip_runtime.h>
 
 #include "copy_ring.h"
+#include "epilogue.h"
 #include "gemm.h"
 #include "mx_device.h"
 #include "tiled_count.h"
@@ -199,9 +200,11 @@ __device__ __forceinline__ int k_stage(const Sched& sc, int nb, int ls) {
   return s < sc.nk ? s : s - sc.nk;
 }
 
-// weight row held at B-tile row jr of an N-block of TN rows
-template <bool FC1, int TN>
+// weight row held at B-tile row jr of an N-block of TN rows; EPI: rows past N
+// repeat the last one (their columns are not stored)
+template <bool FC1, int TN, bool EPI>
 __device__ __forceinline__ int64_t w_row(const FcArgs& p, int nb, int jr) {
+  if (EPI) return min(nb * TN + jr, p.N - 1);
   if (FC1) return jr < TN / 2 ? (int64_t)nb * (TN / 2) + jr : (int64_t)p.N + nb * (TN / 2) + jr - TN / 2;
   return (int64_t)nb * TN + jr;
 }
@@ -275,7 +278,7 @@ __device__ __forceinline__ void compute_stage(v16f (&acc)[Grid<TM>::MAX_SUB][2],
   }
 }
 
-template <bool FC1, int WF, int TM>
+template <bool FC1, int WF, int TM, bool EPI>
 __device__ __forceinline__ void multiply_role(const FcArgs& p, const Sched& sc, uint8_t* smem) {
   using L = Lds<WF, TM>;
   using BL = BLay<WF, TM>;
@@ -331,6 +334,14 @@ __device__ __forceinline__ void multiply_role(const FcArgs& p, const Sched& sc, 
     for (int m = 0; m < kMaxSub; ++m) {
       if (m >= nm) continue;
       const int sbk = wm + G::WM * m;
+      if constexpr (EPI) {
+        // four rows of both column tiles at a time
+#pragma unroll
+        for (int i0 = 0; i0 < 16; i0 += 4)
+          epi_block<4, 2>(p, it.expert, it.p0 + 32 * sbk + 2 * i0 + 4 * g, it.p0 + it.rows,
+                          it.nb * TN + 64 * wn + l32, 32, [&](int i, int n) { return acc[m][n][i0 + i]; });
+        continue;
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int row = 32 * sbk + 8 * (i >> 2) + 4 * g + (i & 3);
@@ -400,7 +411,7 @@ __device__ __forceinline__ void copy_table(const FcArgs& p, const ItemGeom& it, 
   }
 }
 
-template <bool FC1, int WF, int TM>
+template <bool FC1, int WF, int TM, bool EPI>
 __device__ __forceinline__ void activation_role(const FcArgs& p, const Sched& sc, uint8_t* smem) {
   using L = Lds<WF, TM>;
   using AL = ALay<WF, TM>;
@@ -410,7 +421,7 @@ __device__ __forceinline__ void activation_role(const FcArgs& p, const Sched& sc
   static_assert(kMaxWait < 64, "vmcnt range");
   const int lane = threadIdx.x & 63, aw = (threadIdx.x >> 6) - kWaveA;
   const int K = p.K;
-  const bool routed = p.dense_rows == 0;
+  const bool routed = !EPI && p.dense_rows == 0;  // row tables in use
   const uint32_t lds0 = lds_addr(smem);
   const int c = (lane & 7) ^ (lane >> 3);  // chunk that lands in this lane's LDS slot
   const TiledCopyCount<AL::STAGES, kACodeCopies, kGC> cnt{sc.total, sc.total / 4};
@@ -497,7 +508,7 @@ __device__ __forceinline__ void activation_role(const FcArgs& p, const Sched& sc
 
 // --------------------------------------------------------- weight copies ---
 
-template <bool FC1, int WF, int TM>
+template <bool FC1, int WF, int TM, bool EPI>
 __device__ __forceinline__ void weight_role(const FcArgs& p, const Sched& sc, uint8_t* smem) {
   using L = Lds<WF, TM>;
   using BL = BLay<WF, TM>;
@@ -529,7 +540,7 @@ __device__ __forceinline__ void weight_role(const FcArgs& p, const Sched& sc, ui
         jr = cc / 6;
         ch = cc % 6;
       }
-      bsrc[i] = wb + w_row<FC1, TN>(p, it.nb, jr) * wrow + 16 * ch;
+      bsrc[i] = wb + w_row<FC1, TN, EPI>(p, it.nb, jr) * wrow + 16 * ch;
     }
   };
   int li = 0, ls = 0, issued = 0;  // code cursor
@@ -557,7 +568,7 @@ __device__ __forceinline__ void weight_role(const FcArgs& p, const Sched& sc, ui
 #pragma unroll
       for (int i = 0; i < kGC; ++i)
         gsrc[i] = p.w_scale + (int64_t)it.expert * p.ws_estride +
-                  w_row<FC1, TN>(p, it.nb, 64 * (kGC * bw + i) + lane) * (K / 32);
+                  w_row<FC1, TN, EPI>(p, it.nb, 64 * (kGC * bw + i) + lane) * (K / 32);
     }
     const int ks = k_stage(sc, gnb, gls);
 #pragma unroll
@@ -584,7 +595,9 @@ __device__ __forceinline__ void weight_role(const FcArgs& p, const Sched& sc, ui
 // DENSE: the launch is a dense expert (p.dense_rows > 0).  The code is the
 // same; the separate instantiation keeps the routed and dense launches apart
 // in kernel traces.
-template <bool FC1, int WF, int TM, bool DENSE>
+// EPI (mx_linear on FC2): rows of A and out are permuted rows, finished by the
+// epilogue; a dense or grouped launch alike.
+template <bool FC1, int WF, int TM, bool DENSE, bool EPI>
 __global__ __launch_bounds__(kThreads, 1) void k_fc_tiled(FcArgs p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Lds<WF, TM>::TOTAL];
   Sched sc;
@@ -602,20 +615,27 @@ __global__ __launch_bounds__(kThreads, 1) void k_fc_tiled(FcArgs p) {
   sc.total = sc.my_items * sc.nk;  // (item, stage) steps of this workgroup
   if (sc.total == 0) return;
   const int wv = threadIdx.x >> 6;
-  if (wv < kComputeWaves) multiply_role<FC1, WF, TM>(p, sc, smem);
-  else if (wv < kWaveB) activation_role<FC1, WF, TM>(p, sc, smem);
-  else weight_role<FC1, WF, TM>(p, sc, smem);
+  if (wv < kComputeWaves) multiply_role<FC1, WF, TM, EPI>(p, sc, smem);
+  else if (wv < kWaveB) activation_role<FC1, WF, TM, EPI>(p, sc, smem);
+  else weight_role<FC1, WF, TM, EPI>(p, sc, smem);
 }
 
 template <bool FC1, int WF>
 static hipError_t launch_tiled_t(const FcArgs& p, int rows, int grid, hipStream_t st) {
   const bool dense = p.dense_rows > 0;
+  if constexpr (!FC1) {
+    if (p.linear) {
+      if (rows == kTiledRowsLow) k_fc_tiled<false, WF, kTiledRowsLow, false, true><<<grid, kThreads, 0, st>>>(p);
+      else k_fc_tiled<false, WF, kTiledRows, false, true><<<grid, kThreads, 0, st>>>(p);
+      return hipGetLastError();
+    }
+  }
   if (rows == kTiledRowsLow) {
-    if (dense) k_fc_tiled<FC1, WF, kTiledRowsLow, true><<<grid, kThreads, 0, st>>>(p);
-    else k_fc_tiled<FC1, WF, kTiledRowsLow, false><<<grid, kThreads, 0, st>>>(p);
+    if (dense) k_fc_tiled<FC1, WF, kTiledRowsLow, true, false><<<grid, kThreads, 0, st>>>(p);
+    else k_fc_tiled<FC1, WF, kTiledRowsLow, false, false><<<grid, kThreads, 0, st>>>(p);
   } else {
-    if (dense) k_fc_tiled<FC1, WF, kTiledRows, true><<<grid, kThreads, 0, st>>>(p);
-    else k_fc_tiled<FC1, WF, kTiledRows, false><<<grid, kThreads, 0, st>>>(p);
+    if (dense) k_fc_tiled<FC1, WF, kTiledRows, true, false><<<grid, kThreads, 0, st>>>(p);
+    else k_fc_tiled<FC1, WF, kTiledRows, false, false><<<grid, kThreads, 0, st>>>(p);
   }
   return hipGetLastError();
 }

@@ -45,6 +45,7 @@
 #include <hip/hip_runtime.h>
 
 #include "copy_ring.h"
+#include "epilogue.h"
 #include "gemm.h"
 #include "mx_device.h"
 #include "wide_count.h"
@@ -217,7 +218,9 @@ struct CopyCount : WideCopyCount<NS, C> {
 // the row tables.  A row table is read only after the per-step waits have
 // covered the copy that wrote it: the table of item i goes out before item
 // i-1's first code stage, which every wait from step nk*i - nk + 1 on includes.
-template <bool FC1>
+// EPI (mx_linear on FC2): rows of A and out are permuted rows and there are no
+// row tables (the waits then allow fewer copies in flight than there could be)
+template <bool FC1, bool EPI>
 struct ACopier {
   using Count = CopyCount<kAStages, kACodeCopies>;
   uint32_t src[kACodeCopies];  // FC1 routed: byte offsets into the activations (< 4 GiB)
@@ -257,7 +260,7 @@ struct ACopier {
     }
     if (ls == 0) {
       // the next item's table goes out before this item's first stage
-      if (p.dense_rows == 0 && li + 1 < sc.my_items)
+      if (!EPI && p.dense_rows == 0 && li + 1 < sc.my_items)
         copy_table(p, item_geom(p, sc, li + 1), lds0 + L_TBL + ((li + 1) % kTables) * TABLE, wm == 0);
       const ItemGeom it = item_geom(p, sc, li);
       nb = it.nb;
@@ -309,7 +312,7 @@ struct ACopier {
   }
 
   __device__ __forceinline__ void prologue(const FcArgs& p, const Sched& sc, const uint8_t* smem, int wm) {
-    if (p.dense_rows == 0) {
+    if (!EPI && p.dense_rows == 0) {
       copy_table(p, item_geom(p, sc, 0), lds_addr(smem) + L_TBL, wm == 0);
       wait_vm_lgkm0<0>();
     }
@@ -328,7 +331,8 @@ struct ACopier {
 // The weight stream of wave (wm, 1): codes of B-tile rows [64 wm, 64 wm + 64)
 // (1-KB copy t = 4 wm + i holds rows 16t .. 16t+15) and scale groups of rows
 // 64 wm + lane.
-template <bool FC1>
+// EPI: rows past N repeat the last one (their columns are not stored).
+template <bool FC1, bool EPI>
 struct BCopier {
   using Count = CopyCount<kBStages, kBCodeCopies>;
   int nb, expert;  // of the code cursor's item; per-lane offsets are recomputed at each issue
@@ -336,6 +340,7 @@ struct BCopier {
   int gli = 0, gls = 0;  // scale-group cursor
   int gitem = -1;        // item whose scale-row base is held in gbase
   const uint8_t* gbase;
+  int grow;              // its first scale row
 
   // First weight row of the wave's 64 B-tile rows [64 wm, 64 wm + 64): FC1 takes
   // gate rows (even wm) or the matching up rows (odd wm) of h columns
@@ -359,11 +364,21 @@ struct BCopier {
       expert = it.expert;
     }
     const int ks = k_step(sc, nb, ls);
+    const uint32_t base = lds_addr(smem) + L_B + (s % kBStages) * B_STAGE;
+    if (EPI) {
+      const int r0 = (int)row0(p, nb, wm), rb = min(r0, p.N - 1);
+      const uint8_t* wb = p.w + (int64_t)expert * p.w_estride + (int64_t)rb * (p.K / 2) + ks * B_ROW;
+      const uint32_t c16 = 16 * ((lane & 3) ^ ((lane >> 3) & 3));
+#pragma unroll
+      for (int i = 0; i < kBCodeCopies; ++i)
+        lds_copy16_s(wb, (uint32_t)(min(r0 + 16 * i + (lane >> 2), p.N - 1) - rb) * (uint32_t)(p.K / 2) + c16,
+                     base + 1024 * (kBCodeCopies * wm + i));
+      return;
+    }
     const uint8_t* w = p.w + (int64_t)expert * p.w_estride + row0(p, nb, wm) * (p.K / 2) + ks * B_ROW;
     // copy i: rows 16i + lane/4 of the wave's 64, slot lane%4 receiving chunk
     // (lane%4) ^ ((row/2)%4) = (lane%4) ^ ((lane/8)%4)
     const uint32_t lo = (uint32_t)(lane >> 2) * (uint32_t)(p.K / 2) + 16 * ((lane & 3) ^ ((lane >> 3) & 3));
-    const uint32_t base = lds_addr(smem) + L_B + (s % kBStages) * B_STAGE;
 #pragma unroll
     for (int i = 0; i < kBCodeCopies; ++i)
       lds_copy16_s(w, lo + (uint32_t)(16 * i) * (uint32_t)(p.K / 2), base + 1024 * (kBCodeCopies * wm + i));
@@ -380,10 +395,12 @@ struct BCopier {
     }
     if (li != gitem) {
       const ItemGeom it = item_geom(p, sc, li);
-      gbase = p.w_scale + (int64_t)it.expert * p.ws_estride + row0(p, it.nb, wm) * (p.K / 32);
+      // the wave's 64 rows: the first of them within N
+      grow = EPI ? min((int)row0(p, it.nb, wm), p.N - 1) : (int)row0(p, it.nb, wm);
+      gbase = p.w_scale + (int64_t)it.expert * p.ws_estride + (int64_t)grow * (p.K / 32);
       gitem = li;
     }
-    lds_copy16_s(gbase + 4 * ls, (uint32_t)lane * (uint32_t)(p.K / 32), lds_addr(smem) + L_BS + (G % 2) * BS_GROUP + 1024 * wm);
+    lds_copy16_s(gbase + 4 * ls, (uint32_t)(EPI ? min(lane, p.N - 1 - grow) : lane) * (uint32_t)(p.K / 32), lds_addr(smem) + L_BS + (G % 2) * BS_GROUP + 1024 * wm);
   }
 
   __device__ __forceinline__ void prologue(const FcArgs& p, const Sched& sc, const uint8_t* smem, int wm) {
@@ -490,7 +507,7 @@ __device__ __forceinline__ void item_steps(const FcArgs& p, const Sched& sc, v4f
   }
 }
 
-template <bool FC1, int ACT, class Copier>
+template <bool FC1, int ACT, bool EPI, class Copier>
 __device__ __forceinline__ void wave_main(const FcArgs& p, const Sched& sc, uint8_t* smem, int wm, int wn) {
   const int lane = threadIdx.x & 63;
   const int l16 = lane & 15, g = lane >> 4;
@@ -535,6 +552,16 @@ __device__ __forceinline__ void wave_main(const FcArgs& p, const Sched& sc, uint
 #pragma unroll
     for (int m = 0; m < kSubs; ++m) {
       if (m >= nm) continue;
+      if constexpr (EPI) {
+        // a 16-row sub-block, four column tiles at a time: their factors and
+        // residuals are all requested before the first is used
+#pragma unroll
+        for (int n0 = 0; n0 < kTiles; n0 += 4)
+          epi_block<4, 4, ACT>(p, it.expert, it.p0 + 16 * (wm + 4 * m) + 4 * g, it.p0 + it.rows,
+                               it.nb * TBN + 128 * wn + 16 * n0 + l16, 16,
+                               [&](int i, int n) { return acc[m][n0 + n][i]; });
+        continue;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = 16 * (wm + 4 * m) + 4 * g + i;
@@ -589,7 +616,8 @@ __device__ __forceinline__ void wave_main(const FcArgs& p, const Sched& sc, uint
   wait_vm_lgkm0<0>();
 }
 
-template <bool FC1, int ACT>
+// ACT: the gated activation (FC1) or, with EPI, the epilogue's function
+template <bool FC1, int ACT, bool EPI>
 __global__ __launch_bounds__(kThreads, 1) void k_fc_wide(FcArgs p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[L_TOTAL];
   Sched sc;
@@ -609,8 +637,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_fc_wide(FcArgs p) {
   // the wave index is uniform; saying so keeps everything derived from it
   // (copy cursors, sub-block counts, branches) in scalar registers
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (w < 4) wave_main<FC1, ACT, ACopier<FC1>>(p, sc, smem, w, 0);
-  else wave_main<FC1, ACT, BCopier<FC1>>(p, sc, smem, w - 4, 1);
+  if (w < 4) wave_main<FC1, ACT, EPI, ACopier<FC1, EPI>>(p, sc, smem, w, 0);
+  else wave_main<FC1, ACT, EPI, BCopier<FC1, EPI>>(p, sc, smem, w - 4, 1);
 }
 
 }  // namespace
@@ -618,10 +646,19 @@ __global__ __launch_bounds__(kThreads, 1) void k_fc_wide(FcArgs p) {
 hipError_t launch_fc_wide(const FcArgs& p, bool fc1, int grid, hipStream_t st) {
   if (grid < 8) grid = 8;
   grid &= ~7;
-  if (!fc1) k_fc_wide<false, MOE_FN_SILU><<<grid, kThreads, 0, st>>>(p);
-  else if (p.act_fn == MOE_FN_RELU2) k_fc_wide<true, MOE_FN_RELU2><<<grid, kThreads, 0, st>>>(p);
-  else if (p.act_fn == MOE_FN_SWIGLU_OAI) k_fc_wide<true, MOE_FN_SWIGLU_OAI><<<grid, kThreads, 0, st>>>(p);
-  else k_fc_wide<true, MOE_FN_SILU><<<grid, kThreads, 0, st>>>(p);
+  if (p.linear) {
+    switch (p.epi.fn) {
+      case MX_FN_SILU: k_fc_wide<false, MX_FN_SILU, true><<<grid, kThreads, 0, st>>>(p); break;
+      case MX_FN_GELU: k_fc_wide<false, MX_FN_GELU, true><<<grid, kThreads, 0, st>>>(p); break;
+      case MX_FN_RELU2: k_fc_wide<false, MX_FN_RELU2, true><<<grid, kThreads, 0, st>>>(p); break;
+      default: k_fc_wide<false, MX_FN_NONE, true><<<grid, kThreads, 0, st>>>(p);
+    }
+    return hipGetLastError();
+  }
+  if (!fc1) k_fc_wide<false, MOE_FN_SILU, false><<<grid, kThreads, 0, st>>>(p);
+  else if (p.act_fn == MOE_FN_RELU2) k_fc_wide<true, MOE_FN_RELU2, false><<<grid, kThreads, 0, st>>>(p);
+  else if (p.act_fn == MOE_FN_SWIGLU_OAI) k_fc_wide<true, MOE_FN_SWIGLU_OAI, false><<<grid, kThreads, 0, st>>>(p);
+  else k_fc_wide<true, MOE_FN_SILU, false><<<grid, kThreads, 0, st>>>(p);
   return hipGetLastError();
 }
 

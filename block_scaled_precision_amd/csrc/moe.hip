@@ -578,7 +578,8 @@ struct LinearPlan {
   Fc kind;
   int rows;        // M-tile height
   int max_tiles;   // grouped: room of the tile list
-  size_t quant, tiles, ntiles, total;
+  int ksplit;      // dense, few rows: K ranges (0 or 1: none)
+  size_t quant, tiles, ntiles, part, total;
 };
 
 static bool linear_sizes_ok(const mx_linear_problem_t& p) {
@@ -592,10 +593,40 @@ static bool linear_supported(const mx_linear_problem_t& p) {
          (double)p.M * p.N * p.K <= 4503599627370496.0;
 }
 
-static LinearPlan linear_plan(const mx_linear_problem_t& p, bool has_a_scale) {
-  LinearPlan f = {};
+// Average rows per group (one group: all of them), rounded up.
+static int64_t linear_rows(const mx_linear_problem_t& p) {
+  return p.groups > 0 ? (p.M + p.groups - 1) / p.groups : p.M;
+}
+
+// The kernel of a call, by the layer's own thresholds on the average rows per
+// group; the epilogue variants mask columns past N, so any N does.
+static void linear_kind(const mx_linear_problem_t& p, LinearPlan& f) {
+  const int64_t avg = linear_rows(p);
+  const bool e2m1 = p.w_fmt == MX_E2M1;
   f.kind = Fc::kStream;
   f.rows = kStreamRows;
+  if (p.act == MOE_ACT_MXFP8) {
+    if (avg < kTiledMinRowsPerExpert || p.K % kTiledKMultiple) return;
+    // the wide kernel's 32-bit offsets into A
+    if (e2m1 && p.K >= 1024 && p.N > kWideCols / 2 && (double)p.M * p.K < 4294967296.0) {
+      f.kind = Fc::kWide;
+      f.rows = kTiledRows;
+    } else {
+      f.kind = Fc::kTiled;
+      f.rows = avg <= kTiledLowMaxRowsPerExpert ? kTiledRowsLow : kTiledRows;
+    }
+  } else if (e2m1 && avg >= kMidMinRowsPerExpert && p.K % kMidK == 0) {
+    f.kind = Fc::kMid;
+    f.rows = avg >= kMidHighMinRowsPerExpert ? kMidRowsHigh : kMidRows;
+  } else if (e2m1 && p.K % kSmallK == 0) {
+    f.kind = Fc::kSmall;
+  }
+}
+
+static LinearPlan linear_plan(const mx_linear_problem_t& p, bool has_a_scale) {
+  LinearPlan f = {};
+  linear_kind(p, f);
+  if (f.kind == Fc::kSmall && p.groups == 0) f.ksplit = dense_ksplit(p.M, p.N, p.K, p.act, p.w_fmt);
   if (p.groups > 0) f.max_tiles = (int)(p.M / f.rows + (p.M < p.groups ? p.M : p.groups));
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -608,6 +639,7 @@ static LinearPlan linear_plan(const mx_linear_problem_t& p, bool has_a_scale) {
     f.tiles = take((size_t)f.max_tiles * sizeof(Tile));
     f.ntiles = take(4);
   }
+  if (f.ksplit > 1) f.part = take((size_t)f.ksplit * p.M * p.N * 4);
   f.total = o;
   return f;
 }
@@ -685,7 +717,23 @@ extern "C" moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_
   g.nchunks = (int)((N + cols - 1) / cols);
   g.obuf = (uint16_t*)t->out;
   const int wf = p->w_fmt == MX_E2M1 ? 1 : 2;
-  return launch_fc_stream(g, false, mx, wf, stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+  const int cus = device_cus();
+  hipError_t e;
+  switch (f.kind) {
+    case Fc::kSmall:
+      if (f.ksplit > 1) {
+        g.ksplit = f.ksplit;
+        g.part = (float*)(ws + f.part);
+      }
+      e = launch_fc_small(g, false, cus, stream);
+      if (e == hipSuccess && g.ksplit > 1) e = launch_splitk_epilogue(g, stream);
+      break;
+    case Fc::kMid: e = launch_fc_mid(g, false, f.rows, cus, stream); break;
+    case Fc::kWide: e = launch_fc_wide(g, false, cus, stream); break;
+    case Fc::kTiled: e = launch_fc_tiled(g, false, wf, f.rows, cus, stream); break;
+    default: e = launch_fc_stream(g, false, mx, wf, stream);
+  }
+  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 extern "C" size_t moe_fused_workspace_offset(const moe_problem_t* p, moe_ws_part_t part) {
