@@ -1,12 +1,21 @@
 // Epilogue of mx_linear, shared by the FC2 kernels it runs on:
 //   out[m, n] = bf16_RNE(fn(acc + bias[group, n]) * mul[m, n] + residual[m, n])
-// in fp32 on the accumulators, before their one rounding.  A kernel's lanes
-// hold accumulators of fixed columns, so each column's bias is loaded once per
-// item; mul, residual and out are bf16 [M, N].  An element of mul and residual
-// is read by the thread that writes that element of out, and before it does,
-// so either may be out itself.
+// in fp32 on the accumulators, before their one rounding.  mul, residual and out
+// are bf16 [M, N].
+//
+// The kernels multiply with the operands swapped (weights as the MFMA's first),
+// so a lane's four accumulator elements are neighbouring columns of one row, and
+// lay out the weight rows of two column tiles so that a lane's eight elements
+// are eight neighbouring columns (epi_row16, epi_row32): one 16-byte access per
+// operand instead of eight 2-byte ones.  (With 2-byte accesses the epilogue of
+// 8192 x 4096 outputs with a residual took about 90 us more than the product.)
+// N % 8 == 0, so a piece of eight columns lies within N or behind it as a whole.
+//
+// A piece of mul and residual is read by the thread that writes that piece of
+// out, and before it does, so either may be out itself.
 #pragma once
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "gemm.h"
@@ -14,16 +23,35 @@
 
 namespace moe_mx {
 
-// bias of column n (< N) of a group, 0 without one
-__device__ __forceinline__ float epi_bias(const FcArgs& p, int group, int n) {
-  if (!p.epi.bias) return 0.f;
-  const int64_t i = (int64_t)group * p.N + n;
-  return p.epi.bias_bf16 ? bf16_bits_to_f32(((const uint16_t*)p.epi.bias)[i]) : ((const float*)p.epi.bias)[i];
+// Weight row (column of out) held at row j of a tile pair.  16 x 16 MFMAs: row
+// 4g + i of tile t in a pair (32 rows) is column 8g + 4t + i; 32 x 32 MFMAs: row
+// 8q + 4h + i of tile t in a pair (64 rows) is column 16q + 8h + 4t + i.
+__device__ __forceinline__ int epi_row16(int j) { return (j & ~31) | ((j >> 2) & 3) << 3 | ((j >> 4) & 1) << 2 | (j & 3); }
+__device__ __forceinline__ int epi_row32(int j) {
+  return (j & ~63) | ((j >> 3) & 3) << 4 | ((j >> 2) & 1) << 3 | ((j >> 5) & 1) << 2 | (j & 3);
+}
+
+// The epilogue's operands, read from the kernel arguments (FcArgs, the only one)
+// where an epilogue begins: held from the start of a persistent kernel they would
+// take scalar registers from its step loop.
+__device__ __forceinline__ Epilogue epi_load() {
+  const __attribute__((address_space(4))) char* args =
+      (const __attribute__((address_space(4))) char*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(args));
+  return *(const Epilogue*)(args + offsetof(FcArgs, epi));
+}
+
+// The lane, opaque to the compiler: what an epilogue derives from it is computed
+// there, not ahead of the step loop, whose registers it would take.
+__device__ __forceinline__ int epi_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
 }
 
 // SiLU through t = exp(-|v|) <= 1, so that the tail of negative v does not pass
-// through an overflowing exp(-v); erfc rather than 1 + erf: for negative v the sum would cancel, leaving an
-// error relative to v instead of to the result
+// through an overflowing exp(-v); erfc rather than 1 + erf: for negative v the
+// sum would cancel, leaving an error relative to v instead of to the result
 __device__ __forceinline__ float epi_fn(int fn, float v) {
   switch (fn) {
     case MX_FN_SILU: {
@@ -39,47 +67,124 @@ __device__ __forceinline__ float epi_fn(int fn, float v) {
   }
 }
 
-// out[o] from v = acc + bias (o: element offset of (m, n))
-__device__ __forceinline__ void epi_store(const FcArgs& p, int64_t o, float v) {
-  v = epi_fn(p.epi.fn, v);
-  if (p.epi.mul) v *= bf16_bits_to_f32(p.epi.mul[o]);
-  if (p.epi.residual) v += bf16_bits_to_f32(p.epi.residual[o]);
-  ((__bf16*)p.obuf)[o] = (__bf16)v;
+// bias of columns [n, n + 8) (n < N) of a group, 0 without one
+struct EpiBias {
+  float v[8];
+};
+__device__ __forceinline__ EpiBias epi_bias(const Epilogue& e, int N, int group, int n) {
+  EpiBias b;
+  const int64_t i = (int64_t)group * N + n;
+  if (e.bias_kind == kBiasF32) {
+    const float4* p = (const float4*)((const float*)e.bias + i);
+    const float4 lo = p[0], hi = p[1];
+    b = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  } else if (e.bias_kind == kBiasBf16) {
+    const uint4 d = *(const uint4*)((const uint16_t*)e.bias + i);
+    const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      b.v[2 * q] = __uint_as_float(w[q] << 16);
+      b.v[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+    }
+  } else {
+    // none, or not on a 16-byte address
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      b.v[q] = e.bias_kind == kBiasNone ? 0.f
+               : e.bias_kind == kBiasF32Any ? ((const float*)e.bias)[i + q]
+                                            : bf16_bits_to_f32(((const uint16_t*)e.bias)[i + q]);
+  }
+  return b;
 }
 
-// R rows from row0 (rows from row_end on: none) by C columns col0, col0 +
-// cstep, ... of out, v(i, n) their accumulators.  The block's second factors and
-// residuals are loaded before its first store: a store may alias them, so the
-// loads of a row could not pass the stores of the row before, and each would
-// cost a memory latency.  FN: the function, or -1 to take it from p.
-template <int R, int C, int FN = -1, class V>
-__device__ __forceinline__ void epi_block(const FcArgs& p, int group, int64_t row0, int64_t row_end, int col0,
-                                          int cstep, V v) {
-  float bias[C];
-  uint16_t mu[R][C], re[R][C];
+// The second factors and residuals of the piece at element offset o
+struct EpiIn {
+  uint4 mul, residual;
+};
+__device__ __forceinline__ EpiIn epi_in(const Epilogue& e, int64_t o) {
+  EpiIn in = {};
+  if (e.mul) in.mul = *(const uint4*)(e.mul + o);
+  if (e.residual) in.residual = *(const uint4*)(e.residual + o);
+  return in;
+}
+
+// The piece at o from v = accumulators + bias.  FN: the function, or -1 for e.fn.
+template <int FN = -1>
+__device__ __forceinline__ void epi_store(const Epilogue& e, int64_t o, const EpiIn& in, const float (&v)[8]) {
+  const uint32_t mu[4] = {in.mul.x, in.mul.y, in.mul.z, in.mul.w};
+  const uint32_t re[4] = {in.residual.x, in.residual.y, in.residual.z, in.residual.w};
+  uint32_t w[4];
 #pragma unroll
-  for (int n = 0; n < C; ++n) bias[n] = col0 + n * cstep < p.N ? epi_bias(p, group, col0 + n * cstep) : 0.f;
+  for (int q = 0; q < 4; ++q) {
+    float x[2];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+    for (int h = 0; h < 2; ++h) {
+      x[h] = epi_fn(FN < 0 ? e.fn : FN, v[2 * q + h]);
+      if (e.mul) x[h] *= __uint_as_float(h ? mu[q] & 0xffff0000u : mu[q] << 16);
+      if (e.residual) x[h] += __uint_as_float(h ? re[q] & 0xffff0000u : re[q] << 16);
+    }
+    const v2bf o2 = {(__bf16)x[0], (__bf16)x[1]};
+    __builtin_memcpy(&w[q], &o2, 4);
+  }
+  *(uint4*)(e.out + o) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// R pieces of one row of out (row < row_end, else nothing), the first at column
+// col0 and the others cstep apart; acc(q): the accumulators of piece q.  All
+// loads go out before the first store, which they could not pass (out may be mul
+// or residual).
+template <int R, int FN = -1, class Acc>
+__device__ __forceinline__ void epi_row(const Epilogue& e, int N, int64_t row, int64_t row_end, int col0, int cstep,
+                                        const EpiBias (&bias)[R], Acc acc) {
+  if (row >= row_end) return;
+  EpiIn in[R];
 #pragma unroll
-    for (int n = 0; n < C; ++n) {
-      const int col = col0 + n * cstep;
-      const bool in = row0 + i < row_end && col < p.N;
-      const int64_t o = (row0 + i) * p.N + col;
-      mu[i][n] = p.epi.mul && in ? p.epi.mul[o] : 0;
-      re[i][n] = p.epi.residual && in ? p.epi.residual[o] : 0;
+  for (int q = 0; q < R; ++q)
+    if (col0 + q * cstep < N) in[q] = epi_in(e, row * N + col0 + q * cstep);
+#pragma unroll
+  for (int q = 0; q < R; ++q)
+    if (col0 + q * cstep < N) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = acc(q, i) + bias[q].v[i];
+      epi_store<FN>(e, row * N + col0 + q * cstep, in[q], v);
+    }
+}
+template <int R>
+__device__ __forceinline__ void epi_biases(const Epilogue& e, int N, int group, int col0, int cstep,
+                                           EpiBias (&bias)[R]) {
+#pragma unroll
+  for (int q = 0; q < R; ++q)
+    if (col0 + q * cstep < N) bias[q] = epi_bias(e, N, group, col0 + q * cstep);
+}
+
+
+// P pieces whose accumulators started from the bias, `C` at a time: the loads of
+// a chunk go out before the stores of the chunk before.  at(q): element offset of
+// piece q, or -1 for one outside; acc(q, i): its accumulators.
+template <int P, int C, int FN, class At, class Acc>
+__device__ __forceinline__ void epi_pieces(const Epilogue& e, At at, Acc acc) {
+  static_assert(P % C == 0, "whole chunks");
+  EpiIn in[2][C];
+#pragma unroll
+  for (int q = 0; q < C; ++q)
+    if (at(q) >= 0) in[0][q] = epi_in(e, at(q));
+#pragma unroll
+  for (int c = 0; c < P / C; ++c) {
+    if (c + 1 < P / C) {
+#pragma unroll
+      for (int q = 0; q < C; ++q)
+        if (at((c + 1) * C + q) >= 0) in[(c + 1) & 1][q] = epi_in(e, at((c + 1) * C + q));
     }
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+    for (int q = 0; q < C; ++q) {
+      const int64_t o = at(c * C + q);
+      float v[8];
 #pragma unroll
-    for (int n = 0; n < C; ++n) {
-      const int col = col0 + n * cstep;
-      if (row0 + i >= row_end || col >= p.N) continue;
-      float x = epi_fn(FN < 0 ? p.epi.fn : FN, v(i, n) + bias[n]);
-      if (p.epi.mul) x *= bf16_bits_to_f32(mu[i][n]);
-      if (p.epi.residual) x += bf16_bits_to_f32(re[i][n]);
-      ((__bf16*)p.obuf)[(row0 + i) * p.N + col] = (__bf16)x;
+      for (int i = 0; i < 8; ++i) v[i] = acc(c * C + q, i);
+      if (o >= 0) epi_store<FN>(e, o, in[c & 1][q], v);
     }
+  }
 }
 
 }  // namespace moe_mx

@@ -7,13 +7,17 @@
 
 namespace moe_mx {
 
+// Bias of mx_linear: none, fp32 or bf16 rows on 16-byte addresses, or on any
+constexpr int kBiasNone = 0, kBiasF32 = 1, kBiasBf16 = 2, kBiasF32Any = 3, kBiasBf16Any = 4;
+
 // Epilogue operands of mx_linear (epilogue.h); null: absent
 struct Epilogue {
-  const void* bias;          // [groups, N] fp32, or bf16 with bias_bf16
-  int bias_bf16;
+  const void* bias;          // [groups, N] as bias_kind says
+  int bias_kind;             // kBias*
   int fn;                    // mx_fn_t
   const uint16_t* mul;       // [M, N] bf16
   const uint16_t* residual;  // [M, N] bf16
+  __bf16* out;               // [M, N]
 };
 
 struct FcArgs {
@@ -127,7 +131,7 @@ hipError_t launch_fc_small_routed(const FcArgs& p, int grid, hipStream_t st);
 hipError_t launch_splitk_reduce(const float* part, int ksplit, int64_t n4, float alpha, uint16_t* y,
                                 hipStream_t st);
 
-// mx_linear: out = epilogue of the sum over s of p.part[s] (N % 4 == 0, dense)
+// mx_linear: out = epilogue of the sum over s of p.part[s] (N % 8 == 0, dense)
 hipError_t launch_splitk_epilogue(const FcArgs& p, hipStream_t st);
 
 // Mid-M variant for bf16 activations and E2M1 weights when experts see many

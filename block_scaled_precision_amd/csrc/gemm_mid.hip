@@ -129,7 +129,7 @@ __device__ __forceinline__ MGeom m_geom(const FcArgs& p, const MSched& sc, int l
 // past N repeat the last one (their columns are not stored)
 template <bool FC1, bool EPI>
 __device__ __forceinline__ int64_t m_wrow(const FcArgs& p, int nb, int jr) {
-  if (EPI) return min(nb * MBN + jr, p.N - 1);
+  if (EPI) return min(nb * MBN + epi_row16(jr), p.N - 1);
   if (FC1) return jr < MBN / 2 ? (int64_t)nb * (MBN / 2) + jr : (int64_t)p.N + nb * (MBN / 2) + jr - MBN / 2;
   return (int64_t)nb * MBN + jr;
 }
@@ -158,7 +158,7 @@ __device__ __forceinline__ int m_btile(int wc, int n) {
 }
 
 // one stage of one multiply wave: acc[m][n] += A(sub-tile m) * B(column tile n)^T
-template <bool FC1>
+template <bool FC1, bool EPI>
 __device__ __forceinline__ void m_stage(const uint8_t* st, const uint8_t* sg, int wr, int wc, int r16, int g,
                                         v4f (&acc)[2][8]) {
   const uint8_t* as = st + S_B;
@@ -186,7 +186,8 @@ __device__ __forceinline__ void m_stage(const uint8_t* st, const uint8_t* sg, in
       for (int m = 0; m < 2; ++m) {
         v8bf av;
         __builtin_memcpy(&av, &a[m][kq], 16);
-        acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv, acc[m][n], 0, 0, 0);
+        acc[m][n] = EPI ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv, av, acc[m][n], 0, 0, 0)
+                        : __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv, acc[m][n], 0, 0, 0);
       }
     }
   }
@@ -231,7 +232,7 @@ __device__ __forceinline__ void mid_multiply(const FcArgs& p, const MSched& sc, 
       const uint8_t* st = smem + (gidx % L::NSTG) * L::S_STAGE;
       // scale byte of row jr, this stage, MX block g: sg[GROW * jr]
       const uint8_t* sg = smem + L::L_SG + ((gidx / GS) % NG) * G_BYTES + (gidx % GS) * SROW + g;
-      m_stage<FC1>(st, sg, wr, wc, r16, g, acc);
+      m_stage<FC1, EPI>(st, sg, wr, wc, r16, g, acc);
     }
     if (++cs < sc.nk) continue;
 
@@ -251,15 +252,15 @@ __device__ __forceinline__ void mid_multiply(const FcArgs& p, const MSched& sc, 
             }
           }
       } else if (EPI) {
-        // two 16-row sub-tiles, four columns at a time: their factors and
-        // residuals are all requested before the first is used
+        const Epilogue e = epi_load();
+        // the lane holds rows 32wr + 16m + r16, eight columns of each tile pair
+        const int col = it.nb * MBN + 128 * wc + 8 * g;
+        EpiBias bias[4];
+        epi_biases(e, p.N, it.expert, col, 32, bias);
 #pragma unroll
         for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int n0 = 0; n0 < 8; n0 += 4)
-            epi_block<4, 4>(p, it.expert, it.p0 + 32 * wr + 16 * m + 4 * g, it.p0 + it.rows,
-                            it.nb * MBN + 128 * wc + 16 * n0 + r16, 16,
-                            [&](int i, int n) { return acc[m][n0 + n][i]; });
+          epi_row(e, p.N, it.p0 + 32 * wr + 16 * m + r16, it.p0 + it.rows, col, 32, bias,
+                  [&](int q, int i) { return acc[m][2 * q + (i >> 2)][i & 3]; });
       } else {
         // row metadata by plain per-lane loads (the multiply waves issue no
         // copies, so their memory counter holds nothing else)

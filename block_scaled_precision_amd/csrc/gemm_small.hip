@@ -137,7 +137,7 @@ __device__ __forceinline__ SGeom s_geom(const FcArgs& p, const SSched& sc, int l
 // columns are not stored)
 template <bool FC1, bool EPI>
 __device__ __forceinline__ int64_t s_wrow(const FcArgs& p, int nb, int jr) {
-  if (EPI) return min(nb * SBN + jr, p.N - 1);
+  if (EPI) return min(nb * SBN + epi_row16(jr), p.N - 1);
   if (FC1) return jr < SBN / 2 ? (int64_t)nb * (SBN / 2) + jr : (int64_t)p.N + nb * (SBN / 2) + jr - SBN / 2;
   return (int64_t)nb * SBN + jr;
 }
@@ -221,7 +221,8 @@ __device__ __forceinline__ void small_multiply(const FcArgs& p, const SSched& sc
           const v8bf bv = {q0[0], q0[1], q1[0], q1[1], q2[0], q2[1], q3[0], q3[1]};
           v8bf av;
           __builtin_memcpy(&av, &a[4 * blk + kq], 16);
-          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv, acc[n], 0, 0, 0);
+          acc[n] = EPI ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv, av, acc[n], 0, 0, 0)
+                       : __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv, acc[n], 0, 0, 0);
         }
       }
     }
@@ -239,26 +240,31 @@ __device__ __forceinline__ void small_multiply(const FcArgs& p, const SSched& sc
     } else {
       int orow[4];
       float wt[4];
-      if (sc.S > 1) {
+      if (EPI) {
+        // the lane holds row r16, columns 8g .. 8g + 7 of the wave's 32
+        const int col = it.nb * SBN + 32 * w + 8 * g;
+        if (r16 < it.rows && col < p.N) {
+          if (sc.S > 1) {
+            float4* o = (float4*)(p.part + ((int64_t)it.ks * p.dense_rows + it.p0 + r16) * p.N + col);
+            o[0] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
+            o[1] = make_float4(acc[1][0], acc[1][1], acc[1][2], acc[1][3]);
+          } else {
+            const Epilogue e = epi_load();
+            EpiBias bias[1];
+            epi_biases(e, p.N, it.expert, col, 0, bias);
+            epi_row(e, p.N, it.p0 + r16, it.p0 + it.rows, col, 0, bias,
+                    [&](int, int i) { return acc[i >> 2][i & 3]; });
+          }
+        }
+      } else if (sc.S > 1) {
         // split dense GEMM: this K range's unscaled fp32 sums
-        const int col = it.nb * SBN + 32 * w + r16;
-        float* o = p.part + ((int64_t)it.ks * p.dense_rows + it.p0) * p.N + col;
+        float* o = p.part + ((int64_t)it.ks * p.dense_rows + it.p0) * p.N + it.nb * SBN + 32 * w + r16;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (4 * g + i < it.rows) {
-            if (!EPI || col < p.N) o[(int64_t)(4 * g + i) * p.N] = acc[0][i];
-            if (!EPI || col + 16 < p.N) o[(int64_t)(4 * g + i) * p.N + 16] = acc[1][i];
+            o[(int64_t)(4 * g + i) * p.N] = acc[0][i];
+            o[(int64_t)(4 * g + i) * p.N + 16] = acc[1][i];
           }
-        }
-      } else if (EPI) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int col = it.nb * SBN + 32 * w + 16 * n + r16;
-          if (col >= p.N) continue;
-          const float bias = epi_bias(p, it.expert, col);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (4 * g + i < it.rows) epi_store(p, (int64_t)(it.p0 + 4 * g + i) * p.N + col, acc[n][i] + bias);
         }
       } else if (p.dense_rows > 0) {
 #pragma unroll
@@ -557,28 +563,28 @@ __global__ void k_splitk_reduce(const float4* __restrict__ part, int ksplit, int
   y[i] = o;
 }
 
-// The same sums finished by mx_linear's epilogue: 4 neighbouring columns per thread.
-__global__ void k_splitk_epilogue(FcArgs p, int64_t n4) {
+// The same sums finished by mx_linear's epilogue: a piece of 8 columns per thread.
+__global__ __launch_bounds__(64) void k_splitk_epilogue(FcArgs p, int64_t n8) {
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= n4) return;
-  const float4* part = (const float4*)p.part;
-  float4 s = part[i];
-  for (int k = 1; k < p.ksplit; ++k) {
-    const float4 v = part[(int64_t)k * n4 + i];
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
-  }
-  const int col = (int)(4 * i % p.N);
-  const float v[4] = {s.x, s.y, s.z, s.w};
+  if (i >= n8) return;
+  const EpiIn in = epi_in(p.epi, 8 * i);
+  const EpiBias bias = epi_bias(p.epi, p.N, 0, (int)(8 * i % p.N));
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < p.ksplit; ++k) {
+    const float4* v = (const float4*)p.part + 2 * (k * n8 + i);
+    const float4 lo = v[0], hi = v[1];
+    const float a[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-  for (int q = 0; q < 4; ++q) epi_store(p, 4 * i + q, v[q] + epi_bias(p, 0, col + q));
+    for (int q = 0; q < 8; ++q) s[q] += a[q];
+  }
+#pragma unroll
+  for (int q = 0; q < 8; ++q) s[q] += bias.v[q];
+  epi_store(p.epi, 8 * i, in, s);
 }
 
 hipError_t launch_splitk_epilogue(const FcArgs& p, hipStream_t st) {
-  const int64_t n4 = (int64_t)p.dense_rows * p.N / 4;
-  k_splitk_epilogue<<<(unsigned)((n4 + 255) / 256), 256, 0, st>>>(p, n4);
+  const int64_t n8 = (int64_t)p.dense_rows * p.N / 8;
+  k_splitk_epilogue<<<(unsigned)((n8 + 63) / 64), 64, 0, st>>>(p, n8);
   return hipGetLastError();
 }
 

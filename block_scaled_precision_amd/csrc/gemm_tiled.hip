@@ -204,7 +204,7 @@ __device__ __forceinline__ int k_stage(const Sched& sc, int nb, int ls) {
 // repeat the last one (their columns are not stored)
 template <bool FC1, int TN, bool EPI>
 __device__ __forceinline__ int64_t w_row(const FcArgs& p, int nb, int jr) {
-  if (EPI) return min(nb * TN + jr, p.N - 1);
+  if (EPI) return min(nb * TN + epi_row32(jr), p.N - 1);
   if (FC1) return jr < TN / 2 ? (int64_t)nb * (TN / 2) + jr : (int64_t)p.N + nb * (TN / 2) + jr - TN / 2;
   return (int64_t)nb * TN + jr;
 }
@@ -215,7 +215,8 @@ __device__ __forceinline__ int64_t w_row(const FcArgs& p, int nb, int jr) {
 // wm + WM*m of the tile times the wave's two 32-column B tiles.  `ags`
 // and `bgs` point at the stage's scale words in its scale group buffers (row
 // r's word at 16 r).
-template <int WF, int TM, int NM>
+// SWAP: the weights are the MFMA's first operand (mx_linear).
+template <int WF, int TM, int NM, bool SWAP>
 __device__ __forceinline__ void compute_stage(v16f (&acc)[Grid<TM>::MAX_SUB][2], const uint8_t* as, const uint8_t* bs,
                                               const uint8_t* ags, const uint8_t* bgs, int wm, int brow0, int brow1) {
   using BL = BLay<WF, TM>;
@@ -271,10 +272,28 @@ __device__ __forceinline__ void compute_stage(v16f (&acc)[Grid<TM>::MAX_SUB][2],
       const int asc = (int)((asw[m] >> sh) & 0xffu);
 #pragma unroll
       for (int n = 0; n < 2; ++n)
-        acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av[kk][m], bv[kk][n], acc[m][n], 0,
-                                                                    Fmt<WF>::MFMA, 0, asc, 0,
-                                                                    (int)((bsw[n] >> sh) & 0xffu));
+        acc[m][n] = SWAP ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bv[kk][n], av[kk][m], acc[m][n],
+                                                                           Fmt<WF>::MFMA, 0, 0,
+                                                                           (int)((bsw[n] >> sh) & 0xffu), 0, asc)
+                         : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av[kk][m], bv[kk][n], acc[m][n], 0,
+                                                                           Fmt<WF>::MFMA, 0, asc, 0,
+                                                                           (int)((bsw[n] >> sh) & 0xffu));
     }
+  }
+}
+
+// mx_linear: the accumulators of an item start from its bias; the lane holds
+// eight columns of each of four pieces, the first at column col.
+template <int SUBS>
+__device__ __forceinline__ void bias_acc(v16f (&acc)[SUBS][2], int N, int expert, int col) {
+  const Epilogue e = epi_load();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const EpiBias b = epi_bias(e, N, expert, min(col + 16 * q, N - 8));
+#pragma unroll
+    for (int m = 0; m < SUBS; ++m)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[m][i >> 2][4 * q + (i & 3)] = b.v[i];
   }
 }
 
@@ -310,6 +329,7 @@ __device__ __forceinline__ void multiply_role(const FcArgs& p, const Sched& sc, 
   int ci = 0, cs = 0;
   ItemGeom it = item_geom<TM>(p, sc, 0);
   int nm = wave_subs(it.rows);
+  if constexpr (EPI) bias_acc<kMaxSub>(acc, p.N, it.expert, it.nb * TN + 64 * wn + 8 * g);
   for (int gidx = 0; gidx < sc.total; ++gidx) {
     wait_lgkm0();  // this wave's reads of the previous stage are done
     barrier();
@@ -319,10 +339,10 @@ __device__ __forceinline__ void multiply_role(const FcArgs& p, const Sched& sc, 
     const uint8_t* ags = smem + L::AS + gb * AL::GROUP + 4 * q;
     const uint8_t* bgs = smem + L::BS + gb * BL::GROUP + 4 * q;
     switch (nm) {
-      case 4: if constexpr (kMaxSub >= 4) compute_stage<WF, TM, 4>(acc, as, bs, ags, bgs, wm, brow0, brow1); break;
-      case 3: if constexpr (kMaxSub >= 3) compute_stage<WF, TM, 3>(acc, as, bs, ags, bgs, wm, brow0, brow1); break;
-      case 2: if constexpr (kMaxSub >= 2) compute_stage<WF, TM, 2>(acc, as, bs, ags, bgs, wm, brow0, brow1); break;
-      case 1: compute_stage<WF, TM, 1>(acc, as, bs, ags, bgs, wm, brow0, brow1); break;
+      case 4: if constexpr (kMaxSub >= 4) compute_stage<WF, TM, 4, EPI>(acc, as, bs, ags, bgs, wm, brow0, brow1); break;
+      case 3: if constexpr (kMaxSub >= 3) compute_stage<WF, TM, 3, EPI>(acc, as, bs, ags, bgs, wm, brow0, brow1); break;
+      case 2: if constexpr (kMaxSub >= 2) compute_stage<WF, TM, 2, EPI>(acc, as, bs, ags, bgs, wm, brow0, brow1); break;
+      case 1: compute_stage<WF, TM, 1, EPI>(acc, as, bs, ags, bgs, wm, brow0, brow1); break;
       default: break;
     }
     if (++cs < sc.nk) continue;
@@ -335,11 +355,15 @@ __device__ __forceinline__ void multiply_role(const FcArgs& p, const Sched& sc, 
       if (m >= nm) continue;
       const int sbk = wm + G::WM * m;
       if constexpr (EPI) {
-        // four rows of both column tiles at a time
-#pragma unroll
-        for (int i0 = 0; i0 < 16; i0 += 4)
-          epi_block<4, 2>(p, it.expert, it.p0 + 32 * sbk + 2 * i0 + 4 * g, it.p0 + it.rows,
-                          it.nb * TN + 64 * wn + l32, 32, [&](int i, int n) { return acc[m][n][i0 + i]; });
+        // the lane holds row 32sbk + l32, eight columns of each of four pieces
+        const Epilogue e = epi_load();
+        const int col = it.nb * TN + 64 * wn + 8 * g, row = 32 * sbk + l32;
+        epi_pieces<4, 2, -1>(
+            e,
+            [&](int q) -> int64_t {
+              return row < it.rows && col + 16 * q < p.N ? (int64_t)(it.p0 + row) * p.N + col + 16 * q : -1;
+            },
+            [&](int q, int i) { return acc[m][i >> 2][4 * q + (i & 3)]; });
         continue;
       }
 #pragma unroll
@@ -377,16 +401,19 @@ __device__ __forceinline__ void multiply_role(const FcArgs& p, const Sched& sc, 
         }
       }
     }
+    if constexpr (!EPI) {
 #pragma unroll
-    for (int m = 0; m < kMaxSub; ++m)
+      for (int m = 0; m < kMaxSub; ++m)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.f;
+          for (int e = 0; e < 16; ++e) acc[m][n][e] = 0.f;
+    }
     cs = 0;
     if (++ci < sc.my_items) {
       it = item_geom<TM>(p, sc, ci);
       nm = wave_subs(it.rows);
+      if constexpr (EPI) bias_acc<kMaxSub>(acc, p.N, it.expert, it.nb * TN + 64 * wn + 8 * g);
     }
   }
 }

@@ -59,6 +59,10 @@ typedef int v4i_w __attribute__((ext_vector_type(4)));
 __device__ v4f mfma16_f8_f4_w(v8i a, v4i_w b, v4f c, int fa, int fb, int opa, int sa, int opb, int sb)
     __asm("llvm.amdgcn.mfma.scale.f32.16x16x128.f8f6f4.v8i32.v4i32");
 
+// The same with the E2M1 operand first.
+__device__ v4f mfma16_f4_f8_w(v4i_w a, v8i b, v4f c, int fa, int fb, int opa, int sa, int opb, int sb)
+    __asm("llvm.amdgcn.mfma.scale.f32.16x16x128.f8f6f4.v4i32.v8i32");
+
 namespace {
 
 typedef v4i_w v4i;
@@ -331,7 +335,8 @@ struct ACopier {
 // The weight stream of wave (wm, 1): codes of B-tile rows [64 wm, 64 wm + 64)
 // (1-KB copy t = 4 wm + i holds rows 16t .. 16t+15) and scale groups of rows
 // 64 wm + lane.
-// EPI: rows past N repeat the last one (their columns are not stored).
+// EPI (N % 64 == 0): a wave whose 64 rows lie behind N copies the last 64 (their
+// columns are not stored).
 template <bool FC1, bool EPI>
 struct BCopier {
   using Count = CopyCount<kBStages, kBCodeCopies>;
@@ -340,14 +345,14 @@ struct BCopier {
   int gli = 0, gls = 0;  // scale-group cursor
   int gitem = -1;        // item whose scale-row base is held in gbase
   const uint8_t* gbase;
-  int grow;              // its first scale row
 
   // First weight row of the wave's 64 B-tile rows [64 wm, 64 wm + 64): FC1 takes
   // gate rows (even wm) or the matching up rows (odd wm) of h columns
   // nb*128 + 64 (wm/2) + [0, 64); FC2 takes output rows nb*256 + 64 wm + [0, 64).
   __device__ __forceinline__ static int64_t row0(const FcArgs& p, int nb_, int wm) {
     if (FC1) return (int64_t)nb_ * (TBN / 2) + 64 * (wm >> 1) + ((wm & 1) ? (int64_t)p.N : 0);
-    return (int64_t)nb_ * TBN + 64 * wm;
+    const int64_t r = (int64_t)nb_ * TBN + 64 * wm;
+    return EPI ? min(r, (int64_t)p.N - 64) : r;
   }
 
   __device__ __forceinline__ void issue_code(const FcArgs& p, const Sched& sc, const uint8_t* smem, int wm, int s) {
@@ -365,23 +370,15 @@ struct BCopier {
     }
     const int ks = k_step(sc, nb, ls);
     const uint32_t base = lds_addr(smem) + L_B + (s % kBStages) * B_STAGE;
-    if (EPI) {
-      const int r0 = (int)row0(p, nb, wm), rb = min(r0, p.N - 1);
-      const uint8_t* wb = p.w + (int64_t)expert * p.w_estride + (int64_t)rb * (p.K / 2) + ks * B_ROW;
-      const uint32_t c16 = 16 * ((lane & 3) ^ ((lane >> 3) & 3));
-#pragma unroll
-      for (int i = 0; i < kBCodeCopies; ++i)
-        lds_copy16_s(wb, (uint32_t)(min(r0 + 16 * i + (lane >> 2), p.N - 1) - rb) * (uint32_t)(p.K / 2) + c16,
-                     base + 1024 * (kBCodeCopies * wm + i));
-      return;
-    }
     const uint8_t* w = p.w + (int64_t)expert * p.w_estride + row0(p, nb, wm) * (p.K / 2) + ks * B_ROW;
     // copy i: rows 16i + lane/4 of the wave's 64, slot lane%4 receiving chunk
     // (lane%4) ^ ((row/2)%4) = (lane%4) ^ ((lane/8)%4)
-    const uint32_t lo = (uint32_t)(lane >> 2) * (uint32_t)(p.K / 2) + 16 * ((lane & 3) ^ ((lane >> 3) & 3));
+    // (EPI: that row holds column epi_row16 of the 64)
+    const int lr = EPI ? epi_row16(lane >> 2) : lane >> 2;
+    const uint32_t lo = (uint32_t)lr * (uint32_t)(p.K / 2) + 16 * ((lane & 3) ^ ((lane >> 3) & 3));
 #pragma unroll
     for (int i = 0; i < kBCodeCopies; ++i)
-      lds_copy16_s(w, lo + (uint32_t)(16 * i) * (uint32_t)(p.K / 2), base + 1024 * (kBCodeCopies * wm + i));
+      lds_copy16_s(w, lo + (uint32_t)(EPI ? epi_row16(16 * i) : 16 * i) * (uint32_t)(p.K / 2), base + 1024 * (kBCodeCopies * wm + i));
   }
 
   __device__ __forceinline__ void issue_group(const FcArgs& p, const Sched& sc, const uint8_t* smem, int wm, int G) {
@@ -395,12 +392,10 @@ struct BCopier {
     }
     if (li != gitem) {
       const ItemGeom it = item_geom(p, sc, li);
-      // the wave's 64 rows: the first of them within N
-      grow = EPI ? min((int)row0(p, it.nb, wm), p.N - 1) : (int)row0(p, it.nb, wm);
-      gbase = p.w_scale + (int64_t)it.expert * p.ws_estride + (int64_t)grow * (p.K / 32);
+      gbase = p.w_scale + (int64_t)it.expert * p.ws_estride + row0(p, it.nb, wm) * (p.K / 32);
       gitem = li;
     }
-    lds_copy16_s(gbase + 4 * ls, (uint32_t)(EPI ? min(lane, p.N - 1 - grow) : lane) * (uint32_t)(p.K / 32), lds_addr(smem) + L_BS + (G % 2) * BS_GROUP + 1024 * wm);
+    lds_copy16_s(gbase + 4 * ls, (uint32_t)(EPI ? epi_row16(lane) : lane) * (uint32_t)(p.K / 32), lds_addr(smem) + L_BS + (G % 2) * BS_GROUP + 1024 * wm);
   }
 
   __device__ __forceinline__ void prologue(const FcArgs& p, const Sched& sc, const uint8_t* smem, int wm) {
@@ -467,14 +462,17 @@ __device__ __forceinline__ void read_b(const uint8_t* bs, const uint8_t* bss, co
 // step's fragments (stages `nas`, `nbs`) placed between them: a column tile's
 // B fragment is replaced right after its MFMAs, an A fragment right after its
 // MFMA with the last column tile.
-template <int NM>
+// SWAP: the weights are the MFMA's first operand (mx_linear).
+template <int NM, bool SWAP>
 __device__ __forceinline__ void mul_step(v4f (&acc)[kSubs][kTiles], Frags& f, const uint8_t* nas, const uint8_t* nbs,
                                          const uint8_t* nass, const uint8_t* nbss, const LaneOffs& o) {
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) {
 #pragma unroll
     for (int m = 0; m < kSubs; ++m) {
-      if (m < NM) acc[m][n] = mfma16_f8_f4_w(f.a[m], f.b[n], acc[m][n], 0, Fmt<1>::MFMA, 0, f.asc[m], 0, f.bsc[n]);
+      if (m < NM)
+        acc[m][n] = SWAP ? mfma16_f4_f8_w(f.b[n], f.a[m], acc[m][n], Fmt<1>::MFMA, 0, 0, f.bsc[n], 0, f.asc[m])
+                         : mfma16_f8_f4_w(f.a[m], f.b[n], acc[m][n], 0, Fmt<1>::MFMA, 0, f.asc[m], 0, f.bsc[n]);
       if (n == kTiles - 1) read_a(nas, nass, o, m, f.a[m], f.asc[m]);
     }
     read_b(nbs, nbss, o, n, f.b[n], f.bsc[n]);
@@ -491,7 +489,7 @@ __device__ __forceinline__ void mul_step(v4f (&acc)[kSubs][kTiles], Frags& f, co
 // used (and, after a group's last step, the group after next into that group's
 // buffer) and multiplies step g while reading step g+1's fragments (past the
 // last step the reads hit a stale buffer and go unused).
-template <int NM, class Copier>
+template <int NM, bool SWAP, class Copier>
 __device__ __forceinline__ void item_steps(const FcArgs& p, const Sched& sc, v4f (&acc)[kSubs][kTiles], Frags& f,
                                            const LaneOffs& o, uint8_t* smem, Copier& cp, int wm, int gbase) {
   for (int s = 0; s < sc.nk; ++s) {
@@ -502,7 +500,7 @@ __device__ __forceinline__ void item_steps(const FcArgs& p, const Sched& sc, v4f
     cp.issue(p, sc, smem, wm, g);
     const int nx = g + 1;
     const int grp = (nx / kGroup) & 1, q = nx & (kGroup - 1);
-    mul_step<NM>(acc, f, smem + L_A + (nx % kAStages) * A_STAGE, smem + L_B + (nx % kBStages) * B_STAGE,
+    mul_step<NM, SWAP>(acc, f, smem + L_A + (nx % kAStages) * A_STAGE, smem + L_B + (nx % kBStages) * B_STAGE,
                  smem + L_AS + grp * AS_GROUP + 4 * q, smem + L_BS + grp * BS_GROUP + 4 * q, o);
   }
 }
@@ -539,10 +537,10 @@ __device__ __forceinline__ void wave_main(const FcArgs& p, const Sched& sc, uint
   for (int ci = 0; ci < sc.my_items; ++ci) {
     // one step loop per sub-block count, so that the accumulators stay in place
     switch (nm) {
-      case 3: item_steps<3>(p, sc, acc, f, o, smem, cp, wm, gbase); break;
-      case 2: item_steps<2>(p, sc, acc, f, o, smem, cp, wm, gbase); break;
-      case 1: item_steps<1>(p, sc, acc, f, o, smem, cp, wm, gbase); break;
-      default: item_steps<0>(p, sc, acc, f, o, smem, cp, wm, gbase); break;
+      case 3: item_steps<3, EPI>(p, sc, acc, f, o, smem, cp, wm, gbase); break;
+      case 2: item_steps<2, EPI>(p, sc, acc, f, o, smem, cp, wm, gbase); break;
+      case 1: item_steps<1, EPI>(p, sc, acc, f, o, smem, cp, wm, gbase); break;
+      default: item_steps<0, EPI>(p, sc, acc, f, o, smem, cp, wm, gbase); break;
     }
     gbase += sc.nk;
 
@@ -553,13 +551,19 @@ __device__ __forceinline__ void wave_main(const FcArgs& p, const Sched& sc, uint
     for (int m = 0; m < kSubs; ++m) {
       if (m >= nm) continue;
       if constexpr (EPI) {
-        // a 16-row sub-block, four column tiles at a time: their factors and
-        // residuals are all requested before the first is used
+        // the lane holds row l16 of the sub-block, eight columns of each tile pair
+        const Epilogue e = epi_load();
+        const int el = epi_lane();
+        const int col = it.nb * TBN + 128 * wn + 8 * (el >> 4), row = 16 * (wm + 4 * m) + (el & 15);
+        // (one piece at a time: two or four in flight measured 3% and 1% slower
+        // over 8192 x 4096 x 7168, spilling around the epilogue)
 #pragma unroll
-        for (int n0 = 0; n0 < kTiles; n0 += 4)
-          epi_block<4, 4, ACT>(p, it.expert, it.p0 + 16 * (wm + 4 * m) + 4 * g, it.p0 + it.rows,
-                               it.nb * TBN + 128 * wn + 16 * n0 + l16, 16,
-                               [&](int i, int n) { return acc[m][n0 + n][i]; });
+        for (int q = 0; q < kTiles / 2; ++q) {
+          EpiBias bias[1];
+          epi_biases(e, p.N, it.expert, col + 32 * q, 0, bias);
+          epi_row<1, ACT>(e, p.N, it.p0 + row, it.p0 + it.rows, col + 32 * q, 0, bias,
+                          [&](int, int i) { return acc[m][2 * q + (i >> 2)][i & 3]; });
+        }
         continue;
       }
 #pragma unroll
@@ -608,10 +612,21 @@ __device__ __forceinline__ void wave_main(const FcArgs& p, const Sched& sc, uint
     for (int m = 0; m < kSubs; ++m)
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) acc[m][n] = (v4f){0.f, 0.f, 0.f, 0.f};
+    if constexpr (EPI) {
+      // the next step's fragments again (its stages hold until its barrier), so
+      // that they take no registers during the epilogue
+      const int grp = (gbase / kGroup) & 1, q = gbase & (kGroup - 1);
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n)
+        read_b(smem + L_B + (gbase % kBStages) * B_STAGE, smem + L_BS + grp * BS_GROUP + 4 * q, o, n, f.b[n], f.bsc[n]);
+#pragma unroll
+      for (int m = 0; m < kSubs; ++m)
+        read_a(smem + L_A + (gbase % kAStages) * A_STAGE, smem + L_AS + grp * AS_GROUP + 4 * q, o, m, f.a[m], f.asc[m]);
+    }
     if (ci + 1 < sc.my_items) {
       it = item_geom(p, sc, ci + 1);
       nm = wave_subs(it.rows);
-    }
+        }
   }
   wait_vm_lgkm0<0>();
 }

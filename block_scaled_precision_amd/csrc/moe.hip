@@ -608,7 +608,7 @@ static void linear_kind(const mx_linear_problem_t& p, LinearPlan& f) {
   if (p.act == MOE_ACT_MXFP8) {
     if (avg < kTiledMinRowsPerExpert || p.K % kTiledKMultiple) return;
     // the wide kernel's 32-bit offsets into A
-    if (e2m1 && p.K >= 1024 && p.N > kWideCols / 2 && (double)p.M * p.K < 4294967296.0) {
+    if (e2m1 && p.K >= 1024 && p.N % 64 == 0 && p.N > kWideCols / 2 && (double)p.M * p.K < 4294967296.0) {
       f.kind = Fc::kWide;
       f.rows = kTiledRows;
     } else {
@@ -682,7 +682,10 @@ extern "C" moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_
   FcArgs g = {};
   g.linear = true;
   g.epi.bias = t->bias;
-  g.epi.bias_bf16 = p->bias_dtype == MOE_SRC_BF16;
+  // (a bias row is N elements, N % 8 == 0: every row is as aligned as the first)
+  g.epi.bias_kind = !t->bias ? kBiasNone
+                    : p->bias_dtype == MOE_SRC_FP32 ? (aligned16(t->bias) ? kBiasF32 : kBiasF32Any)
+                                                    : (aligned16(t->bias) ? kBiasBf16 : kBiasBf16Any);
   g.epi.fn = p->fn;
   g.epi.mul = (const uint16_t*)t->mul;
   g.epi.residual = (const uint16_t*)t->residual;
@@ -715,7 +718,7 @@ extern "C" moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_
   g.N = (int)N;
   const int cols = fc_cols(f.kind, false, f.rows);
   g.nchunks = (int)((N + cols - 1) / cols);
-  g.obuf = (uint16_t*)t->out;
+  g.epi.out = (__bf16*)t->out;
   const int wf = p->w_fmt == MX_E2M1 ? 1 : 2;
   const int cus = device_cus();
   hipError_t e;
