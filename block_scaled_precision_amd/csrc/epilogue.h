@@ -52,49 +52,62 @@ __device__ __forceinline__ int epi_lane() {
 // SiLU through t = exp(-|v|) <= 1, so that the tail of negative v does not pass
 // through an overflowing exp(-v); erfc rather than 1 + erf: for negative v the
 // sum would cancel, leaving an error relative to v instead of to the result
-__device__ __forceinline__ float epi_fn(int fn, float v) {
+__device__ __forceinline__ float silu(float v) {
+  const float t = expf(-fabsf(v));
+  return v * (v < 0.0f ? t : 1.0f) / (1.0f + t);
+}
+__device__ __forceinline__ float gelu(float v) { return 0.5f * v * erfcf(-0.70710678f * v); }
+__device__ __forceinline__ float relu2(float v) {
+  const float r = fmaxf(v, 0.0f);
+  return r * r;
+}
+// (one choice for the eight values of a piece)
+__device__ __forceinline__ void epi_fn(int fn, float (&v)[8]) {
   switch (fn) {
-    case MX_FN_SILU: {
-      const float t = expf(-fabsf(v));
-      return v * (v < 0.0f ? t : 1.0f) / (1.0f + t);
-    }
-    case MX_FN_GELU: return 0.5f * v * erfcf(-0.70710678f * v);
-    case MX_FN_RELU2: {
-      const float r = fmaxf(v, 0.0f);
-      return r * r;
-    }
-    default: return v;
+    case MX_FN_SILU:
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = silu(v[q]);
+      break;
+    case MX_FN_GELU:
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = gelu(v[q]);
+      break;
+    case MX_FN_RELU2:
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = relu2(v[q]);
+      break;
+    default: break;
   }
 }
 
-// bias of columns [n, n + 8) (n < N) of a group, 0 without one
+// bias of columns [n, n + 8) (n < N) of a group as loaded, and its values (0
+// without one); loading does not wait for the data
 struct EpiBias {
-  float v[8];
+  uint4 lo, hi;
 };
 __device__ __forceinline__ EpiBias epi_bias(const Epilogue& e, int N, int group, int n) {
-  EpiBias b;
+  EpiBias b = {};
   const int64_t i = (int64_t)group * N + n;
   if (e.bias_kind == kBiasF32) {
-    const float4* p = (const float4*)((const float*)e.bias + i);
-    const float4 lo = p[0], hi = p[1];
-    b = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const uint4* p = (const uint4*)((const float*)e.bias + i);
+    b.lo = p[0];
+    b.hi = p[1];
   } else if (e.bias_kind == kBiasBf16) {
-    const uint4 d = *(const uint4*)((const uint16_t*)e.bias + i);
-    const uint32_t w[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      b.v[2 * q] = __uint_as_float(w[q] << 16);
-      b.v[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
-    }
-  } else {
-    // none, or not on a 16-byte address
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      b.v[q] = e.bias_kind == kBiasNone ? 0.f
-               : e.bias_kind == kBiasF32Any ? ((const float*)e.bias)[i + q]
-                                            : bf16_bits_to_f32(((const uint16_t*)e.bias)[i + q]);
+    b.lo = *(const uint4*)((const uint16_t*)e.bias + i);
+  } else if (e.bias_kind == kBiasF32Any) {
+    const uint32_t* p = (const uint32_t*)e.bias + i;
+    b.lo = make_uint4(p[0], p[1], p[2], p[3]);
+    b.hi = make_uint4(p[4], p[5], p[6], p[7]);
+  } else if (e.bias_kind == kBiasBf16Any) {
+    const uint16_t* p = (const uint16_t*)e.bias + i;
+    b.lo = make_uint4(p[0] | p[1] << 16, p[2] | p[3] << 16, p[4] | p[5] << 16, p[6] | p[7] << 16);
   }
   return b;
+}
+__device__ __forceinline__ float epi_bias_at(const Epilogue& e, const EpiBias& b, int q) {
+  const uint32_t w[8] = {b.lo.x, b.lo.y, b.lo.z, b.lo.w, b.hi.x, b.hi.y, b.hi.z, b.hi.w};
+  const bool f32 = e.bias_kind == kBiasF32 || e.bias_kind == kBiasF32Any;
+  return __uint_as_float(f32 ? w[q] : q & 1 ? w[q / 2] & 0xffff0000u : w[q / 2] << 16);
 }
 
 // The second factors and residuals of the piece at element offset o
@@ -110,20 +123,22 @@ __device__ __forceinline__ EpiIn epi_in(const Epilogue& e, int64_t o) {
 
 // The piece at o from v = accumulators + bias.  FN: the function, or -1 for e.fn.
 template <int FN = -1>
-__device__ __forceinline__ void epi_store(const Epilogue& e, int64_t o, const EpiIn& in, const float (&v)[8]) {
+__device__ __forceinline__ void epi_store(const Epilogue& e, int64_t o, const EpiIn& in, float (&v)[8]) {
   const uint32_t mu[4] = {in.mul.x, in.mul.y, in.mul.z, in.mul.w};
   const uint32_t re[4] = {in.residual.x, in.residual.y, in.residual.z, in.residual.w};
+  epi_fn(FN < 0 ? e.fn : FN, v);
+  if (e.mul) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] *= __uint_as_float(q & 1 ? mu[q / 2] & 0xffff0000u : mu[q / 2] << 16);
+  }
+  if (e.residual) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] += __uint_as_float(q & 1 ? re[q / 2] & 0xffff0000u : re[q / 2] << 16);
+  }
   uint32_t w[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    float x[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      x[h] = epi_fn(FN < 0 ? e.fn : FN, v[2 * q + h]);
-      if (e.mul) x[h] *= __uint_as_float(h ? mu[q] & 0xffff0000u : mu[q] << 16);
-      if (e.residual) x[h] += __uint_as_float(h ? re[q] & 0xffff0000u : re[q] << 16);
-    }
-    const v2bf o2 = {(__bf16)x[0], (__bf16)x[1]};
+    const v2bf o2 = {(__bf16)v[2 * q], (__bf16)v[2 * q + 1]};
     __builtin_memcpy(&w[q], &o2, 4);
   }
   *(uint4*)(e.out + o) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -146,7 +161,7 @@ __device__ __forceinline__ void epi_row(const Epilogue& e, int N, int64_t row, i
     if (col0 + q * cstep < N) {
       float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = acc(q, i) + bias[q].v[i];
+      for (int i = 0; i < 8; ++i) v[i] = acc(q, i) + epi_bias_at(e, bias[q], i);
       epi_store<FN>(e, row * N + col0 + q * cstep, in[q], v);
     }
 }

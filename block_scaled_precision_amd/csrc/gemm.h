@@ -131,8 +131,22 @@ hipError_t launch_fc_small_routed(const FcArgs& p, int grid, hipStream_t st);
 hipError_t launch_splitk_reduce(const float* part, int ksplit, int64_t n4, float alpha, uint16_t* y,
                                 hipStream_t st);
 
-// mx_linear: out = epilogue of the sum over s of p.part[s] (N % 8 == 0, dense)
-hipError_t launch_splitk_epilogue(const FcArgs& p, hipStream_t st);
+// mx_linear with few rows (gemm_few.hip): items of 16 rows and kFewCols columns
+// (nchunks column blocks), one workgroup each; quant: bf16 activations are
+// quantized to MXFP8 on the way.
+constexpr int kFewCols = 16;
+hipError_t launch_linear_few(const FcArgs& p, bool mx_act, bool quant, int wfmt, hipStream_t st);
+// mx_linear with weights through LDS (gemm_rows.hip): `grid` persistent
+// workgroups, items of `rows` (16 or 64) rows and kRowsCols columns (nchunks column blocks),
+// any K % 128 == 0 of at least kRowsMinK.  Dense calls may split K's stages in
+// p.ksplit ranges (p.part), joined by launch_linear_join.
+constexpr int kRowsCols = 128;
+constexpr int kRowsK = 256;
+constexpr int kRowsMinK = 512;
+// mx_linear's largest K: 32-bit byte offsets over the rows of a tile of weights
+constexpr int64_t kMaxK = (int64_t)1 << 24;
+hipError_t launch_linear_rows(const FcArgs& p, bool mx_act, int wfmt, int rows, int grid, hipStream_t st);
+hipError_t launch_linear_join(const FcArgs& p, hipStream_t st);
 
 // Mid-M variant for bf16 activations and E2M1 weights when experts see many
 // rows: M-tiles of up to `rows` rows (kMidRows or kMidRowsHigh), N-blocks of

@@ -254,13 +254,16 @@ __device__ __forceinline__ void mid_multiply(const FcArgs& p, const MSched& sc, 
       } else if (EPI) {
         const Epilogue e = epi_load();
         // the lane holds rows 32wr + 16m + r16, eight columns of each tile pair
-        const int col = it.nb * MBN + 128 * wc + 8 * g;
-        EpiBias bias[4];
-        epi_biases(e, p.N, it.expert, col, 32, bias);
+        const int el = epi_lane(), col = it.nb * MBN + 128 * wc + 8 * (el >> 4);
 #pragma unroll
         for (int m = 0; m < 2; ++m)
-          epi_row(e, p.N, it.p0 + 32 * wr + 16 * m + r16, it.p0 + it.rows, col, 32, bias,
-                  [&](int q, int i) { return acc[m][2 * q + (i >> 2)][i & 3]; });
+#pragma unroll
+          for (int q0 = 0; q0 < 4; q0 += 2) {
+            EpiBias bias[2];
+            epi_biases(e, p.N, it.expert, col + 32 * q0, 32, bias);
+            epi_row(e, p.N, it.p0 + 32 * wr + 16 * m + (el & 15), it.p0 + it.rows, col + 32 * q0, 32, bias,
+                    [&](int q, int i) { return acc[m][2 * (q0 + q) + (i >> 2)][i & 3]; });
+          }
       } else {
         // row metadata by plain per-lane loads (the multiply waves issue no
         // copies, so their memory counter holds nothing else)

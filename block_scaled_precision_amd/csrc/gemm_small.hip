@@ -37,7 +37,6 @@
 #include <hip/hip_runtime.h>
 
 #include "copy_ring.h"
-#include "epilogue.h"
 #include "gemm.h"
 #include "mx_device.h"
 #include "batch_route.h"
@@ -133,11 +132,8 @@ __device__ __forceinline__ SGeom s_geom(const FcArgs& p, const SSched& sc, int l
   return g;
 }
 
-// weight row of row jr of N-block nb; EPI: rows past N repeat the last one (their
-// columns are not stored)
-template <bool FC1, bool EPI>
+template <bool FC1>
 __device__ __forceinline__ int64_t s_wrow(const FcArgs& p, int nb, int jr) {
-  if (EPI) return min(nb * SBN + epi_row16(jr), p.N - 1);
   if (FC1) return jr < SBN / 2 ? (int64_t)nb * (SBN / 2) + jr : (int64_t)p.N + nb * (SBN / 2) + jr - SBN / 2;
   return (int64_t)nb * SBN + jr;
 }
@@ -171,7 +167,7 @@ __device__ __forceinline__ void wait_ops(int n) {
 
 // ------------------------------------------------------------ multiply ---
 
-template <bool FC1, int GS, bool RT, bool EPI>
+template <bool FC1, int GS, bool RT>
 __device__ __forceinline__ void small_multiply(const FcArgs& p, const SSched& sc, uint8_t* smem) {
   using SG = SGroup<GS>;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -184,7 +180,7 @@ __device__ __forceinline__ void small_multiply(const FcArgs& p, const SSched& sc
   SGeom it = s_geom<RT>(p, sc, 0, smem);
   // routed FC2: the item's row metadata, loaded when the item starts (scalar
   // cache) so that its epilogue does not wait for it
-  const bool routed2 = !FC1 && !EPI && p.dense_rows == 0;
+  const bool routed2 = !FC1 && p.dense_rows == 0;
   Dw16 m_ids = {}, m_wts = {};
   if (routed2) {
     m_ids = load_dw16(p.sorted_assign + it.p0);
@@ -221,8 +217,7 @@ __device__ __forceinline__ void small_multiply(const FcArgs& p, const SSched& sc
           const v8bf bv = {q0[0], q0[1], q1[0], q1[1], q2[0], q2[1], q3[0], q3[1]};
           v8bf av;
           __builtin_memcpy(&av, &a[4 * blk + kq], 16);
-          acc[n] = EPI ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv, av, acc[n], 0, 0, 0)
-                       : __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv, acc[n], 0, 0, 0);
+          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv, acc[n], 0, 0, 0);
         }
       }
     }
@@ -240,23 +235,7 @@ __device__ __forceinline__ void small_multiply(const FcArgs& p, const SSched& sc
     } else {
       int orow[4];
       float wt[4];
-      if (EPI) {
-        // the lane holds row r16, columns 8g .. 8g + 7 of the wave's 32
-        const int col = it.nb * SBN + 32 * w + 8 * g;
-        if (r16 < it.rows && col < p.N) {
-          if (sc.S > 1) {
-            float4* o = (float4*)(p.part + ((int64_t)it.ks * p.dense_rows + it.p0 + r16) * p.N + col);
-            o[0] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
-            o[1] = make_float4(acc[1][0], acc[1][1], acc[1][2], acc[1][3]);
-          } else {
-            const Epilogue e = epi_load();
-            EpiBias bias[1];
-            epi_biases(e, p.N, it.expert, col, 0, bias);
-            epi_row(e, p.N, it.p0 + r16, it.p0 + it.rows, col, 0, bias,
-                    [&](int, int i) { return acc[i >> 2][i & 3]; });
-          }
-        }
-      } else if (sc.S > 1) {
+      if (sc.S > 1) {
         // split dense GEMM: this K range's unscaled fp32 sums
         float* o = p.part + ((int64_t)it.ks * p.dense_rows + it.p0) * p.N + it.nb * SBN + 32 * w + r16;
 #pragma unroll
@@ -291,7 +270,7 @@ __device__ __forceinline__ void small_multiply(const FcArgs& p, const SSched& sc
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (!EPI && sc.S == 1 && 4 * g + i < it.rows) {
+        if (sc.S == 1 && 4 * g + i < it.rows) {
           uint16_t* o = p.obuf + (int64_t)orow[i] * p.N + it.nb * SBN + 32 * w + r16;
           o[0] = f32_to_bf16_rne(wt[i] * acc[0][i]);
           o[16] = f32_to_bf16_rne(wt[i] * acc[1][i]);
@@ -313,7 +292,7 @@ __device__ __forceinline__ void small_multiply(const FcArgs& p, const SSched& sc
 
 // -------------------------------------------------------- weight copies ---
 
-template <bool FC1, int GS, bool RT, bool EPI>
+template <bool FC1, int GS, bool RT>
 __device__ __forceinline__ void small_weights(const FcArgs& p, const SSched& sc, uint8_t* smem) {
   using SG = SGroup<GS>;
   const int lane = threadIdx.x & 63, bw = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) - kWaveB);
@@ -334,7 +313,7 @@ __device__ __forceinline__ void small_weights(const FcArgs& p, const SSched& sc,
       const int t = kBData * bw + i;  // 1-KB copy index within the stage
       const int jr = (64 / CPR) * t + lane / CPR;
       const int ch = (lane % CPR) ^ wb_swz(jr);
-      src[i] = wb + s_wrow<FC1, EPI>(p, it.nb, jr) * wrow + 16 * ch;
+      src[i] = wb + s_wrow<FC1>(p, it.nb, jr) * wrow + 16 * ch;
     }
     // scale group: GROW bytes per row, SG::LW per lane; copy t covers bytes
     // [64 LW t, 64 LW (t+1)) of the group buffer (row-major)
@@ -342,7 +321,7 @@ __device__ __forceinline__ void small_weights(const FcArgs& p, const SSched& sc,
     for (int i = 0; i < SG::COPIES; ++i) {
       const int byte = SG::LW * (64 * (SG::COPIES * bw + i) + lane);
       const int jr = byte / GROW, within = byte % GROW;
-      ssrc[i] = sb + s_wrow<FC1, EPI>(p, it.nb, jr) * (K / 32) + within;
+      ssrc[i] = sb + s_wrow<FC1>(p, it.nb, jr) * (K / 32) + within;
     }
   };
   int li = 0, ls = 0, issued = 0;
@@ -440,9 +419,7 @@ __device__ __forceinline__ void small_activations(const FcArgs& p, const SSched&
 
 }  // namespace
 
-// EPI (mx_linear on FC2): rows of A and out are permuted rows, finished by the
-// epilogue
-template <bool FC1, int GS, bool EPI>
+template <bool FC1, int GS>
 __global__ __launch_bounds__(kThreadsS, 1) void k_fc_small(FcArgs p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[L_SG + L_SG_SIZE];
   SSched sc;
@@ -457,8 +434,8 @@ __global__ __launch_bounds__(kThreadsS, 1) void k_fc_small(FcArgs p) {
   sc.total = sc.my_items * sc.nk;
   if (sc.total == 0) return;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (w < kMulW) small_multiply<FC1, GS, false, EPI>(p, sc, smem);
-  else if (w < kWaveA) small_weights<FC1, GS, false, EPI>(p, sc, smem);
+  if (w < kMulW) small_multiply<FC1, GS, false>(p, sc, smem);
+  else if (w < kWaveA) small_weights<FC1, GS, false>(p, sc, smem);
   else small_activations<FC1, false>(p, sc, smem);
 }
 
@@ -528,18 +505,18 @@ __global__ __launch_bounds__(kThreadsS, 1) void k_fc_small_routed(FcArgs p) {
   sc.total = sc.my_items * sc.nk;
   if (sc.total == 0) return;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (w < kMulW) small_multiply<true, GS, true, false>(p, sc, smem);
-  else if (w < kWaveA) small_weights<true, GS, true, false>(p, sc, smem);
+  if (w < kMulW) small_multiply<true, GS, true>(p, sc, smem);
+  else if (w < kWaveA) small_weights<true, GS, true>(p, sc, smem);
   else small_activations<true, true>(p, sc, smem);
 }
 
-template <bool FC1, bool EPI>
+template <bool FC1>
 static hipError_t launch_small_t(const FcArgs& p, int grid, hipStream_t st) {
   // scale groups: the largest of 4, 2, 1 stages that divides the stages of an item
   const int nk = p.K / SBK / (p.ksplit > 1 ? p.ksplit : 1);
-  if (nk % 4 == 0) k_fc_small<FC1, 4, EPI><<<grid, kThreadsS, 0, st>>>(p);
-  else if (nk % 2 == 0) k_fc_small<FC1, 2, EPI><<<grid, kThreadsS, 0, st>>>(p);
-  else k_fc_small<FC1, 1, EPI><<<grid, kThreadsS, 0, st>>>(p);
+  if (nk % 4 == 0) k_fc_small<FC1, 4><<<grid, kThreadsS, 0, st>>>(p);
+  else if (nk % 2 == 0) k_fc_small<FC1, 2><<<grid, kThreadsS, 0, st>>>(p);
+  else k_fc_small<FC1, 1><<<grid, kThreadsS, 0, st>>>(p);
   return hipGetLastError();
 }
 
@@ -563,31 +540,6 @@ __global__ void k_splitk_reduce(const float4* __restrict__ part, int ksplit, int
   y[i] = o;
 }
 
-// The same sums finished by mx_linear's epilogue: a piece of 8 columns per thread.
-__global__ __launch_bounds__(64) void k_splitk_epilogue(FcArgs p, int64_t n8) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= n8) return;
-  const EpiIn in = epi_in(p.epi, 8 * i);
-  const EpiBias bias = epi_bias(p.epi, p.N, 0, (int)(8 * i % p.N));
-  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < p.ksplit; ++k) {
-    const float4* v = (const float4*)p.part + 2 * (k * n8 + i);
-    const float4 lo = v[0], hi = v[1];
-    const float a[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-    for (int q = 0; q < 8; ++q) s[q] += a[q];
-  }
-#pragma unroll
-  for (int q = 0; q < 8; ++q) s[q] += bias.v[q];
-  epi_store(p.epi, 8 * i, in, s);
-}
-
-hipError_t launch_splitk_epilogue(const FcArgs& p, hipStream_t st) {
-  const int64_t n8 = (int64_t)p.dense_rows * p.N / 8;
-  k_splitk_epilogue<<<(unsigned)((n8 + 63) / 64), 64, 0, st>>>(p, n8);
-  return hipGetLastError();
-}
-
 hipError_t launch_splitk_reduce(const float* part, int ksplit, int64_t n4, float alpha, uint16_t* y,
                                 hipStream_t st) {
   if (n4 <= 0) return hipSuccess;
@@ -597,8 +549,7 @@ hipError_t launch_splitk_reduce(const float* part, int ksplit, int64_t n4, float
 
 hipError_t launch_fc_small(const FcArgs& p, bool fc1, int grid, hipStream_t st) {
   if (grid < 1) grid = 1;
-  if (p.linear) return launch_small_t<false, true>(p, grid, st);
-  return fc1 ? launch_small_t<true, false>(p, grid, st) : launch_small_t<false, false>(p, grid, st);
+  return fc1 ? launch_small_t<true>(p, grid, st) : launch_small_t<false>(p, grid, st);
 }
 
 template <int GS>

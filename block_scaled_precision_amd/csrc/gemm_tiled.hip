@@ -293,7 +293,7 @@ __device__ __forceinline__ void bias_acc(v16f (&acc)[SUBS][2], int N, int expert
 #pragma unroll
     for (int m = 0; m < SUBS; ++m)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[m][i >> 2][4 * q + (i & 3)] = b.v[i];
+      for (int i = 0; i < 8; ++i) acc[m][i >> 2][4 * q + (i & 3)] = epi_bias_at(e, b, i);
   }
 }
 

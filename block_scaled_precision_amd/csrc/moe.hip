@@ -11,7 +11,9 @@
 // model", "Python API") and its fail-closed validation ("Validated scope").
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 
 #include "gemm.h"
@@ -151,7 +153,7 @@ constexpr int kMidMinRowsPerExpert = 32;
 constexpr int kMidHighMinRowsPerExpert = 96;
 
 // GEMM kernel family of one FC1/FC2 pair
-enum class Fc { kStream, kSmall, kMid, kTiled, kWide };
+enum class Fc { kStream, kSmall, kMid, kTiled, kWide, kFew, kRows };
 
 // N-block width: FC1 in h columns, FC2 in output columns (`rows`: the M-tile
 // height the kernel runs with)
@@ -161,6 +163,8 @@ static int fc_cols(Fc k, bool fc1, int rows) {
     case Fc::kMid: return fc1 ? kWideCols / 2 : kWideCols;
     case Fc::kTiled: return fc1 ? tiled_weight_rows(rows) / 2 : tiled_weight_rows(rows);
     case Fc::kSmall: return fc1 ? kSmallColsFc1 : kSmallColsFc2;
+    case Fc::kRows: return kRowsCols;
+    case Fc::kFew: return kFewCols;
     default: return fc1 ? kStreamColsFc1 : kStreamColsFc2;
   }
 }
@@ -578,7 +582,7 @@ struct LinearPlan {
   Fc kind;
   int rows;        // M-tile height
   int max_tiles;   // grouped: room of the tile list
-  int ksplit;      // dense, few rows: K ranges (0 or 1: none)
+  int ksplit;      // kRows, dense: K ranges (0 or 1: none)
   size_t quant, tiles, ntiles, part, total;
 };
 
@@ -589,44 +593,108 @@ static bool linear_sizes_ok(const mx_linear_problem_t& p) {
 static bool linear_supported(const mx_linear_problem_t& p) {
   // the bounds keep tile counts and per-workgroup step counts inside 32 bits
   return p.w_fmt != MX_E4M3 && p.N % 8 == 0 && p.K % 128 == 0 && p.M <= (int64_t)1 << 30 && p.N <= (int64_t)1 << 30 &&
-         p.K <= (int64_t)1 << 30 && (double)p.M * p.N <= 68719476736.0 &&
+         p.K <= kMaxK && (double)p.M * p.N <= 34359738368.0 &&
          (double)p.M * p.N * p.K <= 4503599627370496.0;
 }
 
-// Average rows per group (one group: all of them), rounded up.
-static int64_t linear_rows(const mx_linear_problem_t& p) {
-  return p.groups > 0 ? (p.M + p.groups - 1) / p.groups : p.M;
-}
+// Choice of the kernel: the smallest of the estimated times below, in
+// microseconds, which follow the kernels' structure: items over kLinearWgs
+// workgroups, rounds of them, steps of K per item, and a measured time per step
+// (MI355X, N = 4096, K = 7168 unless noted; the products themselves, without what
+// every call pays for its launch):
+//   few rows (gemm_few.hip; 16 x 16 items, 1024 K a step)  E2M1 x bf16: 1 row 0.43,
+//     16 rows 1.0; E3M2 0.2 more; MXFP8 0.4 more (it quantizes in place)
+//   rows (gemm_rows.hip; 256 K a step)  16 x 128 items: E2M1 0.55, E3M2 1.0;
+//     64 x 128 items: E2M1 1.2 (bf16), 0.75 (MXFP8), E3M2 1.75, 1.4
+//   mid (E2M1 x bf16; 128 K a step)  64 x 256 items 1.08, 128 x 256 1.6
+//   tiled (MXFP8)  128 x 256 items 1.0, 192 x 128 0.92 (E2M1), 1.05 (E3M2)
+//   wide (E2M1 x MXFP8)  192 x 256 items 1.2
+// E.g. 64 rows of bf16 x E2M1: few 40, 16-row tiles in two K ranges 16.7, 64-row
+// tiles in four 17.3, mid 66; 8192 rows: 64-row tiles 606, mid 423.  A call that
+// streams every expert's weights is bound by that instead (kWeightRate).
+// Sizes only, so that the workspace does not depend on the device.
+constexpr int kLinearWgs = 256;
+constexpr double kWeightRate = 5.2e6;  // bytes per microsecond from HBM
 
-// The kernel of a call, by the layer's own thresholds on the average rows per
-// group; the epilogue variants mask columns past N, so any N does.
-static void linear_kind(const mx_linear_problem_t& p, LinearPlan& f) {
-  const int64_t avg = linear_rows(p);
-  const bool e2m1 = p.w_fmt == MX_E2M1;
-  f.kind = Fc::kStream;
-  f.rows = kStreamRows;
-  if (p.act == MOE_ACT_MXFP8) {
-    if (avg < kTiledMinRowsPerExpert || p.K % kTiledKMultiple) return;
-    // the wide kernel's 32-bit offsets into A
-    if (e2m1 && p.K >= 1024 && p.N % 64 == 0 && p.N > kWideCols / 2 && (double)p.M * p.K < 4294967296.0) {
-      f.kind = Fc::kWide;
-      f.rows = kTiledRows;
+struct LinearCost {
+  const mx_linear_problem_t& p;
+  double active;   // groups with rows (expected)
+  double per;      // rows of one of them
+  bool quant;      // bf16 rows to MXFP8 by a kernel of its own, where one is needed
+
+  LinearCost(const mx_linear_problem_t& q, bool has_a_scale) : p(q), quant(q.act == MOE_ACT_MXFP8 && !has_a_scale) {
+    if (p.groups > 0) {
+      active = p.groups * (1.0 - std::pow(1.0 - 1.0 / p.groups, (double)p.M));
+      active = std::max(active, 1.0);
     } else {
-      f.kind = Fc::kTiled;
-      f.rows = avg <= kTiledLowMaxRowsPerExpert ? kTiledRowsLow : kTiledRows;
+      active = 1.0;
     }
-  } else if (e2m1 && avg >= kMidMinRowsPerExpert && p.K % kMidK == 0) {
-    f.kind = Fc::kMid;
-    f.rows = avg >= kMidHighMinRowsPerExpert ? kMidRowsHigh : kMidRows;
-  } else if (e2m1 && p.K % kSmallK == 0) {
-    f.kind = Fc::kSmall;
+    per = p.M / active;
+  }
+  double tiles(int bm) const {
+    if (p.groups == 0) return std::ceil(p.M / (double)bm);
+    return active * std::max(1.0, per / bm + 0.5);
+  }
+  // items of bm rows and bn columns in `ksplit` K ranges, `steps` of `t` each
+  double time(int bm, int bn, double steps, double t, int ksplit = 1) const {
+    const double items = tiles(bm) * std::ceil(p.N / (double)bn) * ksplit;
+    double rounds = items / kLinearWgs;
+    if (p.groups == 0 || rounds < 1.0) rounds = std::ceil(rounds);
+    const double weights = active * p.N * (double)p.K * (wbits(p.w_fmt) / 8.0 + 1.0 / 32.0) / kWeightRate;
+    return std::max(rounds * std::ceil(steps / ksplit) * t, weights);
+  }
+  double quant_time() const { return quant ? 3.5 + (double)p.M * p.K * 3.0 / 3.5e6 : 0.0; }
+  double join_time(int ksplit) const { return ksplit > 1 ? 4.5 + (double)ksplit * p.M * p.N * 8.0 / 4.0e6 : 0.0; }
+};
+
+static void linear_kind(const mx_linear_problem_t& p, bool has_a_scale, LinearPlan& f) {
+  const LinearCost c(p, has_a_scale);
+  const bool e2m1 = p.w_fmt == MX_E2M1, mx = p.act == MOE_ACT_MXFP8;
+  double best = -1.0;
+  auto take = [&](Fc kind, int rows, int ksplit, double us) {
+    if (best >= 0.0 && us >= best) return;
+    best = us;
+    f.kind = kind;
+    f.rows = rows;
+    f.ksplit = ksplit;
+  };
+  // (its grid has one workgroup per item)
+  if (c.tiles(16) * (p.N / 16) <= 1 << 20) {
+    const double t = 0.43 + 0.57 * std::min(c.per, 16.0) / 16.0 + (e2m1 ? 0.0 : 0.2) + (mx ? 0.4 : 0.0);
+    take(Fc::kFew, kStreamRows, 0, c.time(16, 16, std::ceil(p.K / 2048.0) * 2.0, t));
+  }
+  if (p.K >= kRowsMinK) {
+    const double steps = std::ceil(p.K / (double)kRowsK);
+    const double t16 = e2m1 ? 0.55 : 1.0, t64 = e2m1 ? (mx ? 0.75 : 1.2) : (mx ? 1.4 : 1.75);
+    // K ranges of at least two stages, dense calls only
+    const int most = p.groups > 0 ? 1 : (int)std::min(16.0, std::max(1.0, std::floor(steps / 2.0)));
+    for (int s = 1; s <= most; ++s) {
+      const double more = c.quant_time() + c.join_time(s);
+      take(Fc::kRows, 16, s, c.time(16, kRowsCols, steps, t16, s) + more);
+      take(Fc::kRows, 64, s, c.time(64, kRowsCols, steps, t64, s) + more);
+    }
+  } else {
+    // short K: the stream kernel reads weights straight into the MFMA layout
+    take(Fc::kStream, kStreamRows, 0, c.time(16, 4 * kStreamColsFc2, p.K / 128.0, 1.2) + c.quant_time());
+  }
+  const double steps = p.K / 128.0;
+  if (!mx && e2m1 && p.K % kMidK == 0) {
+    take(Fc::kMid, kMidRows, 0, c.time(kMidRows, kWideCols, steps, 1.08));
+    take(Fc::kMid, kMidRowsHigh, 0, c.time(kMidRowsHigh, kWideCols, steps, 1.6));
+  }
+  if (mx && p.K % kTiledKMultiple == 0) {
+    take(Fc::kTiled, kTiledRowsLow, 0, c.time(128, tiled_weight_rows(kTiledRowsLow), steps, 1.0) + c.quant_time());
+    take(Fc::kTiled, kTiledRows, 0,
+         c.time(192, tiled_weight_rows(kTiledRows), steps, e2m1 ? 0.92 : 1.05) + c.quant_time());
+    // (its 32-bit offsets into A, and column blocks of 64 inside N)
+    if (e2m1 && p.K >= 1024 && p.N % 64 == 0 && (double)p.M * p.K < 4294967296.0)
+      take(Fc::kWide, kTiledRows, 0, c.time(192, kWideCols, steps, 1.2) + c.quant_time());
   }
 }
 
 static LinearPlan linear_plan(const mx_linear_problem_t& p, bool has_a_scale) {
   LinearPlan f = {};
-  linear_kind(p, f);
-  if (f.kind == Fc::kSmall && p.groups == 0) f.ksplit = dense_ksplit(p.M, p.N, p.K, p.act, p.w_fmt);
+  linear_kind(p, has_a_scale, f);
   if (p.groups > 0) f.max_tiles = (int)(p.M / f.rows + (p.M < p.groups ? p.M : p.groups));
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -634,7 +702,7 @@ static LinearPlan linear_plan(const mx_linear_problem_t& p, bool has_a_scale) {
     o = align_up(o + bytes, 256);
     return r;
   };
-  if (p.act == MOE_ACT_MXFP8 && !has_a_scale) f.quant = take(gemm_quant_bytes(p.M, p.K));
+  if (p.act == MOE_ACT_MXFP8 && !has_a_scale && f.kind != Fc::kFew) f.quant = take(gemm_quant_bytes(p.M, p.K));
   if (p.groups > 0) {
     f.tiles = take((size_t)f.max_tiles * sizeof(Tile));
     f.ntiles = take(4);
@@ -692,7 +760,8 @@ extern "C" moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_
   g.k = 1;
   g.a = t->a;
   g.a_scale = t->a_scale;
-  if (mx && !t->a_scale) {
+  const bool quant = mx && !t->a_scale;
+  if (quant && f.kind != Fc::kFew) {
     uint8_t* qc = (uint8_t*)ws + f.quant;
     uint8_t* qs = qc + align_up((size_t)(M * K), 256);
     if (launch_quantize(t->a, MOE_SRC_BF16, M, K, K, MX_E4M3, qc, qs, stream) != hipSuccess) return MOE_ERR_HIP;
@@ -723,17 +792,18 @@ extern "C" moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_
   const int cus = device_cus();
   hipError_t e;
   switch (f.kind) {
-    case Fc::kSmall:
+    case Fc::kRows:
       if (f.ksplit > 1) {
         g.ksplit = f.ksplit;
         g.part = (float*)(ws + f.part);
       }
-      e = launch_fc_small(g, false, cus, stream);
-      if (e == hipSuccess && g.ksplit > 1) e = launch_splitk_epilogue(g, stream);
+      e = launch_linear_rows(g, mx, wf, f.rows, cus, stream);
+      if (e == hipSuccess && g.ksplit > 1) e = launch_linear_join(g, stream);
       break;
     case Fc::kMid: e = launch_fc_mid(g, false, f.rows, cus, stream); break;
     case Fc::kWide: e = launch_fc_wide(g, false, cus, stream); break;
     case Fc::kTiled: e = launch_fc_tiled(g, false, wf, f.rows, cus, stream); break;
+    case Fc::kFew: e = launch_linear_few(g, mx, quant, wf, stream); break;
     default: e = launch_fc_stream(g, false, mx, wf, stream);
   }
   return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;

@@ -286,9 +286,9 @@ typedef struct {
  * is invalid.  It holds the tile list of grouped calls, the partial sums of
  * split ones and, unless a_scale is given, the quantized A of MXFP8 from bf16, so
  * calls that may run at the same time need one each.
- * Requires M >= 0 (0: no-op), M <= 2^30, M*N <= 2^36, M*N*K <= 2^52 and 16-byte
- * aligned a, a_scale, w, w_scale, mul, residual and out (bias: its element size); N % 8
- * != 0, K % 128 != 0, larger sizes or E4M3 weights give MOE_ERR_UNSUPPORTED.
+ * Requires M >= 0 (0: no-op), M <= 2^30, K <= 2^24, M*N <= 2^35, M*N*K <= 2^52 and
+ * 16-byte aligned a, a_scale, w, w_scale, mul, residual and out (bias: its element
+ * size); N % 8 != 0, K % 128 != 0, larger sizes or E4M3 weights give MOE_ERR_UNSUPPORTED.
  * Deterministic: the summation order depends on the problem alone. */
 size_t mx_linear_workspace_bytes(const mx_linear_problem_t* p, int has_a_scale);
 moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_tensors_t* t, void* workspace,

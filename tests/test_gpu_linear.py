@@ -359,6 +359,27 @@ def test_rows_past_32_bit_offsets():
         assert torch.equal(out[0], out[M - 41])
 
 
+@pytest.mark.parametrize("M,N,act", [(20, 136, "bf16"), (100, 136, "bf16"), (3, 24, "mxfp8"), (70, 136, "mxfp8")])
+def test_longest_sum(M, N, act):
+    """K = 2^24, where 128 weight rows of E3M2 and 64 rows of A reach over 2^30
+    bytes: weights that are zero but for a few blocks (the last among them) give
+    the products of those blocks alone, exactly."""
+    from block_scaled_precision_amd import moe_mx as m
+    K = 1 << 24
+    print_flush(f"mx_linear K=2^24 M={M} N={N} {act}")
+    blocks = [0, 5, 1 << 10, (1 << 18) + 3, (1 << 19) - 5, (1 << 19) - 4, (1 << 19) - 2, (1 << 19) - 1]
+    cols = torch.cat([torch.arange(32 * b, 32 * b + 32) for b in blocks])
+    small, (ws, ss) = _ints((M, 256), 17, 20), _weights((N,), 256, "e3m2", 17)
+    w = torch.zeros((N, K * 3 // 4), dtype=torch.uint8, device="cuda")
+    for i, b in enumerate(blocks):
+        w[:, 24 * b:24 * b + 24] = ws[:, 24 * i:24 * i + 24].cuda()
+    s = torch.full((N, K // 32), 127, dtype=torch.uint8, device="cuda")
+    a = torch.ones((M, K), dtype=BF16, device="cuda")
+    a[:, cols.cuda()] = small.cuda()
+    ref, _, _ = og.mx_linear(_np(small), ws.numpy(), ss.numpy(), wfmt="e3m2", act=act)
+    _same_bits(m.mx_linear(a, w, s, "e3m2", act), ref, "longest sum")
+
+
 def _draw(n, seed=20261207):
     rng = np.random.default_rng(seed)
     out = []
