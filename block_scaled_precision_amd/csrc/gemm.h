@@ -94,7 +94,8 @@ hipError_t launch_fc_stream(const FcArgs& p, bool fc1, bool mx_act, int wfmt, hi
 // i.e. half as many h columns (FC1: nchunks = I / (that / 2)) or that many
 // output columns (FC2: nchunks = H / that); `grid` persistent workgroups
 // (rounded down to a multiple of 8, at least 8).  Requires K to be a multiple
-// of kTiledKMultiple (scales travel in groups of 4 128-K stages).
+// of kTiledKMultiple (scales travel in groups of 4 128-K stages; mx_linear: of 128,
+// at least kTiledKMultiple).
 constexpr int kTiledRows = 192;
 constexpr int kTiledRowsLow = 128;
 constexpr int kTiledKMultiple = 512;
@@ -138,11 +139,10 @@ constexpr int kFewCols = 16;
 hipError_t launch_linear_few(const FcArgs& p, bool mx_act, bool quant, int wfmt, hipStream_t st);
 // mx_linear with weights through LDS (gemm_rows.hip): `grid` persistent
 // workgroups, items of `rows` (16 or 64) rows and kRowsCols columns (nchunks column blocks),
-// any K % 128 == 0 of at least kRowsMinK.  Dense calls may split K's stages in
+// any K % 128 == 0.  Dense calls may split K's stages in
 // p.ksplit ranges (p.part), joined by launch_linear_join.
 constexpr int kRowsCols = 128;
 constexpr int kRowsK = 256;
-constexpr int kRowsMinK = 512;
 // mx_linear's largest K: 32-bit byte offsets over the rows of a tile of weights
 constexpr int64_t kMaxK = (int64_t)1 << 24;
 hipError_t launch_linear_rows(const FcArgs& p, bool mx_act, int wfmt, int rows, int grid, hipStream_t st);
@@ -153,7 +153,7 @@ hipError_t launch_linear_join(const FcArgs& p, hipStream_t st);
 // kWideCols weight rows, i.e. 128 h columns (FC1: nchunks = I / 128) or 256
 // output columns (FC2: nchunks = H / 256); `grid` persistent workgroups
 // (rounded down to a multiple of 8, at least 8).  Requires K % kMidK == 0
-// and, for the FC1 gather, A*k < 2^32.
+// (mx_linear: K % 128 == 0, K >= kMidK) and, for the FC1 gather, A*k < 2^32.
 constexpr int kMidRows = 64;
 constexpr int kMidRowsHigh = 128;
 constexpr int kMidK = 512;

@@ -96,6 +96,7 @@ struct MGeom {
 // equal contiguous share of their N-blocks.
 struct MSched {
   int xcd, G, full, tail0, q, Q, NB, nk, my_items, total;
+  int real;  // K stages of the operands, nk of them with mx_linear's padding
 };
 
 template <int TM>
@@ -123,6 +124,17 @@ __device__ __forceinline__ MGeom m_geom(const FcArgs& p, const MSched& sc, int l
     g.rows = t.rows;
   }
   return g;
+}
+
+// mx_linear takes any K >= 512 that is a multiple of 128: the steps of an item are
+// rounded up to whole scale groups.  A step past the end of K copies the last
+// stage once more and is not multiplied; the last group's 16 bytes of scales end
+// where the row ends.
+template <bool EPI> __device__ __forceinline__ int code_stage(const MSched& sc, int ls) {
+  return EPI ? min(ls, sc.real - 1) : ls;
+}
+template <bool EPI> __device__ __forceinline__ int scale_stage(const MSched& sc, int ls) {
+  return EPI ? min(ls, sc.real - GS) : ls;
 }
 
 // weight row (within the expert's matrix) of row jr of N-block nb; EPI: rows
@@ -228,10 +240,11 @@ __device__ __forceinline__ void mid_multiply(const FcArgs& p, const MSched& sc, 
   for (int gidx = 0; gidx < sc.total; ++gidx) {
     wait_lgkm0();
     barrier();
-    if (it.rows > 32 * wr) {
+    if (it.rows > 32 * wr && (!EPI || cs < sc.real)) {
       const uint8_t* st = smem + (gidx % L::NSTG) * L::S_STAGE;
       // scale byte of row jr, this stage, MX block g: sg[GROW * jr]
       const uint8_t* sg = smem + L::L_SG + ((gidx / GS) % NG) * G_BYTES + (gidx % GS) * SROW + g;
+      if (EPI) sg += SROW * ((cs & ~(GS - 1)) - scale_stage<EPI>(sc, cs & ~(GS - 1)));
       m_stage<FC1, EPI>(st, sg, wr, wc, r16, g, acc);
     }
     if (++cs < sc.nk) continue;
@@ -335,11 +348,11 @@ __device__ __forceinline__ void mid_weights(const FcArgs& p, const MSched& sc, u
     if (issued % GS == 0) {
       const uint32_t gb = lds0 + L::L_SG + ((issued / GS) % NG) * G_BYTES;
 #pragma unroll
-      for (int i = 0; i < kGCopies; ++i) lds_copy16(ssrc[i] + ls * SROW, gb + 1024 * (kGCopies * bw + i));
+      for (int i = 0; i < kGCopies; ++i) lds_copy16(ssrc[i] + scale_stage<EPI>(sc, ls) * SROW, gb + 1024 * (kGCopies * bw + i));
     }
     const uint32_t base = lds0 + (issued % L::NSTG) * L::S_STAGE;
 #pragma unroll
-    for (int i = 0; i < kBCopies; ++i) lds_copy16(src[i] + ls * B_ROW, base + 1024 * (kBCopies * bw + i));
+    for (int i = 0; i < kBCopies; ++i) lds_copy16(src[i] + code_stage<EPI>(sc, ls) * B_ROW, base + 1024 * (kBCopies * bw + i));
     ++issued;
     if (++ls == sc.nk) {
       ls = 0;
@@ -359,7 +372,7 @@ __device__ __forceinline__ void mid_weights(const FcArgs& p, const MSched& sc, u
 
 // ---------------------------------------------------- activation copies ---
 
-template <bool FC1, int TM>
+template <bool FC1, int TM, bool EPI>
 __device__ __forceinline__ void mid_activations(const FcArgs& p, const MSched& sc, uint8_t* smem, int aw) {
   using L = ML<TM>;
   constexpr int kACopies = L::A_COPIES;
@@ -404,7 +417,7 @@ __device__ __forceinline__ void mid_activations(const FcArgs& p, const MSched& s
     if (ls == 0) setup(li);
     const uint32_t base = lds0 + (issued % L::NSTG) * L::S_STAGE + S_B;
 #pragma unroll
-    for (int i = 0; i < kACopies; ++i) lds_copy16(src[i] + ls * A_ROW, base + 1024 * (kACopies * aw + i));
+    for (int i = 0; i < kACopies; ++i) lds_copy16(src[i] + code_stage<EPI>(sc, ls) * A_ROW, base + 1024 * (kACopies * aw + i));
     ++issued;
     if (++ls == sc.nk) {
       ls = 0;
@@ -426,7 +439,8 @@ __global__ __launch_bounds__(ML<TM>::THREADS, 1) void k_fc_mid(FcArgs p) {
   using L = ML<TM>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[L::L_TOTAL];
   MSched sc;
-  sc.nk = p.K / MBK;
+  sc.real = p.K / MBK;
+  sc.nk = EPI ? (sc.real + GS - 1) & ~(GS - 1) : sc.real;
   sc.NB = p.nchunks;
   const int ntiles = p.dense_rows > 0 ? (p.dense_rows + TM - 1) / TM : *p.num_tiles;
   sc.xcd = blockIdx.x & 7;
@@ -443,7 +457,7 @@ __global__ __launch_bounds__(ML<TM>::THREADS, 1) void k_fc_mid(FcArgs p) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (w < L::MUL_WAVES) mid_multiply<FC1, TM, EPI>(p, sc, smem, w);
   else if (w < L::MUL_WAVES + 2) mid_weights<FC1, TM, EPI>(p, sc, smem, w - L::MUL_WAVES);
-  else mid_activations<FC1, TM>(p, sc, smem, w - L::MUL_WAVES - 2);
+  else mid_activations<FC1, TM, EPI>(p, sc, smem, w - L::MUL_WAVES - 2);
 }
 
 }  // namespace

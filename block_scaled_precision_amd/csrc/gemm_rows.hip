@@ -29,7 +29,9 @@
 // items.  K may end in half a stage (K % 256 == 128): its copies repeat the first
 // half and the second half is not multiplied.  Scales (8 bytes per row and stage)
 // travel in groups of 4 stages of an item, 32 bytes per row in two 16-byte copies;
-// one that would run past its row's end is moved back to end there.
+// one that would run past its row's end is moved back to end there.  Where a row
+// has fewer than 16 bytes of them (SHORT: K < 512, one group per item) they are
+// copied as words, 16 bytes per row, the last word again in place of those missing.
 //
 // Multiplication (lane = 16 g + r): each 128-K half of a stage is one MX block per
 // lane of row r of a column tile, block g, against the same block of activation
@@ -57,16 +59,10 @@ constexpr int kMulWaves = 4, kWaveA = 6;
 constexpr int rows_awaves(int sub) { return sub == 1 ? 1 : 2; }
 constexpr int rows_threads(int sub) { return 64 * (kWaveA + rows_awaves(sub)); }
 constexpr int kGroupStages = 4;  // stages per scale group
-constexpr int kGroupRow = kGroupStages * RK / 32;  // its scale bytes per row
-// Scale buffers.  A group is copied with its first stage x, after barrier x - NST +
-// 1, which certifies that stages up to x - NST are done with: the stages of the
-// three groups before it have to number NST - 1 = 5 at least.  Items have two or
-// more stages, so three neighbouring groups have (1, 4, 1 or 2, 2, 2 at the least).
-constexpr int kGroupBufs = 4;
 
 // LDS: [stages: weights | activations] [weight scales] [activation scales]
 // for tiles of SUB 16-row sub-tiles
-template <bool MXA, int WF, int SUB> struct Lay {
+template <bool MXA, int WF, int SUB, bool SHORT> struct Lay {
   static constexpr int RM = 16 * SUB;
   static constexpr int AWAVES = rows_awaves(SUB);
   static constexpr int BROW = RK * Fmt<WF>::BITS / 8;  // weight bytes per row and stage
@@ -77,12 +73,25 @@ template <bool MXA, int WF, int SUB> struct Lay {
                              : STAGE <= 48 * 1024 ? 3 : 2;
   static constexpr int BCOP = S_B / 1024 / 2;          // 1-KB copies per weight wave and stage
   static constexpr int ACOP = S_A / 1024 / AWAVES;     // per activation wave and stage
+  // Scales: bytes per row and group, group buffers, copies of a group per wave.  A
+  // group is copied with its first stage x, after barrier x - NST + 1, which
+  // certifies that stages up to x - NST are done with: the stages of the groups that
+  // use the other buffers before it have to number NST - 1 <= 5 at least.  Items of
+  // K >= 512 have two or more stages, so three neighbouring groups have (1, 4, 1 or
+  // 2, 2, 2 at the least); SHORT ones have one at least.
+  static constexpr int GROW = SHORT ? 16 : kGroupStages * RK / 32;
+  static constexpr int BUFS = SHORT ? 8 : 4;
+  static constexpr int WGCOP = SHORT ? 4 : 2;
+  static constexpr int AGCOP = !SHORT || SUB == 1 ? 1 : 2;
   static constexpr int WS = NST * STAGE;               // weight scales
-  static constexpr int WSB = RN * kGroupRow;           // one buffer of them
-  static constexpr int AS = WS + kGroupBufs * WSB;     // activation scales
-  static constexpr int ASB = 1024 * AWAVES;            // one buffer (32 rows a copy)
-  static constexpr int TOTAL = AS + (MXA ? kGroupBufs * ASB : 0);
-  static_assert(TOTAL <= 160 * 1024 && NST <= 6 && ASB >= RM * kGroupRow, "LDS");
+  static constexpr int WSB = RN * GROW;                // one buffer of them
+  static constexpr int AS = WS + BUFS * WSB;           // activation scales
+  static constexpr int ASB = (SHORT ? 256 : 1024) * AGCOP * AWAVES;  // one buffer
+  static constexpr int TOTAL = AS + (MXA ? BUFS * ASB : 0);
+  // copies that may be in flight when a stage is waited for
+  template <int COP, int GCOP>
+  static constexpr int IN_FLIGHT = (NST - 2) * COP + (SHORT ? NST - 2 : 2) * GCOP;
+  static_assert(TOTAL <= 160 * 1024 && NST <= 6 && ASB >= RM * GROW, "LDS");
 };
 
 struct Item {
@@ -135,7 +144,7 @@ __device__ __forceinline__ void wait_upto(int n) {
 // Order of a copy wave: issue(stage) makes COP copies, and GCOP of scales before
 // them where the stage begins a scale group (it returns whether).  A stage has
 // landed once at most the copies of the stages issued after it remain.
-template <int NST, int COP, int GCOP, class Issue>
+template <int NST, int COP, int GCOP, int IN_FLIGHT, class Issue>
 __device__ __forceinline__ void copy_loop(const Sched& sc, Issue issue) {
   uint32_t hist = 0;  // bit i: the stage issued i before the last began a scale group
   int issued = 0;
@@ -146,15 +155,15 @@ __device__ __forceinline__ void copy_loop(const Sched& sc, Issue issue) {
   for (int s = 0; s < NST - 1 && s < sc.total; ++s) next();
   for (int g = 0; g < sc.total; ++g) {
     const int after = issued - 1 - g;
-    wait_upto<0, (NST - 2) * COP + 2 * GCOP>(after * COP + GCOP * __popc(hist & ((1u << after) - 1u)));
+    wait_upto<0, IN_FLIGHT>(after * COP + GCOP * __popc(hist & ((1u << after) - 1u)));
     barrier();
     if (issued < sc.total) next();
   }
 }
 
-template <bool MXA, int WF, int SUB>
+template <bool MXA, int WF, int SUB, bool SHORT>
 __device__ __forceinline__ void copy_weights(const FcArgs& p, const Sched& sc, uint8_t* smem, int bw) {
-  using L = Lay<MXA, WF, SUB>;
+  using L = Lay<MXA, WF, SUB, SHORT>;
   const int lane = threadIdx.x & 63;
   const uint32_t lds0 = lds_addr(smem);
   const int64_t wrow = (int64_t)p.K * Fmt<WF>::BITS / 8;
@@ -165,7 +174,7 @@ __device__ __forceinline__ void copy_weights(const FcArgs& p, const Sched& sc, u
   // of 3/4 byte fit 31 bits; so do 63 activation rows)
   const uint8_t* wb = nullptr;
   const uint8_t* sb = nullptr;
-  uint32_t off[L::BCOP], soff[2];
+  uint32_t off[L::BCOP], soff[L::WGCOP];
   uint32_t back = 0;  // bit i: piece i of this lane lies in a stage's second half
   Item it = {};
   int li = 0, ls = 0, group = -1;
@@ -185,17 +194,21 @@ __device__ __forceinline__ void copy_weights(const FcArgs& p, const Sched& sc, u
         back |= (uint32_t)(ch >= CPR / 2) << i;
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        soff[i] = (uint32_t)min(epi_row16(64 * bw + 32 * i + (lane >> 1)), last) * (uint32_t)srow;
+      for (int i = 0; i < L::WGCOP; ++i) {
+        const int jr = SHORT ? 64 * bw + 16 * i + (lane >> 2) : 64 * bw + 32 * i + (lane >> 1);
+        soff[i] = (uint32_t)min(epi_row16(jr), last) * (uint32_t)srow;
+      }
     }
     const int s = it.s0 + ls;
     const bool fresh = ls % kGroupStages == 0;
     if (fresh) {
       ++group;
+      const uint32_t buf = lds0 + L::WS + (group % L::BUFS) * L::WSB;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        lds_copy16_s(sb, soff[i] + (uint32_t)scale_at(s, lane & 1, srow),
-                     lds0 + L::WS + (group % kGroupBufs) * L::WSB + 1024 * (2 * bw + i));
+      for (int i = 0; i < L::WGCOP; ++i) {
+        if (SHORT) lds_copy4(sb + soff[i] + min(4 * (lane & 3), srow - 4), buf + 256 * (L::WGCOP * bw + i));
+        else lds_copy16_s(sb, soff[i] + (uint32_t)scale_at(s, lane & 1, srow), buf + 1024 * (L::WGCOP * bw + i));
+      }
     }
     const uint32_t base = lds0 + (g % L::NST) * L::STAGE;
     const uint8_t* ws = wb + (int64_t)s * L::BROW;
@@ -213,12 +226,12 @@ __device__ __forceinline__ void copy_weights(const FcArgs& p, const Sched& sc, u
     }
     return fresh;
   };
-  copy_loop<L::NST, L::BCOP, 2>(sc, issue);
+  copy_loop<L::NST, L::BCOP, L::WGCOP, L::template IN_FLIGHT<L::BCOP, L::WGCOP>>(sc, issue);
 }
 
-template <bool MXA, int WF, int SUB>
+template <bool MXA, int WF, int SUB, bool SHORT>
 __device__ __forceinline__ void copy_rows(const FcArgs& p, const Sched& sc, uint8_t* smem, int aw) {
-  using L = Lay<MXA, WF, SUB>;
+  using L = Lay<MXA, WF, SUB, SHORT>;
   const int lane = threadIdx.x & 63;
   const uint32_t lds0 = lds_addr(smem);
   const bool half = p.K % RK != 0;
@@ -227,7 +240,7 @@ __device__ __forceinline__ void copy_rows(const FcArgs& p, const Sched& sc, uint
   constexpr int CPR = L::AROW / 16;
   const uint8_t* ab = nullptr;
   const uint8_t* sb = nullptr;
-  uint32_t off[L::ACOP], soff = 0;
+  uint32_t off[L::ACOP], soff[L::AGCOP] = {};
   uint32_t back = 0;
   Item it = {};
   int li = 0, ls = 0, group = -1;
@@ -244,14 +257,22 @@ __device__ __forceinline__ void copy_rows(const FcArgs& p, const Sched& sc, uint
         off[i] = (uint32_t)min(r, it.rows - 1) * (uint32_t)arow + 16 * ch;
         back |= (uint32_t)(ch >= CPR / 2) << i;
       }
-      if (MXA) soff = (uint32_t)min(32 * aw + (lane >> 1), it.rows - 1) * (uint32_t)srow;
+#pragma unroll
+      for (int i = 0; MXA && i < L::AGCOP; ++i) {
+        const int r = SHORT ? 16 * (L::AGCOP * aw + i) + (lane >> 2) : 32 * aw + (lane >> 1);
+        soff[i] = (uint32_t)min(r, it.rows - 1) * (uint32_t)srow;
+      }
     }
     const int s = it.s0 + ls;
     const bool fresh = MXA && ls % kGroupStages == 0;
     if (fresh) {
       ++group;
-      lds_copy16_s(sb, soff + (uint32_t)scale_at(s, lane & 1, srow),
-                   lds0 + L::AS + (group % kGroupBufs) * L::ASB + 1024 * aw);
+      const uint32_t buf = lds0 + L::AS + (group % L::BUFS) * L::ASB;
+#pragma unroll
+      for (int i = 0; i < L::AGCOP; ++i) {
+        if (SHORT) lds_copy4(sb + soff[i] + min(4 * (lane & 3), srow - 4), buf + 256 * (L::AGCOP * aw + i));
+        else lds_copy16_s(sb, soff[i] + (uint32_t)scale_at(s, lane & 1, srow), buf + 1024 * aw);
+      }
     }
     const uint32_t base = lds0 + (g % L::NST) * L::STAGE + L::S_B;
     const uint8_t* as = ab + (int64_t)s * L::AROW;
@@ -269,21 +290,21 @@ __device__ __forceinline__ void copy_rows(const FcArgs& p, const Sched& sc, uint
     }
     return fresh;
   };
-  copy_loop<L::NST, L::ACOP, 1>(sc, issue);
+  copy_loop<L::NST, L::ACOP, L::AGCOP, L::template IN_FLIGHT<L::ACOP, L::AGCOP>>(sc, issue);
 }
 
 // One 128-K half h of a stage: acc[m][n] += W(column tile n) A(sub-tile m)^T for
 // the first nm sub-tiles (FULL: all of them, with no branches between their reads)
-template <bool MXA, int WF, int SUB, bool FULL>
+template <bool MXA, int WF, int SUB, bool SHORT, bool FULL>
 __device__ __forceinline__ void mul_half(v4f (&acc)[SUB][2], const uint8_t* bs, const uint8_t* as, const uint8_t* ws,
                                          const uint8_t* xs, int h, int w, int g, int r, int nm) {
-  using L = Lay<MXA, WF, SUB>;
+  using L = Lay<MXA, WF, SUB, SHORT>;
   const int blk = 4 * h + g;
   uint32_t b[2][6], wsc[2];
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     const int jr = 32 * w + 16 * n + r;
-    wsc[n] = ws[kGroupRow * jr + blk];
+    wsc[n] = ws[L::GROW * jr + blk];
     if (WF == 1) {
       const uint4 v = *(const uint4*)(bs + jr * L::BROW + 16 * (blk ^ (jr & 7)));
       b[n][0] = v.x; b[n][1] = v.y; b[n][2] = v.z; b[n][3] = v.w; b[n][4] = 0; b[n][5] = 0;
@@ -310,7 +331,7 @@ __device__ __forceinline__ void mul_half(v4f (&acc)[SUB][2], const uint8_t* bs, 
       if (!FULL && m >= nm) continue;
       const uint4 lo = row(m, 8 * h + g), hi = row(m, 8 * h + 4 + g);
       const v8i av = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-      const int asc = (int)xs[kGroupRow * (16 * m + r) + blk];
+      const int asc = (int)xs[L::GROW * (16 * m + r) + blk];
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         const v8i bv = {(int)b[n][0], (int)b[n][1], (int)b[n][2], (int)b[n][3], (int)b[n][4], (int)b[n][5], 0, 0};
@@ -358,35 +379,57 @@ __device__ __forceinline__ void mul_half(v4f (&acc)[SUB][2], const uint8_t* bs, 
   }
 }
 
-template <bool MXA, int WF, int SUB>
+template <bool MXA, int WF, int SUB, bool SHORT>
 __device__ __forceinline__ void multiply(const FcArgs& p, const Sched& sc, const uint8_t* smem, int w) {
-  using L = Lay<MXA, WF, SUB>;
+  using L = Lay<MXA, WF, SUB, SHORT>;
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int srow = p.K / 32;
   const bool half = p.K % RK != 0;
   v4f acc[SUB][2];
 #pragma unroll
   for (int m = 0; m < SUB; ++m) acc[m][0] = acc[m][1] = (v4f){0.f, 0.f, 0.f, 0.f};
-  Item it = {};
-  EpiIn in[SUB];
-  EpiBias bias = {};
+  // The epilogue's operands are requested when the item starts; with 64 rows and
+  // short K, whose items have one stage or two, an item ahead (8192 x 4096 x 256 E2M1
+  // x bf16: 79 against 94 us; the other kernels lose 2 to 10% by it).
+  constexpr bool kAhead = SUB > 1 && SHORT;
+  Item it = {}, next = {};
+  EpiIn in[SUB], next_in[SUB];
+  EpiBias bias = {}, next_bias = {};
   int li = 0, ls = 0, group = -1, gs = 0, col = 0, nm = 1;  // gs: the group's first stage
   // the lane holds a piece of out per sub-tile: its row r, columns 8g .. 8g + 7
   // of the wave's 32
-  auto mine = [&](int m) { return 16 * m + r < it.rows && col < p.N; };
-  auto at = [&](int m) { return (int64_t)(it.p0 + 16 * m + r) * p.N + col; };
+  auto column = [&](const Item& i) { return i.nb * RN + 32 * w + 8 * g; };
+  auto mine = [&](const Item& i, int m, int c) { return 16 * m + r < i.rows && c < p.N; };
+  auto at = [&](const Item& i, int m, int c) { return (int64_t)(i.p0 + 16 * m + r) * p.N + c; };
+  auto request = [&](const Item& i, EpiIn (&to)[SUB], EpiBias& b) {
+    if (sc.S > 1) return;  // (launch_linear_join's)
+    const int c = column(i);
+#pragma unroll
+    for (int m = 0; m < SUB; ++m)
+      if (mine(i, m, c)) to[m] = epi_in(p.epi, at(i, m, c));
+    if (c < p.N) b = epi_bias(p.epi, p.N, i.expert, c);
+  };
+  if (kAhead) {
+    next = item_at<L::RM>(p, sc, 0);
+    request(next, next_in, next_bias);
+  }
   for (int gi = 0; gi < sc.total; ++gi) {
     if (ls == 0) {
-      // the epilogue's operands are requested when the item starts
-      it = item_at<L::RM>(p, sc, li);
-      nm = (it.rows + 15) >> 4;
-      col = it.nb * RN + 32 * w + 8 * g;
-      if (sc.S == 1) {
+      if (kAhead) {
+        it = next;
+        bias = next_bias;
 #pragma unroll
-        for (int m = 0; m < SUB; ++m)
-          if (mine(m)) in[m] = epi_in(p.epi, at(m));
-        if (col < p.N) bias = epi_bias(p.epi, p.N, it.expert, col);
+        for (int m = 0; m < SUB; ++m) in[m] = next_in[m];
+        if (li + 1 < sc.items) {
+          next = item_at<L::RM>(p, sc, li + 1);
+          request(next, next_in, next_bias);
+        }
+      } else {
+        it = item_at<L::RM>(p, sc, li);
+        request(it, in, bias);
       }
+      nm = (it.rows + 15) >> 4;
+      col = column(it);
     }
     const int s = it.s0 + ls;
     if (ls % kGroupStages == 0) {
@@ -396,39 +439,39 @@ __device__ __forceinline__ void multiply(const FcArgs& p, const Sched& sc, const
     wait_lgkm0();
     barrier();
     const uint8_t* st = smem + (gi % L::NST) * L::STAGE;
-    // scale byte of block b of the stage: [kGroupRow row + b]
-    const int h = (s - gs) >> 1, so = 16 * h + 8 * s - scale_at(gs, h, srow);
-    const uint8_t* ws = smem + L::WS + (group % kGroupBufs) * L::WSB + so;
-    const uint8_t* xs = smem + L::AS + (group % kGroupBufs) * L::ASB + so;
+    // scale byte of block b of the stage: [GROW row + b]
+    const int h = (s - gs) >> 1, so = SHORT ? 8 * s : 16 * h + 8 * s - scale_at(gs, h, srow);
+    const uint8_t* ws = smem + L::WS + (group % L::BUFS) * L::WSB + so;
+    const uint8_t* xs = smem + L::AS + (group % L::BUFS) * L::ASB + so;
     // A whole stage of a whole tile in one block lets the two halves' LDS reads and
     // conversions run together: 16-row E3M2 x bf16 606 against 656 us, 64-row tiles up
     // to 5%; the others of 16 rows lose 3% by it and take a branch between.
     const bool two = !(half && s == sc.stages - 1);
     if (SUB == 1 && (MXA || WF == 1)) {
-      mul_half<MXA, WF, SUB, true>(acc, st, st + L::S_B, ws, xs, 0, w, g, r, nm);
-      if (two) mul_half<MXA, WF, SUB, true>(acc, st, st + L::S_B, ws, xs, 1, w, g, r, nm);
-    } else if (nm == SUB && two) {
-      mul_half<MXA, WF, SUB, true>(acc, st, st + L::S_B, ws, xs, 0, w, g, r, nm);
-      mul_half<MXA, WF, SUB, true>(acc, st, st + L::S_B, ws, xs, 1, w, g, r, nm);
+      mul_half<MXA, WF, SUB, SHORT, true>(acc, st, st + L::S_B, ws, xs, 0, w, g, r, nm);
+      if (two) mul_half<MXA, WF, SUB, SHORT, true>(acc, st, st + L::S_B, ws, xs, 1, w, g, r, nm);
+    } else if ((SUB == 1 || nm == SUB) && two) {
+      mul_half<MXA, WF, SUB, SHORT, true>(acc, st, st + L::S_B, ws, xs, 0, w, g, r, nm);
+      mul_half<MXA, WF, SUB, SHORT, true>(acc, st, st + L::S_B, ws, xs, 1, w, g, r, nm);
     } else {
-      mul_half<MXA, WF, SUB, false>(acc, st, st + L::S_B, ws, xs, 0, w, g, r, nm);
-      if (two) mul_half<MXA, WF, SUB, false>(acc, st, st + L::S_B, ws, xs, 1, w, g, r, nm);
+      mul_half<MXA, WF, SUB, SHORT, false>(acc, st, st + L::S_B, ws, xs, 0, w, g, r, nm);
+      if (two) mul_half<MXA, WF, SUB, SHORT, false>(acc, st, st + L::S_B, ws, xs, 1, w, g, r, nm);
     }
     if (++ls < it.ns) continue;
 #pragma unroll
     for (int m = 0; m < SUB; ++m) {
-      if (mine(m)) {
+      if (mine(it, m, col)) {
         if (sc.S > 1) {
           // a K range's sums, for launch_linear_join
           const int ks = (sc.q + li * sc.Q) % sc.S;
-          float4* part = (float4*)(p.part + (int64_t)ks * p.dense_rows * p.N + at(m));
+          float4* part = (float4*)(p.part + (int64_t)ks * p.dense_rows * p.N + at(it, m, col));
           part[0] = make_float4(acc[m][0][0], acc[m][0][1], acc[m][0][2], acc[m][0][3]);
           part[1] = make_float4(acc[m][1][0], acc[m][1][1], acc[m][1][2], acc[m][1][3]);
         } else {
           float v[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = acc[m][i >> 2][i & 3] + epi_bias_at(p.epi, bias, i);
-          epi_store(p.epi, at(m), in[m], v);
+          epi_store(p.epi, at(it, m, col), in[m], v);
         }
       }
       acc[m][0] = acc[m][1] = (v4f){0.f, 0.f, 0.f, 0.f};
@@ -438,17 +481,22 @@ __device__ __forceinline__ void multiply(const FcArgs& p, const Sched& sc, const
   }
 }
 
-template <bool MXA, int WF, int SUB>
+template <bool MXA, int WF, int SUB, bool SHORT>
 __global__ __launch_bounds__(rows_threads(SUB), 1) void k_linear_rows(FcArgs p) {
-  using L = Lay<MXA, WF, SUB>;
+  using L = Lay<MXA, WF, SUB, SHORT>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[L::TOTAL];
   Sched sc;
   sc.S = p.ksplit > 1 ? p.ksplit : 1;
   sc.NB = p.nchunks;
   sc.stages = (p.K + RK - 1) / RK;
   const int ntiles = p.dense_rows > 0 ? (p.dense_rows + L::RM - 1) / L::RM : *p.num_tiles;
-  sc.q = blockIdx.x;
   sc.Q = gridDim.x;
+  // Workgroups b, b + 8, .. share an XCD's L2 (11824 rows over 75 experts, 240 x 2944
+  // E2M1 x MXFP8: 50 against 55 us).  Where the column blocks of a tile
+  // go round the XCDs evenly and each XCD has two or more, items are dealt out in
+  // turn, and an XCD keeps its columns' weights for all tiles; otherwise an XCD takes
+  // neighbouring items, so that the tiles' rows are read by one XCD or two.
+  sc.q = (sc.NB % 8 == 0 && sc.NB >= 16) || sc.Q % 8 ? blockIdx.x : (blockIdx.x & 7) * (sc.Q >> 3) + (blockIdx.x >> 3);
   const int nitems = ntiles * sc.NB * sc.S;
   sc.items = nitems > sc.q ? (nitems - sc.q + sc.Q - 1) / sc.Q : 0;
   sc.total = 0;
@@ -462,9 +510,9 @@ __global__ __launch_bounds__(rows_threads(SUB), 1) void k_linear_rows(FcArgs p) 
   }
   if (sc.total == 0) return;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (w < kMulWaves) multiply<MXA, WF, SUB>(p, sc, smem, w);
-  else if (w < kWaveA) copy_weights<MXA, WF, SUB>(p, sc, smem, w - kMulWaves);
-  else copy_rows<MXA, WF, SUB>(p, sc, smem, w - kWaveA);
+  if (w < kMulWaves) multiply<MXA, WF, SUB, SHORT>(p, sc, smem, w);
+  else if (w < kWaveA) copy_weights<MXA, WF, SUB, SHORT>(p, sc, smem, w - kMulWaves);
+  else copy_rows<MXA, WF, SUB, SHORT>(p, sc, smem, w - kWaveA);
 }
 
 // The sums of a split call's K ranges, in ascending order, and its epilogue: a
@@ -490,23 +538,25 @@ __global__ __launch_bounds__(64) void k_linear_join(FcArgs p, int64_t n8) {
 
 }  // namespace
 
-template <int SUB>
+template <int SUB, bool SHORT>
 static hipError_t launch_rows_t(const FcArgs& p, bool mx_act, int wfmt, int grid, hipStream_t st) {
-  if (mx_act && wfmt == 1) k_linear_rows<true, 1, SUB><<<grid, rows_threads(SUB), 0, st>>>(p);
-  else if (mx_act) k_linear_rows<true, 2, SUB><<<grid, rows_threads(SUB), 0, st>>>(p);
-  else if (wfmt == 1) k_linear_rows<false, 1, SUB><<<grid, rows_threads(SUB), 0, st>>>(p);
-  else k_linear_rows<false, 2, SUB><<<grid, rows_threads(SUB), 0, st>>>(p);
+  if (mx_act && wfmt == 1) k_linear_rows<true, 1, SUB, SHORT><<<grid, rows_threads(SUB), 0, st>>>(p);
+  else if (mx_act) k_linear_rows<true, 2, SUB, SHORT><<<grid, rows_threads(SUB), 0, st>>>(p);
+  else if (wfmt == 1) k_linear_rows<false, 1, SUB, SHORT><<<grid, rows_threads(SUB), 0, st>>>(p);
+  else k_linear_rows<false, 2, SUB, SHORT><<<grid, rows_threads(SUB), 0, st>>>(p);
   return hipGetLastError();
 }
 
 hipError_t launch_linear_rows(const FcArgs& p, bool mx_act, int wfmt, int rows, int grid, hipStream_t st) {
   if (grid < 1) grid = 1;
-  // what the scale copies and buffers assume: 16 scale bytes a row, two stages an item
-  if (p.K < kRowsMinK || p.K > kMaxK || p.K % 128 ||
-      (p.K + RK - 1) / RK < 2 * (p.ksplit > 1 ? p.ksplit : 1)) return hipErrorInvalidValue;
-  if (rows == 16) return launch_rows_t<1>(p, mx_act, wfmt, grid, st);
-  if (rows == 64) return launch_rows_t<4>(p, mx_act, wfmt, grid, st);
-  return hipErrorInvalidValue;
+  // a K range has two stages at least, as the scale buffers assume
+  if (p.K < 128 || p.K > kMaxK || p.K % 128 || (rows != 16 && rows != 64)) return hipErrorInvalidValue;
+  if (p.ksplit > 1 && (p.K + RK - 1) / RK < 2 * p.ksplit) return hipErrorInvalidValue;
+  if (p.K < 512)
+    return rows == 16 ? launch_rows_t<1, true>(p, mx_act, wfmt, grid, st)
+                      : launch_rows_t<4, true>(p, mx_act, wfmt, grid, st);
+  return rows == 16 ? launch_rows_t<1, false>(p, mx_act, wfmt, grid, st)
+                    : launch_rows_t<4, false>(p, mx_act, wfmt, grid, st);
 }
 
 hipError_t launch_linear_join(const FcArgs& p, hipStream_t st) {

@@ -25,7 +25,6 @@
 // MXFP4 weight; mxfp6-sm120 page: block-scaled MMA with FP32 accumulation).
 #include <hip/hip_runtime.h>
 
-#include "epilogue.h"
 #include "gemm.h"
 #include "mx_device.h"
 
@@ -78,15 +77,7 @@ __device__ __forceinline__ void load_b(BFrag& f, const uint8_t* row, const uint8
   f.scale = *(const uint32_t*)(srow + 4 * c);
 }
 
-// SWAP (mx_linear): the weights are the first operand, so the accumulators hold
-// out transposed
-template <bool SWAP>
-__device__ __forceinline__ v4f mma_bf16(v8bf a, v8bf b, v4f c) {
-  return SWAP ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0)
-              : __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
-template <bool MXA, int WF, bool SWAP>
+template <bool MXA, int WF>
 __device__ __forceinline__ void mma_chunk(v4f (&acc)[NB], const AFrag& a, const BFrag (&b)[NB], int g) {
   if (MXA) {
     const v8i av = {(int)a.d[0].x, (int)a.d[0].y, (int)a.d[0].z, (int)a.d[0].w,
@@ -97,10 +88,8 @@ __device__ __forceinline__ void mma_chunk(v4f (&acc)[NB], const AFrag& a, const 
       const v8i bv = {(int)b[n].d[0], (int)b[n].d[1], (int)b[n].d[2], (int)b[n].d[3],
                       (int)b[n].d[4], (int)b[n].d[5], 0, 0};
       const int bsc = (int)((b[n].scale >> (8 * g)) & 0xffu);
-      if (SWAP)
-        acc[n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, av, acc[n], Fmt<WF>::MFMA, 0, 0, bsc, 0, asc);
-      else
-        acc[n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc[n], 0, Fmt<WF>::MFMA, 0, asc, 0, bsc);
+      acc[n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc[n], 0, Fmt<WF>::MFMA, 0, asc,
+                                                                0, bsc);
     }
   } else if (WF == 2) {
     // E3M2: the lane's 32 codes (24 bytes, element i in bits 6i..6i+5) to 32
@@ -118,7 +107,7 @@ __device__ __forceinline__ void mma_chunk(v4f (&acc)[NB], const AFrag& a, const 
         const uint4 ad = a.d[s];
         v8bf av;
         __builtin_memcpy(&av, &ad, 16);
-        acc[n] = mma_bf16<SWAP>(av, bv, acc[n]);
+        acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv, acc[n], 0, 0, 0);
       }
     }
   } else {
@@ -136,14 +125,14 @@ __device__ __forceinline__ void mma_chunk(v4f (&acc)[NB], const AFrag& a, const 
         const uint4 ad = a.d[s];
         v8bf av;
         __builtin_memcpy(&av, &ad, 16);
-        acc[n] = mma_bf16<SWAP>(av, bv, acc[n]);
+        acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv, acc[n], 0, 0, 0);
       }
     }
   }
 }
 
 // Full-K mainloop with the next chunk's loads issued before the current MFMAs.
-template <bool MXA, int WF, bool SWAP = false>
+template <bool MXA, int WF>
 __device__ __forceinline__ void mainloop(v4f (&acc)[NB], const uint8_t* arow, const uint8_t* asrow,
                                          const uint8_t* const (&brow)[NB],
                                          const uint8_t* const (&bsrow)[NB], int nchunk, int g) {
@@ -159,15 +148,15 @@ __device__ __forceinline__ void mainloop(v4f (&acc)[NB], const uint8_t* arow, co
 #pragma unroll
       for (int n = 0; n < NB; ++n) load_b<WF>(b1[n], brow[n], bsrow[n], c + 1, g);
     }
-    mma_chunk<MXA, WF, SWAP>(acc, a0, b0, g);
+    mma_chunk<MXA, WF>(acc, a0, b0, g);
     if (c + 2 < nchunk) {
       load_a<MXA>(a0, arow, asrow, c + 2, g);
 #pragma unroll
       for (int n = 0; n < NB; ++n) load_b<WF>(b0[n], brow[n], bsrow[n], c + 2, g);
     }
-    mma_chunk<MXA, WF, SWAP>(acc, a1, b1, g);
+    mma_chunk<MXA, WF>(acc, a1, b1, g);
   }
-  if (c < nchunk) mma_chunk<MXA, WF, SWAP>(acc, a0, b0, g);
+  if (c < nchunk) mma_chunk<MXA, WF>(acc, a0, b0, g);
 }
 
 __device__ __forceinline__ bool tile_of(const FcArgs& p, int ti, Tile& t) {
@@ -260,9 +249,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
 }
 
 // FC2: obuf[a(p), n] = w(p) * (A W2^T)[p, n] for the wave's 64 columns n;
-// rows of A are rows of h in permuted order.  EPI (mx_linear): row p itself,
-// finished by the epilogue.
-template <bool MXA, int WF, bool EPI>
+// rows of A are rows of h in permuted order.
+template <bool MXA, int WF>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) void k_fc2_stream(FcArgs p) {
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int gw = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -288,24 +276,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 2))) voi
   for (int n = 0; n < NB; ++n) {
     // columns past N (a dense GEMM with N % 64 != 0) read the last weight
     // row and are not stored
-    const int j = 16 * n + r;
-    const int row = min(col0 + (EPI ? epi_row16(j) : j), H - 1);
+    const int row = min(col0 + 16 * n + r, H - 1);
     brow[n] = wb + (int64_t)row * wrow;
     bsrow[n] = sb + (int64_t)row * (K / 32);
   }
   v4f acc[NB];
 #pragma unroll
   for (int n = 0; n < NB; ++n) acc[n] = (v4f){0.f, 0.f, 0.f, 0.f};
-  mainloop<MXA, WF, EPI>(acc, arow, asrow, brow, bsrow, K / 128, g);
+  mainloop<MXA, WF>(acc, arow, asrow, brow, bsrow, K / 128, g);
 
-  if constexpr (EPI) {
-    const Epilogue e = epi_load();
-    EpiBias bias[NB / 2];
-    epi_biases(e, H, t.expert, col0 + 8 * g, 32, bias);
-    epi_row(e, H, t.p0 + r, t.p0 + t.rows, col0 + 8 * g, 32, bias,
-            [&](int q, int i) { return acc[2 * q + (i >> 2)][i & 3]; });
-    return;
-  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = 4 * g + i;
@@ -335,8 +314,7 @@ static hipError_t launch_pair(const FcArgs& p, bool fc1, hipStream_t st) {
   if (waves == 0) return hipSuccess;
   const int64_t blocks = (waves + 3) / 4;
   if (fc1) k_fc1_stream<MXA, WF><<<blocks, 256, 0, st>>>(p);
-  else if (p.linear) k_fc2_stream<MXA, WF, true><<<blocks, 256, 0, st>>>(p);
-  else k_fc2_stream<MXA, WF, false><<<blocks, 256, 0, st>>>(p);
+  else k_fc2_stream<MXA, WF><<<blocks, 256, 0, st>>>(p);
   return hipGetLastError();
 }
 

@@ -90,7 +90,7 @@ template <int TM> struct Grid {
 // are contiguous in both operands, so one 16-byte copy per row serves 4
 // stages (a 4-byte copy per row and stage costs one memory request per row
 // for 4 bytes, as many requests as the codes themselves).  K is a multiple of
-// 512, so an item's steps fill whole groups.
+// 512 (mx_linear: its steps are rounded up), so an item's steps fill whole groups.
 template <int WF, int TM> struct ALay {
   static_assert(TM % 64 == 0 && TM <= 256, "tile rows");
   // E3M2 stages of 256 weight rows (24 KB) leave room for 3 activation stages
@@ -160,6 +160,7 @@ struct ItemGeom {
 // the N-blocks of the ntiles % 8 remaining tiles.
 struct Sched {
   int xcd, full, tail0, q, Q, NB, nk, my_items, total;
+  int real;  // K stages of the operands, nk of them with mx_linear's padding
 };
 
 template <int TM>
@@ -198,6 +199,18 @@ __device__ __forceinline__ ItemGeom item_geom(const FcArgs& p, const Sched& sc, 
 __device__ __forceinline__ int k_stage(const Sched& sc, int nb, int ls) {
   const int s = ls + ((nb * sc.nk / sc.NB) & ~3);
   return s < sc.nk ? s : s - sc.nk;
+}
+
+// mx_linear takes any K >= 512 that is a multiple of 128: the steps of an item are
+// rounded up to whole scale groups.  A step past the end of K copies the last
+// stage once more and is not multiplied (K = 1408, 12 steps for 11 stages, costs
+// what K = 1536 costs, less a little); the last group's 16 bytes of scales end
+// where the row ends.
+template <bool EPI> __device__ __forceinline__ int code_stage(const Sched& sc, int ks) {
+  return EPI ? min(ks, sc.real - 1) : ks;
+}
+template <bool EPI> __device__ __forceinline__ int scale_stage(const Sched& sc, int ks) {
+  return EPI ? min(ks, sc.real - 4) : ks;
 }
 
 // weight row held at B-tile row jr of an N-block of TN rows; EPI: rows past N
@@ -329,16 +342,26 @@ __device__ __forceinline__ void multiply_role(const FcArgs& p, const Sched& sc, 
   int ci = 0, cs = 0;
   ItemGeom it = item_geom<TM>(p, sc, 0);
   int nm = wave_subs(it.rows);
-  if constexpr (EPI) bias_acc<kMaxSub>(acc, p.N, it.expert, it.nb * TN + 64 * wn + 8 * g);
+  int ks = 0;  // mx_linear: the step's K stage
+  if constexpr (EPI) {
+    bias_acc<kMaxSub>(acc, p.N, it.expert, it.nb * TN + 64 * wn + 8 * g);
+    ks = k_stage(sc, it.nb, 0);
+  }
   for (int gidx = 0; gidx < sc.total; ++gidx) {
     wait_lgkm0();  // this wave's reads of the previous stage are done
     barrier();
     const uint8_t* as = smem + L::A + (gidx % AL::STAGES) * AL::STAGE;
     const uint8_t* bs = smem + L::B + (gidx % BL::NBS) * BL::STAGE;
-    const int gb = (gidx >> 2) & 1, q = gidx & 3;
+    const int gb = (gidx >> 2) & 1;
+    int q = gidx & 3, subs = nm;
+    if constexpr (EPI) {
+      if (ks >= sc.real) subs = 0;
+      q += (ks & ~3) - scale_stage<EPI>(sc, ks & ~3);
+      if (++ks == sc.nk) ks = 0;
+    }
     const uint8_t* ags = smem + L::AS + gb * AL::GROUP + 4 * q;
     const uint8_t* bgs = smem + L::BS + gb * BL::GROUP + 4 * q;
-    switch (nm) {
+    switch (subs) {
       case 4: if constexpr (kMaxSub >= 4) compute_stage<WF, TM, 4, EPI>(acc, as, bs, ags, bgs, wm, brow0, brow1); break;
       case 3: if constexpr (kMaxSub >= 3) compute_stage<WF, TM, 3, EPI>(acc, as, bs, ags, bgs, wm, brow0, brow1); break;
       case 2: if constexpr (kMaxSub >= 2) compute_stage<WF, TM, 2, EPI>(acc, as, bs, ags, bgs, wm, brow0, brow1); break;
@@ -413,7 +436,10 @@ __device__ __forceinline__ void multiply_role(const FcArgs& p, const Sched& sc, 
     if (++ci < sc.my_items) {
       it = item_geom<TM>(p, sc, ci);
       nm = wave_subs(it.rows);
-      if constexpr (EPI) bias_acc<kMaxSub>(acc, p.N, it.expert, it.nb * TN + 64 * wn + 8 * g);
+      if constexpr (EPI) {
+        bias_acc<kMaxSub>(acc, p.N, it.expert, it.nb * TN + 64 * wn + 8 * g);
+        ks = k_stage(sc, it.nb, 0);
+      }
     }
   }
 }
@@ -483,7 +509,7 @@ __device__ __forceinline__ void activation_role(const FcArgs& p, const Sched& sc
       for (int i = 0; i < kACodeCopies; ++i)
         asrc[i] = (const uint8_t*)p.a + src_row(it, li, 8 * (kACodeCopies * aw + i) + (lane >> 3)) * K + 16 * c;
     }
-    const int ks = k_stage(sc, load_nb, ls);
+    const int ks = code_stage<EPI>(sc, k_stage(sc, load_nb, ls));
     const uint32_t base = lds0 + L::A + (issued % AL::STAGES) * AL::STAGE;
 #pragma unroll
     for (int i = 0; i < kACodeCopies; ++i) lds_copy16(asrc[i] + ks * TBK, base + 1024 * (kACodeCopies * aw + i));
@@ -506,7 +532,7 @@ __device__ __forceinline__ void activation_role(const FcArgs& p, const Sched& sc
       for (int i = 0; i < kGC; ++i)
         gsrc[i] = p.a_scale + src_row(it, gli, 64 * min(kGC * aw + i, AL::SCALE_CHUNKS - 1) + lane) * (K / 32);
     }
-    const int ks = k_stage(sc, gnb, gls);
+    const int ks = scale_stage<EPI>(sc, k_stage(sc, gnb, gls));
     const uint32_t base = lds0 + L::AS + (G & 1) * AL::GROUP;
 #pragma unroll
     for (int i = 0; i < kGC; ++i)
@@ -577,7 +603,7 @@ __device__ __forceinline__ void weight_role(const FcArgs& p, const Sched& sc, ui
   auto issue_stage = [&]() {
     if (ls == 0) setup(li);
     const uint32_t base = lds0 + L::B + (issued % BL::NBS) * BL::STAGE;
-    const int ks = k_stage(sc, load_nb, ls);
+    const int ks = code_stage<EPI>(sc, k_stage(sc, load_nb, ls));
     const int bo = ks * (TBK * Fmt<WF>::BITS / 8);
 #pragma unroll
     for (int i = 0; i < BL::PER_WAVE; ++i) lds_copy16(bsrc[i] + bo, base + 1024 * (BL::PER_WAVE * bw + i));
@@ -597,7 +623,7 @@ __device__ __forceinline__ void weight_role(const FcArgs& p, const Sched& sc, ui
         gsrc[i] = p.w_scale + (int64_t)it.expert * p.ws_estride +
                   w_row<FC1, TN, EPI>(p, it.nb, 64 * (kGC * bw + i) + lane) * (K / 32);
     }
-    const int ks = k_stage(sc, gnb, gls);
+    const int ks = scale_stage<EPI>(sc, k_stage(sc, gnb, gls));
 #pragma unroll
     for (int i = 0; i < kGC; ++i)
       lds_copy16(gsrc[i] + 4 * ks, lds0 + L::BS + (G & 1) * BL::GROUP + 1024 * (kGC * bw + i));
@@ -628,7 +654,8 @@ template <bool FC1, int WF, int TM, bool DENSE, bool EPI>
 __global__ __launch_bounds__(kThreads, 1) void k_fc_tiled(FcArgs p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[Lds<WF, TM>::TOTAL];
   Sched sc;
-  sc.nk = p.K / TBK;
+  sc.real = p.K / TBK;
+  sc.nk = EPI ? (sc.real + 3) & ~3 : sc.real;
   sc.NB = p.nchunks;
   const int ntiles = p.dense_rows > 0 ? (p.dense_rows + TM - 1) / TM : *p.num_tiles;
   sc.xcd = blockIdx.x & 7;

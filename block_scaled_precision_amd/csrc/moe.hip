@@ -599,19 +599,23 @@ static bool linear_supported(const mx_linear_problem_t& p) {
 
 // Choice of the kernel: the smallest of the estimated times below, in
 // microseconds, which follow the kernels' structure: items over kLinearWgs
-// workgroups, rounds of them, steps of K per item, and a measured time per step
-// (MI355X, N = 4096, K = 7168 unless noted; the products themselves, without what
-// every call pays for its launch):
+// workgroups, rounds of them, steps of K per item, a measured time per step and one
+// per item for its epilogue (MI355X; without what every call pays for its launch):
 //   few rows (gemm_few.hip; 16 x 16 items, 1024 K a step)  E2M1 x bf16: 1 row 0.43,
-//     16 rows 1.0; E3M2 0.2 more; MXFP8 0.4 more (it quantizes in place)
+//     16 rows 1.0; E3M2 0.2 more; MXFP8 0.4 more, 0.8 up to K = 1024 (it quantizes in
+//     place); twice that with groups, whose weights come from HBM (184 rows over 69 experts, 1840 x 896: 42 us, 16-row tiles 21)
 //   rows (gemm_rows.hip; 256 K a step)  16 x 128 items: E2M1 0.55, E3M2 1.0;
-//     64 x 128 items: E2M1 1.2 (bf16), 0.75 (MXFP8), E3M2 1.75, 1.4
-//   mid (E2M1 x bf16; 128 K a step)  64 x 256 items 1.08, 128 x 256 1.6
-//   tiled (MXFP8)  128 x 256 items 1.0, 192 x 128 0.92 (E2M1), 1.05 (E3M2)
-//   wide (E2M1 x MXFP8)  192 x 256 items 1.2
-// E.g. 64 rows of bf16 x E2M1: few 40, 16-row tiles in two K ranges 16.7, 64-row
-// tiles in four 17.3, mid 66; 8192 rows: 64-row tiles 606, mid 423.  A call that
-// streams every expert's weights is bound by that instead (kWeightRate).
+//     64 x 128 items: E2M1 1.1 (bf16), 0.75 (MXFP8), E3M2 1.75, 1.4; 1.15
+//     times that with groups
+//   mid (E2M1 x bf16; 128 K a step)  64 x 256 items 1.06, 128 x 256 1.6
+//   tiled (MXFP8)  128 x 256 items 1.08, E3M2 1.3; 192 x 128 0.88, 1.1
+//   wide (E2M1 x MXFP8)  192 x 256 items 1.27
+//   epilogues with a residual: 13.6 us per 128 x 256 item of mid, 9.6 of tiled, 18 of
+//     wide's, 4.3 of 64 x 128 (8192 x 4096, K = 1024 and 7168)
+// E.g. 64 rows of bf16 x E2M1, N = 4096, K = 7168: few 40, 16-row tiles in two K
+// ranges 16.1, 64-row tiles in four 16.5, mid 66; 8192 rows: 64-row tiles 547, mid
+// 433; 8192 rows of MXFP8 x E2M1: K = 7168 wide 276, tiled 288; K = 1024 wide 93, tiled
+// 81.  A call that streams every expert's weights is bound by that (kWeightRate).
 // Sizes only, so that the workspace does not depend on the device.
 constexpr int kLinearWgs = 256;
 constexpr double kWeightRate = 5.2e6;  // bytes per microsecond from HBM
@@ -639,9 +643,9 @@ struct LinearCost {
   double time(int bm, int bn, double steps, double t, int ksplit = 1) const {
     const double items = tiles(bm) * std::ceil(p.N / (double)bn) * ksplit;
     double rounds = items / kLinearWgs;
-    if (p.groups == 0 || rounds < 1.0) rounds = std::ceil(rounds);
+    if (p.groups == 0 || rounds < 8.0) rounds = std::ceil(rounds);  // (else the tile count is too rough)
     const double weights = active * p.N * (double)p.K * (wbits(p.w_fmt) / 8.0 + 1.0 / 32.0) / kWeightRate;
-    return std::max(rounds * std::ceil(steps / ksplit) * t, weights);
+    return std::max(rounds * (std::ceil(steps / ksplit) * t + 1.0 + 0.3 / 1024.0 * bm * bn), weights);
   }
   double quant_time() const { return quant ? 3.5 + (double)p.M * p.K * 3.0 / 3.5e6 : 0.0; }
   double join_time(int ksplit) const { return ksplit > 1 ? 4.5 + (double)ksplit * p.M * p.N * 8.0 / 4.0e6 : 0.0; }
@@ -660,35 +664,38 @@ static void linear_kind(const mx_linear_problem_t& p, bool has_a_scale, LinearPl
   };
   // (its grid has one workgroup per item)
   if (c.tiles(16) * (p.N / 16) <= 1 << 20) {
-    const double t = 0.43 + 0.57 * std::min(c.per, 16.0) / 16.0 + (e2m1 ? 0.0 : 0.2) + (mx ? 0.4 : 0.0);
-    take(Fc::kFew, kStreamRows, 0, c.time(16, 16, std::ceil(p.K / 2048.0) * 2.0, t));
+    const double more = (e2m1 ? 0.0 : 0.2) + (!mx ? 0.0 : p.K <= 1024 ? 0.8 : 0.4);
+    const double t = (p.groups > 0 ? 2.0 : 1.0) * (0.43 + 0.57 * std::min(c.per, 16.0) / 16.0 + more);
+    // (with bf16 several of its workgroups share a CU: no whole rounds)
+    const double steps = p.K <= 1024 ? 1.0 : std::ceil(p.K / 2048.0) * 2.0;
+    const double rounds = std::max(1.0, c.tiles(16) * (p.N / 16) / kLinearWgs);
+    take(Fc::kFew, kStreamRows, 0, mx ? c.time(16, 16, steps, t) : 1.0 + rounds * t * steps);
   }
-  if (p.K >= kRowsMinK) {
-    const double steps = std::ceil(p.K / (double)kRowsK);
-    const double t16 = e2m1 ? 0.55 : 1.0, t64 = e2m1 ? (mx ? 0.75 : 1.2) : (mx ? 1.4 : 1.75);
-    // K ranges of at least two stages, dense calls only
-    const int most = p.groups > 0 ? 1 : (int)std::min(16.0, std::max(1.0, std::floor(steps / 2.0)));
-    for (int s = 1; s <= most; ++s) {
-      const double more = c.quant_time() + c.join_time(s);
-      take(Fc::kRows, 16, s, c.time(16, kRowsCols, steps, t16, s) + more);
-      take(Fc::kRows, 64, s, c.time(64, kRowsCols, steps, t64, s) + more);
-    }
-  } else {
-    // short K: the stream kernel reads weights straight into the MFMA layout
-    take(Fc::kStream, kStreamRows, 0, c.time(16, 4 * kStreamColsFc2, p.K / 128.0, 1.2) + c.quant_time());
+  const double stages = std::ceil(p.K / (double)kRowsK);
+  const double own = p.groups > 0 ? 1.15 : 1.0;  // groups share no weights in the caches
+  const double t16 = own * (e2m1 ? 0.55 : 1.0), t64 = own * (e2m1 ? (mx ? 0.75 : 1.1) : (mx ? 1.4 : 1.75));
+  // K ranges of at least two stages, dense calls only
+  const int most = p.groups > 0 ? 1 : (int)std::min(16.0, std::max(1.0, std::floor(stages / 2.0)));
+  for (int s = 1; s <= most; ++s) {
+    const double more = c.quant_time() + c.join_time(s);
+    take(Fc::kRows, 16, s, c.time(16, kRowsCols, stages, t16, s) + more);
+    take(Fc::kRows, 64, s, c.time(64, kRowsCols, stages, t64, s) + more);
   }
-  const double steps = p.K / 128.0;
-  if (!mx && e2m1 && p.K % kMidK == 0) {
-    take(Fc::kMid, kMidRows, 0, c.time(kMidRows, kWideCols, steps, 1.08));
+  // (whole scale groups of 512 K)
+  if (p.K < kMidK) return;
+  const double steps = std::ceil(p.K / (double)kMidK) * (kMidK / 128);
+  if (!mx && e2m1) {
+    take(Fc::kMid, kMidRows, 0, c.time(kMidRows, kWideCols, steps, 1.06));
     take(Fc::kMid, kMidRowsHigh, 0, c.time(kMidRowsHigh, kWideCols, steps, 1.6));
   }
-  if (mx && p.K % kTiledKMultiple == 0) {
-    take(Fc::kTiled, kTiledRowsLow, 0, c.time(128, tiled_weight_rows(kTiledRowsLow), steps, 1.0) + c.quant_time());
+  if (mx) {
+    take(Fc::kTiled, kTiledRowsLow, 0,
+         c.time(128, tiled_weight_rows(kTiledRowsLow), steps, e2m1 ? 1.08 : 1.3) + c.quant_time());
     take(Fc::kTiled, kTiledRows, 0,
-         c.time(192, tiled_weight_rows(kTiledRows), steps, e2m1 ? 0.92 : 1.05) + c.quant_time());
+         c.time(192, tiled_weight_rows(kTiledRows), steps, e2m1 ? 0.88 : 1.1) + c.quant_time());
     // (its 32-bit offsets into A, and column blocks of 64 inside N)
-    if (e2m1 && p.K >= 1024 && p.N % 64 == 0 && (double)p.M * p.K < 4294967296.0)
-      take(Fc::kWide, kTiledRows, 0, c.time(192, kWideCols, steps, 1.2) + c.quant_time());
+    if (e2m1 && p.K >= 1024 && p.K % kTiledKMultiple == 0 && p.N % 64 == 0 && (double)p.M * p.K < 4294967296.0)
+      take(Fc::kWide, kTiledRows, 0, c.time(192, kWideCols, steps, 1.27) + c.quant_time());
   }
 }
 
@@ -804,7 +811,7 @@ extern "C" moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_
     case Fc::kWide: e = launch_fc_wide(g, false, cus, stream); break;
     case Fc::kTiled: e = launch_fc_tiled(g, false, wf, f.rows, cus, stream); break;
     case Fc::kFew: e = launch_linear_few(g, mx, quant, wf, stream); break;
-    default: e = launch_fc_stream(g, false, mx, wf, stream);
+    default: return MOE_ERR_UNSUPPORTED;  // linear_kind chooses no other
   }
   return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

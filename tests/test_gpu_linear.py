@@ -68,6 +68,8 @@ DENSE = [
     (300, 256, 512, "e3m2", "mxfp8"), (192, 128, 1536, "e3m2", "mxfp8"), (40, 136, 256, "e3m2", "mxfp8"),
     (129, 504, 896, "e3m2", "mxfp8"), (16, 256, 512, "e3m2", "mxfp8"), (2, 640, 3584, "e2m1", "mxfp8"),
 ]
+DENSE += [(M, 520, K, f, a) for M, K in ((1900, 128), (700, 256), (1500, 384), (20, 384), (1300, 896), (1300, 640),
+                                         (2100, 1152)) for f in ("e2m1", "e3m2") for a in ("bf16", "mxfp8")]
 IDS = [f"{M}x{N}x{K}_{f}_{a}" for M, N, K, f, a in DENSE]
 
 
