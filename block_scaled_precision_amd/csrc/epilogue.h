@@ -50,13 +50,32 @@ __device__ __forceinline__ int epi_lane() {
 }
 
 // SiLU through t = exp(-|v|) <= 1, so that the tail of negative v does not pass
-// through an overflowing exp(-v); erfc rather than 1 + erf: for negative v the
-// sum would cancel, leaving an error relative to v instead of to the result
+// through an overflowing exp(-v).  1 + t lies in [1, 2], where the reciprocal
+// instruction is good to a step.
 __device__ __forceinline__ float silu(float v) {
   const float t = expf(-fabsf(v));
-  return v * (v < 0.0f ? t : 1.0f) / (1.0f + t);
+  return v * (v < 0.0f ? t : 1.0f) * __builtin_amdgcn_rcpf(1.0f + t);
 }
-__device__ __forceinline__ float gelu(float v) { return 0.5f * v * erfcf(-0.70710678f * v); }
+// GELU: v Phi(v), with Phi(-|v|) = erfc(x) / 2 at x = |v| / sqrt(2), which keeps the
+// tail of negative v accurate relative to itself (1 + erf would cancel).  erfc(x) =
+// exp(-x^2) t P(t), t = 1 / (1 + x/2): P is a weighted least-squares fit of degree 8 to
+// erfcx(x) / t over x in [0, 14], off by at most 4.5e-8 of the value; beyond it the
+// product is 0.  In fp32 the result is within 7 + 2 v^2 half steps of its value.
+// (4674 x 7464 x 1280, E2M1 x bf16: 130 us, with erfcf 152, without a function 116.)
+__device__ __forceinline__ float gelu(float v) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.35355339f, fabsf(v), 1.0f));
+  float p = -5.938633031e-02f;
+  p = fmaf(p, t, 2.861234119e-01f);
+  p = fmaf(p, t, -4.904054181e-01f);
+  p = fmaf(p, t, 2.817324350e-01f);
+  p = fmaf(p, t, -2.914813096e-02f);
+  p = fmaf(p, t, 2.037524415e-01f);
+  p = fmaf(p, t, 2.428351139e-01f);
+  p = fmaf(p, t, 2.824121019e-01f);
+  p = fmaf(p, t, 2.820843310e-01f);
+  const float q = 0.5f * t * p * __builtin_amdgcn_exp2f(-0.72134752f * (v * v));  // exp(-v^2 / 2)
+  return v * (v < 0.0f ? q : 1.0f - q);
+}
 __device__ __forceinline__ float relu2(float v) {
   const float r = fmaxf(v, 0.0f);
   return r * r;
