@@ -236,64 +236,62 @@ __global__ __launch_bounds__(kThreadsD) void k_gather_sum(RowMap m, const T* __r
 }
 
 // drows[row_of[t, j]] = w[t, j] dy[t] and dw[t, j] = <dy[t], rows[row_of[t, j]]>:
-// one workgroup per token; the slots are taken kSlots at a time, each thread
-// holding one partial dot product per slot over its pieces of the row.
-template <typename T, int V, bool STREAM>
-__global__ __launch_bounds__(kThreadsD) void k_unpermute_grad(int64_t tokens, int pieces, const T* __restrict__ dy,
-                                                              int64_t dy_ld, const T* __restrict__ rows,
-                                                              int64_t rows_ld, int num_rows,
-                                                              const int32_t* __restrict__ row_of,
-                                                              const float* __restrict__ w, int k,
-                                                              T* __restrict__ drows, int64_t drows_ld,
-                                                              float* __restrict__ dw) {
+// one workgroup of TH threads per Q slots of a token, each thread holding one
+// partial dot product per slot over its pieces of the row.
+template <typename T, int V, bool STREAM, int TH, int Q>
+__global__ __launch_bounds__(TH) void k_unpermute_grad(int64_t tokens, int pieces, const T* __restrict__ dy,
+                                                       int64_t dy_ld, const T* __restrict__ rows, int64_t rows_ld,
+                                                       int num_rows, const int32_t* __restrict__ row_of,
+                                                       const float* __restrict__ w, int k, T* __restrict__ drows,
+                                                       int64_t drows_ld, float* __restrict__ dw) {
   using P = Pack<T, V>;
-  __shared__ float part[kThreadsD / 64][kSlots];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
-    for (int j0 = 0; j0 < k; j0 += kSlots) {
-      int32_t p[kSlots];
-      float wt[kSlots], dot[kSlots];
+  __shared__ float part[TH / 64][Q];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, parts = (k + Q - 1) / Q;
+  for (int64_t i = blockIdx.x; i < tokens * parts; i += gridDim.x) {
+    const int64_t t = i / parts;
+    const int j0 = Q * (int)(i % parts);
+    int32_t p[Q];
+    float wt[Q], dot[Q];
 #pragma unroll
-      for (int q = 0; q < kSlots; ++q) {
-        p[q] = j0 + q < k ? row_of[t * k + j0 + q] : -1;
-        if (p[q] >= num_rows) p[q] = -1;
-        wt[q] = p[q] >= 0 ? w[t * k + j0 + q] : 0.f;
-        dot[q] = 0.f;
-      }
-      for (int c = threadIdx.x; c < pieces; c += kThreadsD) {
-        const P g = *(const P*)(dy + t * dy_ld + (int64_t)c * V);
-        P v[kSlots];
-#pragma unroll
-        for (int q = 0; q < kSlots; ++q)
-          if (p[q] >= 0) v[q] = load_piece<STREAM>((const P*)(rows + (int64_t)p[q] * rows_ld + (int64_t)c * V));
-#pragma unroll
-        for (int q = 0; q < kSlots; ++q)
-          if (p[q] >= 0) {
-            P o;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              const float gi = to_f32(g.v[i]);
-              dot[q] = fmaf(gi, to_f32(v[q].v[i]), dot[q]);
-              o.v[i] = (T)(wt[q] * gi);
-            }
-            store_piece<STREAM>((P*)(drows + (int64_t)p[q] * drows_ld + (int64_t)c * V), o);
-          }
-      }
-#pragma unroll
-      for (int q = 0; q < kSlots; ++q) {
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) dot[q] += __shfl_xor(dot[q], d);
-        if (lane == 0) part[wv][q] = dot[q];
-      }
-      __syncthreads();
-      if (threadIdx.x < kSlots && j0 + (int)threadIdx.x < k) {
-        float s = part[0][threadIdx.x];
-#pragma unroll
-        for (int i = 1; i < kThreadsD / 64; ++i) s += part[i][threadIdx.x];
-        dw[t * k + j0 + threadIdx.x] = s;
-      }
-      __syncthreads();
+    for (int q = 0; q < Q; ++q) {
+      p[q] = j0 + q < k ? row_of[t * k + j0 + q] : -1;
+      if (p[q] >= num_rows) p[q] = -1;
+      wt[q] = p[q] >= 0 ? w[t * k + j0 + q] : 0.f;
+      dot[q] = 0.f;
     }
+    for (int c = threadIdx.x; c < pieces; c += TH) {
+      const P g = *(const P*)(dy + t * dy_ld + (int64_t)c * V);
+      P v[Q];
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        if (p[q] >= 0) v[q] = load_piece<STREAM>((const P*)(rows + (int64_t)p[q] * rows_ld + (int64_t)c * V));
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        if (p[q] >= 0) {
+          P o;
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float ge = to_f32(g.v[e]);
+            dot[q] = fmaf(ge, to_f32(v[q].v[e]), dot[q]);
+            o.v[e] = (T)(wt[q] * ge);
+          }
+          store_piece<STREAM>((P*)(drows + (int64_t)p[q] * drows_ld + (int64_t)c * V), o);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) dot[q] += __shfl_xor(dot[q], d);
+      if (lane == 0) part[wv][q] = dot[q];
+    }
+    __syncthreads();
+    if (threadIdx.x < Q && j0 + (int)threadIdx.x < k) {
+      float s = part[0][threadIdx.x];
+#pragma unroll
+      for (int u = 1; u < TH / 64; ++u) s += part[u][threadIdx.x];
+      dw[t * k + j0 + threadIdx.x] = s;
+    }
+    __syncthreads();
   }
 }
 
@@ -479,16 +477,33 @@ extern "C" moe_status_t moe_unpermute(const void* rows, moe_src_t dtype, int64_t
   return gather_sum(rows, dtype, rows_ld, num_rows, row_of, topk_w, T, H, k, residual, residual_ld, y, y_ld, stream);
 }
 
+// A workgroup takes a token with all of its slots, so that dy is read once (4096 x
+// 2048 bf16, k = 6: 43 us, 50 with a workgroup per slot).  Otherwise one per slot:
+// a wave where rows are narrow and four would mostly wait for their sums (4096 x 864
+// bf16, k = 8: 31 us against 45; 4096 x 267, k = 4: 10 against 18), and where there are
+// few tokens 256 threads (64 x 2048, k = 6: 4.8 against 6.0) or, for rows of two pieces
+// per thread and more, 1024 (64 x 27392, k = 3: 7 against 24; 11 x 7168, k = 8: 4.9
+// against 10.6).  From 1024 tokens of 2048 or more values on the first is as fast.
+constexpr int kNarrowRow = 1024;  // values
+constexpr int kFewTokens = 256;
 template <typename T, int V>
 static void launch_unpermute_grad(const void* dy, int64_t dy_ld, const void* rows, int64_t rows_ld, int32_t num_rows,
                                   const int32_t* row_of, const float* w, int32_t tokens, int32_t H, int32_t k,
                                   void* drows, int64_t drows_ld, float* dw, hipStream_t st) {
-#define MOE_UNPERMUTE_GRAD(S)                                                                                      \
-  k_unpermute_grad<T, V, S><<<grid_blocks(tokens), kThreadsD, 0, st>>>(tokens, H / V, (const T*)dy, dy_ld,         \
-                                                                       (const T*)rows, rows_ld, num_rows, row_of,  \
-                                                                       w, k, (T*)drows, drows_ld, dw)
-  if ((int64_t)tokens * H * (int64_t)sizeof(T) >= kStreamBytes) MOE_UNPERMUTE_GRAD(true);
-  else MOE_UNPERMUTE_GRAD(false);
+#define MOE_UNPERMUTE_GRAD(S, TH, Q)                                                                               \
+  k_unpermute_grad<T, V, S, TH, Q><<<grid_blocks((int64_t)tokens * ((k + Q - 1) / Q)), TH, 0, st>>>(               \
+      tokens, H / V, (const T*)dy, dy_ld, (const T*)rows, rows_ld, num_rows, row_of, w, k, (T*)drows, drows_ld, dw)
+  const bool stream = (int64_t)tokens * H * (int64_t)sizeof(T) >= kStreamBytes;
+  if (H <= kNarrowRow) {
+    if (stream) MOE_UNPERMUTE_GRAD(true, 64, 1);
+    else MOE_UNPERMUTE_GRAD(false, 64, 1);
+  } else if (tokens <= kFewTokens) {
+    if (H / V >= 2 * 1024) MOE_UNPERMUTE_GRAD(false, 1024, 1);
+    else MOE_UNPERMUTE_GRAD(false, kThreadsD, 1);
+  } else {
+    if (stream) MOE_UNPERMUTE_GRAD(true, kThreadsD, kSlots);
+    else MOE_UNPERMUTE_GRAD(false, kThreadsD, kSlots);
+  }
 #undef MOE_UNPERMUTE_GRAD
 }
 

@@ -54,7 +54,8 @@ def _rand(shape, seed, dtype):
 CASES = [
     (1, 7168, 384, 8, 0, 0), (1, 1, 1, 1, 0, 0), (5, 333, 7, 3, 0, 0), (3, 8, 4, 4, 1, 2), (64, 1024, 32, 8, 0, 0),
     (64, 1024, 32, 8, 16, 16), (257, 72, 20, 11, 0, 0), (33, 4104, 64, 17, 7, 1), (130, 520, 512, 6, 100, 300),
-    (2, 64, 16, 2, 15, 1),
+    (2, 64, 16, 2, 15, 1), (11, 16896, 8, 3, 0, 0), (3, 4100, 16, 12, 2, 9), (256, 1032, 8, 2, 0, 0),
+    (300, 1544, 32, 11, 0, 0), (9000, 1000, 8, 2, 0, 0), (4500, 2000, 8, 2, 0, 0),
 ]
 
 
