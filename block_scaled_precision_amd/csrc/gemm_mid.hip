@@ -43,6 +43,7 @@ namespace {
 
 constexpr int MBN = kWideCols;  // weight rows per item
 constexpr int MBK = 128;        // K per stage
+constexpr int kTouchSteps = 6;  // mx_linear: copied steps left when the epilogue's operands are requested
 constexpr int GS = 4;           // stages per scale group
 constexpr int NG = 2;           // scale-group buffers
 constexpr int B_ROW = MBK / 2;  // 64 B of codes per weight row and stage
@@ -65,7 +66,8 @@ template <int TM> struct ML {
   static constexpr int S_A = TM * A_ROW;
   static constexpr int S_STAGE = S_B + S_A;
   static constexpr int L_SG = NSTG * S_STAGE;
-  static constexpr int L_TOTAL = L_SG + NG * G_BYTES;
+  static constexpr int L_TOUCH = L_SG + NG * G_BYTES;  // epi_touch's
+  static constexpr int L_TOTAL = L_TOUCH + 256;
   static constexpr int MUL_WAVES = TM / 16;
   static constexpr int THREADS = 64 * (MUL_WAVES + 4);
   static constexpr int A_COPIES = S_A / 1024 / 2;  // 1-KB copies per activation wave and stage
@@ -413,8 +415,13 @@ __device__ __forceinline__ void mid_activations(const FcArgs& p, const MSched& s
     }
   };
   int li = 0, ls = 0, issued = 0;
+  const int touch = EPI ? max(0, sc.nk - kTouchSteps) : -1;
   auto issue_next = [&]() {
     if (ls == 0) setup(li);
+    if (EPI && ls == touch) {
+      const MGeom it = m_geom<TM>(p, sc, li);
+      epi_touch<TM / 2, MBN>(p.epi, p.N, it.p0 + TM / 2 * aw, it.p0 + it.rows, it.nb * MBN, lds0 + L::L_TOUCH);
+    }
     const uint32_t base = lds0 + (issued % L::NSTG) * L::S_STAGE + S_B;
 #pragma unroll
     for (int i = 0; i < kACopies; ++i) lds_copy16(src[i] + code_stage<EPI>(sc, ls) * A_ROW, base + 1024 * (kACopies * aw + i));

@@ -482,18 +482,39 @@ __device__ __forceinline__ void mul_step(v4f (&acc)[kSubs][kTiles], Frags& f, co
   }
 }
 
+// mx_linear: requests the wave's part of an item's second factors and residuals, a
+// word of each 128-byte line, copied to LDS that nothing reads (the row tables',
+// which it does without), so that the epilogue, which has registers for one piece at
+// a time, finds them in L2 (8192 x 4096 x 7168 with a residual: 264 us, 273 without;
+// K = 1024 88 and 92; requested an item ahead 267 and 89).
+constexpr int kTouchSteps = 6;  // steps before the item's end
+__device__ __forceinline__ void touch(const FcArgs& p, const ItemGeom& it, uint32_t lds, int wm, int wn) {
+  const Epilogue e = epi_load();
+  const int el = epi_lane();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = min(64 * i + el, 95);  // 3 sub-blocks of 16 rows, two lines each
+    const int r = min(16 * (wm + 4 * (j >> 5)) + (j & 15), it.rows - 1);
+    const int c = min(it.nb * TBN + 128 * wn + 64 * ((j >> 4) & 1), p.N - 2);
+    const int64_t o = (int64_t)(it.p0 + r) * p.N + c;
+    if (e.mul) lds_copy4(e.mul + o, lds);
+    if (e.residual) lds_copy4(e.residual + o, lds);
+  }
+}
+
 // The nk steps of one item for a wave holding NM sub-blocks, from global step
 // gbase.  Before barrier g the wave's own copies for step g+1 (code stage and,
 // at a group start, scale group) have landed and its reads of step g's data
 // are complete; after it, the wave copies its next stage into the buffer step g
 // used (and, after a group's last step, the group after next into that group's
 // buffer) and multiplies step g while reading step g+1's fragments (past the
-// last step the reads hit a stale buffer and go unused).
+// last step the reads hit a stale buffer and go unused).  nk >= 8.
 template <int NM, bool SWAP, class Copier>
 __device__ __forceinline__ void item_steps(const FcArgs& p, const Sched& sc, v4f (&acc)[kSubs][kTiles], Frags& f,
-                                           const LaneOffs& o, uint8_t* smem, Copier& cp, int wm, int gbase) {
+                                           const LaneOffs& o, uint8_t* smem, Copier& cp, int wm, int gbase, const ItemGeom& it, int wn) {
   for (int s = 0; s < sc.nk; ++s) {
     const int g = gbase + s;
+    if (SWAP && s == sc.nk - kTouchSteps) touch(p, it, lds_addr(smem) + L_TBL, wm, wn);
     if (g + kTailWaits < sc.total) cp.wait_for(g);
     else wait_vm_lgkm0<0>();
     barrier();
@@ -537,10 +558,10 @@ __device__ __forceinline__ void wave_main(const FcArgs& p, const Sched& sc, uint
   for (int ci = 0; ci < sc.my_items; ++ci) {
     // one step loop per sub-block count, so that the accumulators stay in place
     switch (nm) {
-      case 3: item_steps<3, EPI>(p, sc, acc, f, o, smem, cp, wm, gbase); break;
-      case 2: item_steps<2, EPI>(p, sc, acc, f, o, smem, cp, wm, gbase); break;
-      case 1: item_steps<1, EPI>(p, sc, acc, f, o, smem, cp, wm, gbase); break;
-      default: item_steps<0, EPI>(p, sc, acc, f, o, smem, cp, wm, gbase); break;
+      case 3: item_steps<3, EPI>(p, sc, acc, f, o, smem, cp, wm, gbase, it, wn); break;
+      case 2: item_steps<2, EPI>(p, sc, acc, f, o, smem, cp, wm, gbase, it, wn); break;
+      case 1: item_steps<1, EPI>(p, sc, acc, f, o, smem, cp, wm, gbase, it, wn); break;
+      default: item_steps<0, EPI>(p, sc, acc, f, o, smem, cp, wm, gbase, it, wn); break;
     }
     gbase += sc.nk;
 
@@ -555,8 +576,8 @@ __device__ __forceinline__ void wave_main(const FcArgs& p, const Sched& sc, uint
         const Epilogue e = epi_load();
         const int el = epi_lane();
         const int col = it.nb * TBN + 128 * wn + 8 * (el >> 4), row = 16 * (wm + 4 * m) + (el & 15);
-        // (one piece at a time: two or four in flight measured 3% and 1% slower
-        // over 8192 x 4096 x 7168, spilling around the epilogue)
+        // (one piece at a time: with two to four in flight registers spill, 339 us and
+        // more over 8192 x 4096 x 7168)
 #pragma unroll
         for (int q = 0; q < kTiles / 2; ++q) {
           EpiBias bias[1];
