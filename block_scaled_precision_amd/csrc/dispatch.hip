@@ -117,10 +117,10 @@ __device__ __forceinline__ void store_piece(P* p, const P& v) {
 }
 // Outputs from this size on are stored past the caches, and the rows of
 // moe_unpermute_backward, whose rows and drows then exceed them several times
-// over, are loaded past them too.  (fp32 gradient of 4096 x 4096 tokens: 52 us
-// against 55; 2047 x 5120 bf16 tokens, half of their rows local: 22.4 against 34,
-// as the rows stay in the last-level cache; gradient of 8192 x 4096 bf16 tokens:
-// 226 against 239.  Outputs of decode batches stay cached for their reader.)
+// over, are loaded past them too.  (With a piece per thread: gradient of 4096 x 4096
+// fp32 tokens 52 us against 55; 2047 x 5120 bf16 tokens, half of their rows local, 22.4
+// against 34, as the rows stay in the last-level cache; gradient of 8192 x 4096 bf16
+// tokens 226 against 239.  Outputs of decode batches stay cached for their reader.)
 constexpr int64_t kStreamBytes = 16 << 20;
 
 // ------------------------------------------------------------- permute ---
@@ -190,28 +190,42 @@ __global__ __launch_bounds__(kThreadsD) void k_permute_rows(RowMap m, const P* _
 
 // ----------------------------------------------------------- unpermute ---
 
-// y[t] = residual[t] + sum over slots j of (w[t, j]) rows[row_of[t, j]]
-template <typename T, int V, bool WEIGHTED, bool STREAM>
+// y[t] = residual[t] + sum over slots j of (w[t, j]) rows[row_of[t, j]]; U pieces,
+// tpr apart, per thread.  A thread waits for row_of and then for the rows; in large
+// calls several pieces per wait keep more of them in flight (gradients of permute:
+// 4096 x 4096 fp32 tokens with a quarter of their rows 43 against 55 us, bf16 17.5
+// against 40; 8192 x 7168 bf16 198 against 247; 4096 x 4095 bf16 in elements 74
+// against 175).  Four pieces of 16 bytes take too many registers (8192 x 7168 with
+// weights 463 us against 255).
+template <typename T, int V, bool WEIGHTED, bool STREAM, int U>
 __global__ __launch_bounds__(kThreadsD) void k_gather_sum(RowMap m, const T* __restrict__ rows, int64_t rows_ld,
                                                           int num_rows, const int32_t* __restrict__ row_of,
                                                           const float* __restrict__ w, int k, const T* residual,
                                                           int64_t res_ld, T* y, int64_t y_ld) {
   using P = Pack<T, V>;
   for (int64_t b = blockIdx.x; b < m.nblocks; b += gridDim.x) {
-    int64_t t;
-    int c;
-    if (!row_piece(m, b, t, c)) continue;
-    float s[V];
-    if (residual) {
-      const P r = *(const P*)(residual + t * res_ld + (int64_t)c * V);
+    const int64_t rb = b / m.cblocks;
+    const int cb = (int)(b - rb * m.cblocks);
+    const int64_t t = rb * (kThreadsD >> m.lg) + (threadIdx.x >> m.lg);
+    const int c0 = cb * m.tpr * U + (threadIdx.x & (m.tpr - 1));
+    if (t >= m.nrows || c0 >= m.pieces) continue;
+    int64_t c[U];  // past the row: its last piece again, not stored
 #pragma unroll
-      for (int q = 0; q < V; ++q) s[q] = to_f32(r.v[q]);
-    } else {
+    for (int u = 0; u < U; ++u) c[u] = (int64_t)min(c0 + u * m.tpr, m.pieces - 1) * V;
+    float s[U][V];
 #pragma unroll
-      for (int q = 0; q < V; ++q) s[q] = 0.f;
+    for (int u = 0; u < U; ++u) {
+      if (residual) {
+        const P r = *(const P*)(residual + t * res_ld + c[u]);
+#pragma unroll
+        for (int q = 0; q < V; ++q) s[u][q] = to_f32(r.v[q]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < V; ++q) s[u][q] = 0.f;
+      }
     }
     for (int j0 = 0; j0 < k; j0 += kSlots) {
-      P v[kSlots];
+      P v[kSlots][U];
       float wt[kSlots];
       bool use[kSlots];
 #pragma unroll
@@ -219,19 +233,28 @@ __global__ __launch_bounds__(kThreadsD) void k_gather_sum(RowMap m, const T* __r
         const int32_t p = j0 + q < k ? row_of[t * k + j0 + q] : -1;
         use[q] = p >= 0 && p < num_rows;
         wt[q] = WEIGHTED && use[q] ? w[t * k + j0 + q] : 1.f;
-        if (use[q]) v[q] = *((const P*)(rows + (int64_t)p * rows_ld + (int64_t)c * V));
+        if (use[q]) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) v[q][u] = *((const P*)(rows + (int64_t)p * rows_ld + c[u]));
+        }
       }
 #pragma unroll
       for (int q = 0; q < kSlots; ++q)
         if (use[q]) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) s[i] = WEIGHTED ? fmaf(wt[q], to_f32(v[q].v[i]), s[i]) : s[i] + to_f32(v[q].v[i]);
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              s[u][i] = WEIGHTED ? fmaf(wt[q], to_f32(v[q][u].v[i]), s[u][i]) : s[u][i] + to_f32(v[q][u].v[i]);
         }
     }
-    P o;
 #pragma unroll
-    for (int q = 0; q < V; ++q) o.v[q] = (T)s[q];
-    store_piece<STREAM>((P*)(y + t * y_ld + (int64_t)c * V), o);
+    for (int u = 0; u < U; ++u) {
+      P o;
+#pragma unroll
+      for (int q = 0; q < V; ++q) o.v[q] = (T)s[u][q];
+      if (c0 + u * m.tpr < m.pieces) store_piece<STREAM>((P*)(y + t * y_ld + c[u]), o);
+    }
   }
 }
 
@@ -361,16 +384,25 @@ template <typename T, int V>
 void launch_gather_sum(const void* rows, int64_t rows_ld, int32_t num_rows, const int32_t* row_of, const float* w,
                        int32_t T_, int32_t H, int32_t k, const void* residual, int64_t res_ld, void* y, int64_t y_ld,
                        hipStream_t st) {
-  const RowMap m = row_map(T_, H / V);
-  const unsigned g = grid_blocks(m.nblocks);
+  RowMap m = row_map(T_, H / V);
   const bool stream = (int64_t)T_ * H * (int64_t)sizeof(T) >= kStreamBytes;
-#define MOE_GATHER_SUM(W, S)                                                                                  \
-  k_gather_sum<T, V, W, S><<<g, kThreadsD, 0, st>>>(m, (const T*)rows, rows_ld, num_rows, row_of, w, k,       \
-                                                    (const T*)residual, res_ld, (T*)y, y_ld)
-  if (w && stream) MOE_GATHER_SUM(true, true);
-  else if (w) MOE_GATHER_SUM(true, false);
-  else if (stream) MOE_GATHER_SUM(false, true);
-  else MOE_GATHER_SUM(false, false);
+  constexpr int U = V == 1 ? 4 : 2;
+  const bool more = stream && m.cblocks >= U;
+  if (more) {
+    m.nblocks /= m.cblocks;
+    m.cblocks = (m.cblocks + U - 1) / U;
+    m.nblocks *= m.cblocks;
+  }
+  const unsigned g = grid_blocks(m.nblocks);
+#define MOE_GATHER_SUM(W, S, U)                                                                               \
+  k_gather_sum<T, V, W, S, U><<<g, kThreadsD, 0, st>>>(m, (const T*)rows, rows_ld, num_rows, row_of, w, k,    \
+                                                       (const T*)residual, res_ld, (T*)y, y_ld)
+  if (w && more) MOE_GATHER_SUM(true, true, U);
+  else if (w && stream) MOE_GATHER_SUM(true, true, 1);
+  else if (w) MOE_GATHER_SUM(true, false, 1);
+  else if (more) MOE_GATHER_SUM(false, true, U);
+  else if (stream) MOE_GATHER_SUM(false, true, 1);
+  else MOE_GATHER_SUM(false, false, 1);
 #undef MOE_GATHER_SUM
 }
 
