@@ -73,12 +73,20 @@ RowMap row_map(int64_t nrows, int64_t pieces) {
   return m;
 }
 
-// (row, piece) of this thread in unit b, or false
+// The same with U pieces per thread, tpr apart.
+RowMap with_pieces(RowMap m, int U) {
+  m.nblocks = m.nblocks / m.cblocks * ((m.cblocks + U - 1) / U);
+  m.cblocks = (m.cblocks + U - 1) / U;
+  return m;
+}
+
+// (row, first piece) of this thread in unit b, or false
+template <int U = 1>
 __device__ __forceinline__ bool row_piece(const RowMap& m, int64_t b, int64_t& row, int& c) {
   const int64_t rb = b / m.cblocks;
   const int cb = (int)(b - rb * m.cblocks);
   row = rb * (kThreadsD >> m.lg) + (threadIdx.x >> m.lg);
-  c = cb * m.tpr + (threadIdx.x & (m.tpr - 1));
+  c = cb * m.tpr * U + (threadIdx.x & (m.tpr - 1));
   return row < m.nrows && c < m.pieces;
 }
 
@@ -129,8 +137,12 @@ constexpr int64_t kStreamBytes = 16 << 20;
 // then one that reads each token's row once for all of its rows.  Below it one
 // launch gathers row by row, reading x up to k times, from the caches.  (bf16, H
 // 7168, k 8: 8192 tokens 219 us against 364, 1024 tokens 31.8 against 35.9, 256
-// tokens 11.5 against 10.3, one token 11.9 against 8.7.)
+// tokens 11.5 against 10.3, one token 11.9 against 8.7; in elements, H 4095, k 8: 4096
+// tokens 110 against 133.)
 constexpr int64_t kTokenBytes = 64 << 20;
+// Rows that only elements of 2 or 4 bytes can walk (odd lengths, strides or
+// addresses): workgroups of a piece per thread from which on each takes four.
+constexpr int64_t kElementBlocks = 8192;
 
 // row_of[a] of every assignment a
 __global__ __launch_bounds__(kThreadsD) void k_invert(int64_t A, const int32_t* __restrict__ offsets,
@@ -167,8 +179,8 @@ __global__ __launch_bounds__(kThreadsD) void k_permute_tokens(RowMap m, const P*
 }
 
 // One row per assignment g of sorted_assign: row g - base is the row of its
-// token; thread 0 of the row notes where it went.
-template <typename P>
+// token; thread 0 of the row notes where it went.  U pieces per thread.
+template <typename P, int U>
 __global__ __launch_bounds__(kThreadsD) void k_permute_rows(RowMap m, const P* __restrict__ x, int64_t x_ld, int k,
                                                             const int32_t* __restrict__ offsets,
                                                             const int32_t* __restrict__ sorted_assign, int lo, int n,
@@ -179,12 +191,18 @@ __global__ __launch_bounds__(kThreadsD) void k_permute_rows(RowMap m, const P* _
   for (int64_t b = blockIdx.x; b < m.nblocks; b += gridDim.x) {
     int64_t g;
     int c;
-    if (!row_piece(m, b, g, c)) continue;
+    if (!row_piece<U>(m, b, g, c)) continue;
     const int32_t a = sorted_assign[g];
     if (a < 0 || a >= m.nrows) continue;
     const bool here = g >= base && g < end && g - base < num_rows;
     if (c == 0) row_of[a] = here ? (int32_t)(g - base) : -1;
-    if (here) rows[(g - base) * rows_ld + c] = x[(int64_t)(a / k) * x_ld + c];
+    if (!here) continue;
+    P v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = x[(int64_t)(a / k) * x_ld + min(c + u * m.tpr, m.pieces - 1)];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c + u * m.tpr < m.pieces) rows[(g - base) * rows_ld + c + u * m.tpr] = v[u];
   }
 }
 
@@ -204,11 +222,9 @@ __global__ __launch_bounds__(kThreadsD) void k_gather_sum(RowMap m, const T* __r
                                                           int64_t res_ld, T* y, int64_t y_ld) {
   using P = Pack<T, V>;
   for (int64_t b = blockIdx.x; b < m.nblocks; b += gridDim.x) {
-    const int64_t rb = b / m.cblocks;
-    const int cb = (int)(b - rb * m.cblocks);
-    const int64_t t = rb * (kThreadsD >> m.lg) + (threadIdx.x >> m.lg);
-    const int c0 = cb * m.tpr * U + (threadIdx.x & (m.tpr - 1));
-    if (t >= m.nrows || c0 >= m.pieces) continue;
+    int64_t t;
+    int c0;
+    if (!row_piece<U>(m, b, t, c0)) continue;
     int64_t c[U];  // past the row: its last piece again, not stored
 #pragma unroll
     for (int u = 0; u < U; ++u) c[u] = (int64_t)min(c0 + u * m.tpr, m.pieces - 1) * V;
@@ -386,22 +402,21 @@ void launch_gather_sum(const void* rows, int64_t rows_ld, int32_t num_rows, cons
                        hipStream_t st) {
   RowMap m = row_map(T_, H / V);
   const bool stream = (int64_t)T_ * H * (int64_t)sizeof(T) >= kStreamBytes;
+  // several pieces per thread: 16-byte ones in large calls, elements where that
+  // leaves enough workgroups
   constexpr int U = V == 1 ? 4 : 2;
-  const bool more = stream && m.cblocks >= U;
-  if (more) {
-    m.nblocks /= m.cblocks;
-    m.cblocks = (m.cblocks + U - 1) / U;
-    m.nblocks *= m.cblocks;
-  }
+  const bool more = m.cblocks >= U && (V == 1 ? m.nblocks >= kElementBlocks : stream);
+  if (more) m = with_pieces(m, U);
   const unsigned g = grid_blocks(m.nblocks);
 #define MOE_GATHER_SUM(W, S, U)                                                                               \
   k_gather_sum<T, V, W, S, U><<<g, kThreadsD, 0, st>>>(m, (const T*)rows, rows_ld, num_rows, row_of, w, k,    \
                                                        (const T*)residual, res_ld, (T*)y, y_ld)
-  if (w && more) MOE_GATHER_SUM(true, true, U);
-  else if (w && stream) MOE_GATHER_SUM(true, true, 1);
+  constexpr bool S = V > 1;  // (elements are not stored past the caches)
+  if (w && more) MOE_GATHER_SUM(true, S, U);
+  else if (w && stream && S) MOE_GATHER_SUM(true, S, 1);
   else if (w) MOE_GATHER_SUM(true, false, 1);
-  else if (more) MOE_GATHER_SUM(false, true, U);
-  else if (stream) MOE_GATHER_SUM(false, true, 1);
+  else if (more) MOE_GATHER_SUM(false, S, U);
+  else if (stream && S) MOE_GATHER_SUM(false, S, 1);
   else MOE_GATHER_SUM(false, false, 1);
 #undef MOE_GATHER_SUM
 }
@@ -455,31 +470,30 @@ extern "C" moe_status_t moe_permute(const void* x, moe_src_t dtype, int64_t x_ld
     const RowMap mt = row_map(T, H / V);
     const unsigned gi = grid_blocks((A + kThreadsD - 1) / kThreadsD), gt = grid_blocks(mt.nblocks);
     k_invert<<<gi, kThreadsD, 0, stream>>>(A, expert_offsets, sorted_assign, local_expert_offset, n, num_rows, row_of);
-    if (vec)
-      k_permute_tokens<uint4><<<gt, kThreadsD, 0, stream>>>(mt, (const uint4*)x, x_ld / V, k, row_of, (uint4*)rows,
-                                                            rows_ld / V, num_rows);
-    else if (dtype == MOE_SRC_BF16)
-      k_permute_tokens<uint16_t><<<gt, kThreadsD, 0, stream>>>(mt, (const uint16_t*)x, x_ld, k, row_of,
-                                                               (uint16_t*)rows, rows_ld, num_rows);
-    else
-      k_permute_tokens<uint32_t><<<gt, kThreadsD, 0, stream>>>(mt, (const uint32_t*)x, x_ld, k, row_of,
-                                                               (uint32_t*)rows, rows_ld, num_rows);
+#define MOE_PERMUTE_TOKENS(P)                                                                                       \
+  k_permute_tokens<P><<<gt, kThreadsD, 0, stream>>>(mt, (const P*)x, x_ld / V, k, row_of, (P*)rows, rows_ld / V,    \
+                                                    num_rows)
+    if (vec) MOE_PERMUTE_TOKENS(uint4);
+    else if (dtype == MOE_SRC_BF16) MOE_PERMUTE_TOKENS(uint16_t);
+    else MOE_PERMUTE_TOKENS(uint32_t);
+#undef MOE_PERMUTE_TOKENS
     return launched();
   }
-  const RowMap m = row_map(A, H / V);
+  RowMap m = row_map(A, H / V);
+  // four elements per thread where that leaves enough workgroups (1024 x 4095 bf16,
+  // k = 4: 20 us against 46)
+  const bool more = !vec && m.cblocks >= 4 && m.nblocks >= kElementBlocks;
+  if (more) m = with_pieces(m, 4);
   const unsigned g = grid_blocks(m.nblocks);
-  if (vec)
-    k_permute_rows<uint4><<<g, kThreadsD, 0, stream>>>(m, (const uint4*)x, x_ld / V, k, expert_offsets, sorted_assign,
-                                                       local_expert_offset, n, (uint4*)rows, rows_ld / V, num_rows,
-                                                       row_of);
-  else if (dtype == MOE_SRC_BF16)
-    k_permute_rows<uint16_t><<<g, kThreadsD, 0, stream>>>(m, (const uint16_t*)x, x_ld, k, expert_offsets,
-                                                          sorted_assign, local_expert_offset, n, (uint16_t*)rows,
-                                                          rows_ld, num_rows, row_of);
-  else
-    k_permute_rows<uint32_t><<<g, kThreadsD, 0, stream>>>(m, (const uint32_t*)x, x_ld, k, expert_offsets,
-                                                          sorted_assign, local_expert_offset, n, (uint32_t*)rows,
-                                                          rows_ld, num_rows, row_of);
+#define MOE_PERMUTE_ROWS(P, U)                                                                                      \
+  k_permute_rows<P, U><<<g, kThreadsD, 0, stream>>>(m, (const P*)x, x_ld / V, k, expert_offsets, sorted_assign,     \
+                                                    local_expert_offset, n, (P*)rows, rows_ld / V, num_rows, row_of)
+  if (vec) MOE_PERMUTE_ROWS(uint4, 1);
+  else if (dtype == MOE_SRC_BF16 && more) MOE_PERMUTE_ROWS(uint16_t, 4);
+  else if (dtype == MOE_SRC_BF16) MOE_PERMUTE_ROWS(uint16_t, 1);
+  else if (more) MOE_PERMUTE_ROWS(uint32_t, 4);
+  else MOE_PERMUTE_ROWS(uint32_t, 1);
+#undef MOE_PERMUTE_ROWS
   return launched();
 }
 

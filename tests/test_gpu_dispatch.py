@@ -56,7 +56,7 @@ CASES = [
     (64, 1024, 32, 8, 16, 16), (257, 72, 20, 11, 0, 0), (33, 4104, 64, 17, 7, 1), (130, 520, 512, 6, 100, 300),
     (2, 64, 16, 2, 15, 1), (11, 16896, 8, 3, 0, 0), (3, 4100, 16, 12, 2, 9), (256, 1032, 8, 2, 0, 0),
     (300, 1544, 32, 11, 0, 0), (9000, 1000, 8, 2, 0, 0), (4500, 2000, 8, 2, 0, 0),
-    (2100, 4100, 16, 9, 3, 9), (8200, 1031, 16, 2, 0, 0),
+    (2100, 4100, 16, 9, 3, 9), (8200, 1031, 16, 2, 0, 0), (520, 4099, 16, 4, 2, 11),
 ]
 
 
