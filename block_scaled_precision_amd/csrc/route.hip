@@ -283,7 +283,7 @@ __global__ __launch_bounds__(1024) void k_permute_small(const float* __restrict_
   }
 }
 
-// One workgroup; thread g owns group g.  Offsets are clamped so that they
+// One workgroup of as many waves as the groups need; thread g owns group g.  Offsets are clamped so that they
 // ascend within [0, M] whatever the buffer holds, which bounds the tiles by
 // M / bm + groups.
 __global__ __launch_bounds__(1024) void k_group_tiles(const int32_t* __restrict__ offsets, int groups, int M, int bm,
@@ -325,12 +325,12 @@ __global__ __launch_bounds__(1024) void k_group_tiles(const int32_t* __restrict_
     tl.pad = 0;
     tiles[inc - ntile + i] = tl;
   }
-  if (g == 1023) *num_tiles = inc;
+  if (g == (int)blockDim.x - 1) *num_tiles = inc;
 }
 
 hipError_t launch_group_tiles(const int32_t* offsets, int groups, int64_t M, int bm, Tile* tiles,
                               int32_t* num_tiles, hipStream_t stream) {
-  k_group_tiles<<<1, 1024, 0, stream>>>(offsets, groups, (int)M, bm, tiles, num_tiles);
+  k_group_tiles<<<1, (groups + 63) / 64 * 64, 0, stream>>>(offsets, groups, (int)M, bm, tiles, num_tiles);
   return hipGetLastError();
 }
 
