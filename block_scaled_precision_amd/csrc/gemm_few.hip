@@ -12,7 +12,7 @@
 // operand, activations to the second; rows past the tile load nothing.  Every lane
 // then reads another row, which costs the cache lookups that the LDS copies of
 // gemm_rows.hip save: from about 16 rows on those win in spite of a second launch.
-// (One token, 4096 x 7168 E2M1 x bf16: 8.4 us a call against 11.6 for 16-row LDS
+// (One token, 4096 x 7168 E2M1 x bf16: 8.0 us a call against 11.6 for 16-row LDS
 // tiles in 7 K ranges and their join; 16 rows 12.9 against 12.1.)
 //
 // Lane layouts are those of the stream kernels (gemm_stream.hip).  QUANT: bf16 rows
