@@ -288,7 +288,8 @@ class OpCall:
     buffers (their contents may change between calls): each call then costs the
     host only the C call.  The stream is the current one at each call unless
     one is given.  Calling returns the operator's outputs, the same tensors each
-    time.
+    time: its calls must not run at the same time (on two streams, or in two
+    graphs), and it has to live as long as a graph that captured one.
 
         combine = OpCall(moe_unpermute, rows, row_of, topk_w)
         y = combine()

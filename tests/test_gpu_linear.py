@@ -133,6 +133,37 @@ def test_activations_within_their_bound(M, N, K, fmt, act, fn):
         assert (d <= bound).all(), f"{(d > bound).sum()} out of bounds, worst ratio {(d / bound).max():.2f}"
 
 
+# K below, at and off the scale groups of every kernel, with few rows and many
+PICKED = [(M, N, K) for M, N, K in [(5, 264, 128), (1900, 136, 128), (20, 520, 384), (1500, 136, 384), (700, 264, 256),
+                                    (3, 64, 3200), (40, 264, 640), (300, 1000, 1152), (1300, 520, 896), (2100, 520, 640),
+                                    (70, 136, 3712), (400, 512, 3584)]]
+
+
+@pytest.mark.parametrize("G", [0, 5])
+@pytest.mark.parametrize("fmt,act", [("e2m1", "bf16"), ("e3m2", "bf16"), ("e2m1", "mxfp8"), ("e3m2", "mxfp8")])
+@pytest.mark.parametrize("M,N,K", PICKED)
+def test_every_weight_meets_its_scale(M, N, K, fmt, act, G):
+    """Row m holds one nonzero power of two, at k = 33 m mod K, so out[m, n] is a
+    weight times its block's scale (of any size) and that power: exact, whatever
+    the order of the sum."""
+    from block_scaled_precision_amd import moe_mx as m
+    print_flush(f"mx_linear picked M={M} N={N} K={K} G={G} {fmt}/{act}")
+    w, s = _weights((G, N) if G else (N,), K, fmt, 18, scales=(60, 190))
+    rows, k = torch.arange(M), 33 * torch.arange(M) % K
+    a = torch.zeros((M, K), dtype=BF16)
+    power = 2.0 ** (rows % 9 - 4)
+    a[rows, k] = power.to(BF16)
+    off = torch.tensor([0, 0, M // 3, M // 3 + 1, M - M // 4, M]).int() if G else None
+    got = _np(m.mx_linear(a.cuda(), w.cuda(), s.cuda(), fmt, act, expert_offsets=None if off is None else off.cuda()))
+    for g, (lo, hi) in enumerate(zip(off[:-1].tolist(), off[1:].tolist()) if G else [(0, M)]):
+        if lo == hi:
+            continue
+        codes = mx.unpack((w[g] if G else w).numpy(), fmt, K)
+        weights = mx.dequantize(codes, (s[g] if G else s).numpy(), fmt)
+        ref = weights[:, k[lo:hi].numpy()].T * _np(power)[lo:hi, None]
+        assert np.array_equal(got[lo:hi], ref), f"group {g}"
+
+
 def test_activations_over_the_whole_range():
     """One product per output (K = 128, one nonzero weight of 1), so v = a over
     the range where exp overflows and erfc vanishes."""
