@@ -375,6 +375,46 @@ def test_prepared_call_and_stream_argument():
         assert torch.equal(y2, y)
 
 
+# split K with its join, MXFP8 quantized into the workspace, grouped tile lists
+AT_ONCE = [(40, 512, 4096, "e2m1", "bf16", 0), (64, 1024, 4096, "e3m2", "mxfp8", 0), (300, 512, 1024, "e2m1", "mxfp8", 4),
+           (200, 256, 768, "e2m1", "bf16", 6)]
+
+
+def test_prepared_calls_at_once_and_captured():
+    """Prepared calls of the same problem on two streams at the same time, then
+    captured ones replayed among eager work: each has its own workspace."""
+    from block_scaled_precision_amd import moe_mx as m
+    for M, N, K, fmt, act, G in AT_ONCE:
+        print_flush(f"mx_linear at once M={M} N={N} K={K} G={G} {fmt}/{act}")
+        (w, s) = _weights((G, N) if G else (N,), K, fmt, 19, scales=(118, 123))
+        w, s = w.cuda(), s.cuda()
+        off = torch.linspace(0, M, G + 1).int().cuda() if G else None
+        a = [gen.normal((M, K), 19 + i, 25).to(BF16).cuda() for i in range(2)]
+        want = [m.mx_linear(x, w, s, fmt, act, expert_offsets=off) for x in a]
+        calls = [m.OpCall(m.mx_linear, x, w, s, fmt, act, expert_offsets=off) for x in a]
+        streams = [torch.cuda.Stream() for _ in a]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for call, st in zip(calls, streams):
+                with torch.cuda.stream(st):
+                    out = call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(call(), r) for call, r in zip(calls, want))
+        graphs = []
+        for call in calls:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                out = call()
+            graphs.append((g, out))
+        for i in (0, 1, 1, 0, 1):
+            g, out = graphs[i]
+            out.zero_()
+            g.replay()
+            other = m.mx_linear(a[1 - i], w, s, fmt, act, expert_offsets=off)
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[i]) and torch.equal(other, want[1 - i])
+
+
 def test_rows_past_32_bit_offsets():
     """Output and operand offsets beyond 2^32 bytes and elements: the last rows
     of a long batch against the same rows alone."""
