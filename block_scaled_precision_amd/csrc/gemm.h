@@ -27,6 +27,10 @@ struct FcArgs {
   const int32_t* num_tiles;
   int max_tiles;
   int dense_rows;
+  // mx_linear's few-row kernel: no tile list, but the offsets of `groups` groups
+  // over group_rows rows
+  const int32_t* group_offsets;
+  int groups, group_rows;
   // routed rows: permuted position p -> assignment a = t*k + j
   const int32_t* sorted_assign;
   int k;

@@ -148,6 +148,54 @@ __device__ __forceinline__ void mul_chunk(v4f& acc, const Chunk& f, int g, int r
   acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, av, acc, Fmt<WF>::MFMA, 0, 0, wsc, 0, asc);
 }
 
+// Tile ti of the list that k_group_tiles would make (16 rows each, groups in order,
+// ends clamped so that they ascend within [0, M]), by each wave on its own: a lane
+// takes a run of groups.  rows = 0 behind the last tile.  (A launch that writes the
+// list costs a call of a few rows more than its product: 4 rows over 11 groups, 232
+// x 512, 4.7 us a call against 8.3.)
+__device__ __forceinline__ Tile find_tile(const int32_t* offsets, int groups, int M, int ti) {
+  const int lane = threadIdx.x & 63, per = (groups + 63) >> 6, g0 = lane * per, g1 = min(g0 + per, groups);
+  const int64_t first = offsets[0];
+  auto end = [&](int g) { return (int32_t)min(max((int64_t)offsets[g + 1] - first, (int64_t)0), (int64_t)M); };
+  int32_t last = 0;
+  for (int g = g0; g < g1; ++g) last = max(last, end(g));
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t v = __shfl_up(last, d);
+    if (lane >= d) last = max(last, v);
+  }
+  int32_t start = __shfl_up(last, 1);
+  if (lane == 0) start = 0;
+  int32_t s = start, n = 0;
+  for (int g = g0; g < g1; ++g) {
+    const int32_t e = max(s, end(g));
+    n += (e - s + 15) >> 4;
+    s = e;
+  }
+  int32_t upto = n;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t v = __shfl_up(upto, d);
+    if (lane >= d) upto += v;
+  }
+  Tile t = {0, 0, 0, 0};
+  int c = ti - (upto - n);  // the tile's place in this lane's run
+  const uint64_t holder = __ballot(c >= 0 && c < n);
+  if (holder == 0) return t;
+  s = start;
+  for (int g = g0; g < g1; ++g) {
+    const int32_t e = max(s, end(g)), nt = (e - s + 15) >> 4;
+    if (c >= 0 && c < nt) t = {g, s + 16 * c, min(16, e - s - 16 * c), 0};
+    c -= nt;
+    s = e;
+  }
+  const int src = __builtin_ctzll(holder);
+  t.expert = __builtin_amdgcn_readlane(t.expert, src);
+  t.p0 = __builtin_amdgcn_readlane(t.p0, src);
+  t.rows = __builtin_amdgcn_readlane(t.rows, src);
+  return t;
+}
+
 template <int ACT, int WF>
 __global__ __launch_bounds__(64 * W) void k_linear_few(FcArgs p) {
   __shared__ float part[W][16][kFewCols + 4];
@@ -160,8 +208,8 @@ __global__ __launch_bounds__(64 * W) void k_linear_few(FcArgs p) {
     t.p0 = 16 * ti;
     t.rows = min(16, p.dense_rows - 16 * ti);
   } else {
-    if (ti >= *p.num_tiles) return;
-    t = p.tiles[ti];
+    t = find_tile(p.group_offsets, p.groups, p.group_rows, ti);
+    if (t.rows == 0) return;
   }
   // the first 32 threads finish a piece of out each
   const int prow = threadIdx.x >> 1, pcol = col0 + 8 * (threadIdx.x & 1);

@@ -603,7 +603,8 @@ static bool linear_supported(const mx_linear_problem_t& p) {
 // per item for its epilogue (MI355X; without what every call pays for its launch):
 //   few rows (gemm_few.hip; 16 x 16 items, 1024 K a step)  E2M1 x bf16: 1 row 0.43,
 //     16 rows 1.0; E3M2 0.2 more; MXFP8 0.4 more, 0.8 up to K = 1024 (it quantizes in
-//     place); twice that with groups, whose weights come from HBM (184 rows over 69 experts, 1840 x 896: 42 us, 16-row tiles 21)
+//     place); twice that with groups, whose weights come from HBM (184 rows over 69
+//     experts, 1840 x 896: 42 us, 16-row tiles 21)
 //   rows (gemm_rows.hip; 256 K a step)  16 x 128 items: E2M1 0.55, E3M2 1.0;
 //     64 x 128 items: E2M1 1.1 (bf16), 0.75 (MXFP8), E3M2 1.75, 1.4; 1.15
 //     times that with groups
@@ -647,7 +648,10 @@ struct LinearCost {
     const double weights = active * p.N * (double)p.K * (wbits(p.w_fmt) / 8.0 + 1.0 / 32.0) / kWeightRate;
     return std::max(rounds * (std::ceil(steps / ksplit) * t + 1.0 + 0.3 / 1024.0 * bm * bn), weights);
   }
-  double quant_time() const { return quant ? 3.5 + (double)p.M * p.K * 3.0 / 3.5e6 : 0.0; }
+  // launches in front of a kernel: the tile list and the quantized activations
+  double before() const {
+    return (p.groups > 0 ? 4.0 : 0.0) + (quant ? 3.5 + (double)p.M * p.K * 3.0 / 3.5e6 : 0.0);
+  }
   double join_time(int ksplit) const { return ksplit > 1 ? 4.5 + (double)ksplit * p.M * p.N * 8.0 / 4.0e6 : 0.0; }
 };
 
@@ -666,10 +670,12 @@ static void linear_kind(const mx_linear_problem_t& p, bool has_a_scale, LinearPl
   if (c.tiles(16) * (p.N / 16) <= 1 << 20) {
     const double more = (e2m1 ? 0.0 : 0.2) + (!mx ? 0.0 : p.K <= 1024 ? 0.8 : 0.4);
     const double t = (p.groups > 0 ? 2.0 : 1.0) * (0.43 + 0.57 * std::min(c.per, 16.0) / 16.0 + more);
-    // (with bf16 several of its workgroups share a CU: no whole rounds)
+    // (with bf16 several of its workgroups share a CU: no whole rounds; each finds
+    // its tile in the offsets)
     const double steps = p.K <= 1024 ? 1.0 : std::ceil(p.K / 2048.0) * 2.0;
     const double rounds = std::max(1.0, c.tiles(16) * (p.N / 16) / kLinearWgs);
-    take(Fc::kFew, kStreamRows, 0, mx ? c.time(16, 16, steps, t) : 1.0 + rounds * t * steps);
+    const double find = p.groups > 0 ? 1.5 : 0.0;
+    take(Fc::kFew, kStreamRows, 0, mx ? c.time(16, 16, steps, t) : 1.0 + rounds * (t * steps + find));
   }
   const double stages = std::ceil(p.K / (double)kRowsK);
   const double own = p.groups > 0 ? 1.15 : 1.0;  // groups share no weights in the caches
@@ -677,7 +683,7 @@ static void linear_kind(const mx_linear_problem_t& p, bool has_a_scale, LinearPl
   // K ranges of at least two stages, dense calls only
   const int most = p.groups > 0 ? 1 : (int)std::min(16.0, std::max(1.0, std::floor(stages / 2.0)));
   for (int s = 1; s <= most; ++s) {
-    const double more = c.quant_time() + c.join_time(s);
+    const double more = c.before() + c.join_time(s);
     take(Fc::kRows, 16, s, c.time(16, kRowsCols, stages, t16, s) + more);
     take(Fc::kRows, 64, s, c.time(64, kRowsCols, stages, t64, s) + more);
   }
@@ -685,17 +691,17 @@ static void linear_kind(const mx_linear_problem_t& p, bool has_a_scale, LinearPl
   if (p.K < kMidK) return;
   const double steps = std::ceil(p.K / (double)kMidK) * (kMidK / 128);
   if (!mx && e2m1) {
-    take(Fc::kMid, kMidRows, 0, c.time(kMidRows, kWideCols, steps, 1.06));
-    take(Fc::kMid, kMidRowsHigh, 0, c.time(kMidRowsHigh, kWideCols, steps, 1.6));
+    take(Fc::kMid, kMidRows, 0, c.time(kMidRows, kWideCols, steps, 1.06) + c.before());
+    take(Fc::kMid, kMidRowsHigh, 0, c.time(kMidRowsHigh, kWideCols, steps, 1.6) + c.before());
   }
   if (mx) {
     take(Fc::kTiled, kTiledRowsLow, 0,
-         c.time(128, tiled_weight_rows(kTiledRowsLow), steps, e2m1 ? 1.08 : 1.3) + c.quant_time());
+         c.time(128, tiled_weight_rows(kTiledRowsLow), steps, e2m1 ? 1.08 : 1.3) + c.before());
     take(Fc::kTiled, kTiledRows, 0,
-         c.time(192, tiled_weight_rows(kTiledRows), steps, e2m1 ? 0.88 : 1.1) + c.quant_time());
+         c.time(192, tiled_weight_rows(kTiledRows), steps, e2m1 ? 0.88 : 1.1) + c.before());
     // (its 32-bit offsets into A, and column blocks of 64 inside N)
     if (e2m1 && p.K >= 1024 && p.K % kTiledKMultiple == 0 && p.N % 64 == 0 && (double)p.M * p.K < 4294967296.0)
-      take(Fc::kWide, kTiledRows, 0, c.time(192, kWideCols, steps, 1.27) + c.quant_time());
+      take(Fc::kWide, kTiledRows, 0, c.time(192, kWideCols, steps, 1.27) + c.before());
   }
 }
 
@@ -710,7 +716,7 @@ static LinearPlan linear_plan(const mx_linear_problem_t& p, bool has_a_scale) {
     return r;
   };
   if (p.act == MOE_ACT_MXFP8 && !has_a_scale && f.kind != Fc::kFew) f.quant = take(gemm_quant_bytes(p.M, p.K));
-  if (p.groups > 0) {
+  if (p.groups > 0 && f.kind != Fc::kFew) {
     f.tiles = take((size_t)f.max_tiles * sizeof(Tile));
     f.ntiles = take(4);
   }
@@ -775,7 +781,12 @@ extern "C" moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_
     g.a = qc;
     g.a_scale = qs;
   }
-  if (p->groups > 0) {
+  if (p->groups > 0 && f.kind == Fc::kFew) {
+    g.group_offsets = t->expert_offsets;
+    g.groups = p->groups;
+    g.group_rows = (int)M;
+    g.max_tiles = f.max_tiles;
+  } else if (p->groups > 0) {
     Tile* tiles = (Tile*)(ws + f.tiles);
     int32_t* ntiles = (int32_t*)(ws + f.ntiles);
     if (launch_group_tiles(t->expert_offsets, p->groups, M, f.rows, tiles, ntiles, stream) != hipSuccess)

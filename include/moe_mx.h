@@ -283,9 +283,9 @@ typedef struct {
 
 /* Workspace of mx_linear: mx_linear_workspace_bytes(p, has_a_scale) bytes,
  * 256-byte aligned, contents need not be set; 0 for a problem that needs none or
- * is invalid.  It holds the tile list of grouped calls, the partial sums of
- * split ones and, unless a_scale is given, the quantized A of MXFP8 from bf16, so
- * calls that may run at the same time need one each.
+ * is invalid.  As the problem needs it, it holds the tile list of a grouped call,
+ * the partial sums of a split one and the quantized A of MXFP8 from bf16, so calls
+ * that may run at the same time need one each.
  * Requires M >= 0 (0: no-op), M <= 2^30, K <= 2^24, M*N <= 2^35, M*N*K <= 2^52 and
  * 16-byte aligned a, a_scale, w, w_scale, mul, residual and out (bias: its element
  * size); N % 8 != 0, K % 128 != 0, larger sizes or E4M3 weights give MOE_ERR_UNSUPPORTED.
