@@ -15,11 +15,11 @@
 //
 // Measured (MI355X): 512 rows over 384 experts (64 tokens with 8 each; 283 experts
 // have rows), N = 7168, K = 2048, 16-row tiles, with the rate of the weights' bytes:
-//   E2M1 x bf16 416 us (5.3 TB/s), E2M1 x MXFP8 394 (5.6), E3M2 x bf16 606 (5.4),
-//   E3M2 x MXFP8 592 (5.5); a copy of 1 GiB runs at 5.1.
+//   E2M1 x bf16 416 us (5.3 TB/s), E2M1 x MXFP8 394 (5.6), E3M2 x bf16 557 (5.8),
+//   E3M2 x MXFP8 553 (5.9); a copy of 1 GiB runs at 5.1.
 // One matrix, N = 4096, K = 7168, in the same order: 64 rows in two K ranges of
-// 16-row tiles 16.1, 16.6, 22.4, 24.7 us, in four of 64-row tiles 16.5, 17.0, 20.6,
-// 21.9; 1024 rows in 64-row tiles 75, 54, 102, 93.  The weights of a dense matrix
+// 16-row tiles 16.1, 16.6, 18.9, 18.6 us, in four of 64-row tiles 16.5, 17.0, 17.3,
+// 18.1; 1024 rows in 64-row tiles 75, 54, 81, 66.  The weights of a dense matrix
 // come from the caches; there the multiply waves' own instructions between two
 // barriers bound it.  Eight multiply waves (4% slower), fragments of the next stage
 // kept in registers ahead of time (E2M1 x MXFP8 4% faster, the others 4 to 18%
@@ -53,6 +53,9 @@ typedef int v6i __attribute__((ext_vector_type(6)));
 typedef __bf16 v32bf __attribute__((ext_vector_type(32)));
 
 constexpr int RN = kRowsCols;    // columns per item
+// E3M2 weight row jr holds piece c of its 12 at slot (c + turn(jr)) % 12, so that the
+// rows of a read, four of which would start at the same bank, are spread over them
+__device__ __forceinline__ int turn(int jr) { return (jr >> 2) & 3; }
 constexpr int RK = kRowsK;       // K per stage
 constexpr int kMulWaves = 4, kWaveA = 6;
 // activation-copy waves and threads for tiles of `sub` 16-row sub-tiles
@@ -188,8 +191,8 @@ __device__ __forceinline__ void copy_weights(const FcArgs& p, const Sched& sc, u
 #pragma unroll
       for (int i = 0; i < L::BCOP; ++i) {
         const int cc = 64 * (L::BCOP * bw + i) + lane, jr = cc / CPR;
-        // E2M1: piece c of row jr at slot c ^ (jr & 7)
-        const int ch = WF == 1 ? (cc % CPR) ^ (jr & 7) : cc % CPR;
+        // E2M1: piece c of row jr at slot c ^ (jr & 7); E3M2: see turn()
+        const int ch = WF == 1 ? (cc % CPR) ^ (jr & 7) : (cc % CPR + CPR - turn(jr)) % CPR;
         off[i] = (uint32_t)min(epi_row16(jr), last) * (uint32_t)wrow + 16 * ch;
         back |= (uint32_t)(ch >= CPR / 2) << i;
       }
@@ -309,16 +312,23 @@ __device__ __forceinline__ void mul_half(v4f (&acc)[SUB][2], const uint8_t* bs, 
       const uint4 v = *(const uint4*)(bs + jr * L::BROW + 16 * (blk ^ (jr & 7)));
       b[n][0] = v.x; b[n][1] = v.y; b[n][2] = v.z; b[n][3] = v.w; b[n][4] = 0; b[n][5] = 0;
     } else {
-      const uint8_t* q = bs + jr * L::BROW + 24 * blk;  // 16-byte address where g is even
-      if ((g & 1) == 0) {
-        const uint4 v = *(const uint4*)q;
-        const uint2 d = *(const uint2*)(q + 16);
-        b[n][0] = v.x; b[n][1] = v.y; b[n][2] = v.z; b[n][3] = v.w; b[n][4] = d.x; b[n][5] = d.y;
-      } else {
-        const uint2 d = *(const uint2*)q;
-        const uint4 v = *(const uint4*)(q + 8);
-        b[n][0] = d.x; b[n][1] = d.y; b[n][2] = v.x; b[n][3] = v.y; b[n][4] = v.z; b[n][5] = v.w;
-      }
+      // 24 bytes: a 16-byte piece and half of one, which follows it where g is even and
+      // precedes it where g is odd.  (Both kinds of lane read at once; a branch for each
+      // and no turn: 16-row tiles 607 against 557 us over 384 experts, 64-row tiles 102
+      // against 81, MXFP8 94 against 66 over 1024 x 4096 x 7168.)
+      const uint8_t* q = bs + jr * L::BROW;
+      const bool odd = g & 1;
+      int cv = (3 * blk + 1) / 2 + turn(jr), cd = (odd ? (3 * blk) / 2 : 3 * blk / 2 + 1) + turn(jr);
+      cv -= cv >= 12 ? 12 : 0;
+      cd -= cd >= 12 ? 12 : 0;
+      const uint4 v = *(const uint4*)(q + 16 * cv);
+      const uint2 d = *(const uint2*)(q + 16 * cd + (odd ? 8 : 0));
+      b[n][0] = odd ? d.x : v.x;
+      b[n][1] = odd ? d.y : v.y;
+      b[n][2] = odd ? v.x : v.z;
+      b[n][3] = odd ? v.y : v.w;
+      b[n][4] = odd ? v.z : d.x;
+      b[n][5] = odd ? v.w : d.y;
     }
   }
   // a lane's part of sub-tile m: its row's block
@@ -444,8 +454,8 @@ __device__ __forceinline__ void multiply(const FcArgs& p, const Sched& sc, const
     const uint8_t* ws = smem + L::WS + (group % L::BUFS) * L::WSB + so;
     const uint8_t* xs = smem + L::AS + (group % L::BUFS) * L::ASB + so;
     // A whole stage of a whole tile in one block lets the two halves' LDS reads and
-    // conversions run together: 16-row E3M2 x bf16 606 against 656 us, 64-row tiles up
-    // to 5%; the others of 16 rows lose 3% by it and take a branch between.
+    // conversions run together: 16-row E3M2 x bf16 8% faster, 64-row tiles up to 5%; the
+    // others of 16 rows lose 3% by it and take a branch between.
     const bool two = !(half && s == sc.stages - 1);
     if (SUB == 1 && (MXA || WF == 1)) {
       mul_half<MXA, WF, SUB, SHORT, true>(acc, st, st + L::S_B, ws, xs, 0, w, g, r, nm);

@@ -605,8 +605,9 @@ static bool linear_supported(const mx_linear_problem_t& p) {
 //     16 rows 1.0; E3M2 0.2 more; MXFP8 0.4 more, 0.8 up to K = 1024 (it quantizes in
 //     place); twice that with groups, whose weights come from HBM (184 rows over 69
 //     experts, 1840 x 896: 42 us, 16-row tiles 21)
-//   rows (gemm_rows.hip; 256 K a step)  16 x 128 items: E2M1 0.55, E3M2 1.0;
-//     64 x 128 items: E2M1 1.1 (bf16), 0.75 (MXFP8), E3M2 1.75, 1.4; 1.15
+//   rows (gemm_rows.hip; 256 K a step)  16 x 128 items: E2M1 0.55, E3M2 0.75
+//     (bf16), 0.6;
+//     64 x 128 items: E2M1 1.1 (bf16), 0.75 (MXFP8), E3M2 1.3, 0.95; 1.15
 //     times that with groups
 //   mid (E2M1 x bf16; 128 K a step)  64 x 256 items 1.06, 128 x 256 1.6
 //   tiled (MXFP8)  128 x 256 items 1.08, E3M2 1.3; 192 x 128 0.88, 1.1
@@ -679,7 +680,7 @@ static void linear_kind(const mx_linear_problem_t& p, bool has_a_scale, LinearPl
   }
   const double stages = std::ceil(p.K / (double)kRowsK);
   const double own = p.groups > 0 ? 1.15 : 1.0;  // groups share no weights in the caches
-  const double t16 = own * (e2m1 ? 0.55 : 1.0), t64 = own * (e2m1 ? (mx ? 0.75 : 1.1) : (mx ? 1.4 : 1.75));
+  const double t16 = own * (e2m1 ? 0.55 : mx ? 0.6 : 0.75), t64 = own * (e2m1 ? (mx ? 0.75 : 1.1) : (mx ? 0.95 : 1.3));
   // K ranges of at least two stages, dense calls only
   const int most = p.groups > 0 ? 1 : (int)std::min(16.0, std::max(1.0, std::floor(stages / 2.0)));
   for (int s = 1; s <= most; ++s) {
