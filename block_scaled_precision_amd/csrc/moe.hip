@@ -610,7 +610,7 @@ static bool linear_supported(const mx_linear_problem_t& p) {
 //     64 x 128 items: E2M1 1.1 (bf16), 0.75 (MXFP8), E3M2 1.3, 0.95; 1.15
 //     times that with groups
 //   mid (E2M1 x bf16; 128 K a step)  64 x 256 items 1.06, 128 x 256 1.6
-//   tiled (MXFP8)  128 x 256 items 1.08, E3M2 1.3; 192 x 128 0.88, 1.1
+//   tiled (MXFP8)  128 x 256 items 1.08, E3M2 1.2; 192 x 128 0.88, 1.1
 //   wide (E2M1 x MXFP8)  192 x 256 items 1.27
 //   epilogues with a residual: 13.6 us per 128 x 256 item of mid, 9.6 of tiled, 18 of
 //     wide's, 4.3 of 64 x 128 (8192 x 4096, K = 1024 and 7168)
@@ -697,7 +697,7 @@ static void linear_kind(const mx_linear_problem_t& p, bool has_a_scale, LinearPl
   }
   if (mx) {
     take(Fc::kTiled, kTiledRowsLow, 0,
-         c.time(128, tiled_weight_rows(kTiledRowsLow), steps, e2m1 ? 1.08 : 1.3) + c.before());
+         c.time(128, tiled_weight_rows(kTiledRowsLow), steps, e2m1 ? 1.08 : 1.2) + c.before());
     take(Fc::kTiled, kTiledRows, 0,
          c.time(192, tiled_weight_rows(kTiledRows), steps, e2m1 ? 0.88 : 1.1) + c.before());
     // (its 32-bit offsets into A, and column blocks of 64 inside N)
