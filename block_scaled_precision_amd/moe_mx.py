@@ -242,7 +242,7 @@ def moe_route(logits: torch.Tensor, k: int, workspace: torch.Tensor | None = Non
 class _Plan:
     """One checked and marshalled call of a C entry point: everything but the
     stream, which is its last argument."""
-    __slots__ = ("name", "fn", "args", "result", "device", "keep")
+    __slots__ = ("name", "fn", "args", "result", "device", "keep", "recorded")
 
     def __init__(self, name, args, result, device, keep):
         # sizes cross the ABI as 32-bit integers, strides and addresses as 64-bit
@@ -251,8 +251,11 @@ class _Plan:
                 raise ValueError(f"{name}: size {v} does not fit 32 bits")
         self.name, self.fn, self.args = name, getattr(lib(), name), args
         self.result, self.device, self.keep = result, device, keep
+        self.recorded = set()  # handles of the streams that the tensors' memory is kept for
 
-    def launch(self, stream):
+    def launch(self, stream, prepared=False):
+        """prepared: the plan may hold the last reference to its tensors, and their
+        memory may come from another stream than the one it is launched on."""
         index = self.device.index
         if torch.cuda.current_device() != index:
             raise ValueError(f"{self.name}: tensors on {self.device}, which is not the current device")
@@ -267,7 +270,23 @@ class _Plan:
         status = self.fn(*self.args, handle)
         if status != MOE_OK:
             raise MoeError(status, self.name)
+        if (prepared or stream is not None) and handle not in self.recorded:
+            self._record(stream, handle)
         return self.result
+
+    def _record(self, stream, handle):
+        """Keep the memory of the call's tensors from reuse, once they are dropped, until
+        the stream has run the calls made on it.  Once per stream is enough; a capture
+        does not run, and its graph's tensors have to outlive it anyway."""
+        if torch.cuda.is_current_stream_capturing():
+            return
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        outputs = self.result if isinstance(self.result, tuple) else (self.result,)
+        for t in (*outputs, *self.keep):
+            if t is not None:
+                t.record_stream(stream)
+        self.recorded.add(handle)
 
 
 _PLANNERS = {}  # operator -> function that plans a call of it
@@ -289,7 +308,8 @@ class OpCall:
     host only the C call.  The stream is the current one at each call unless
     one is given.  Calling returns the operator's outputs, the same tensors each
     time: its calls must not run at the same time (on two streams, or in two
-    graphs), and it has to live as long as a graph that captured one.
+    graphs), and it has to live as long as a graph that captured one.  It may be
+    dropped, and so may its outputs and arguments, while a call is still running.
 
         combine = OpCall(moe_unpermute, rows, row_of, topk_w)
         y = combine()
@@ -302,7 +322,7 @@ class OpCall:
         self._stream = stream
 
     def __call__(self):
-        return self._plan.launch(self._stream)
+        return self._plan.launch(self._stream, prepared=True)
 
 
 def _on_gpu(stream, *ts):
