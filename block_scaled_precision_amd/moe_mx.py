@@ -139,6 +139,16 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _hold(stream, *tensors):
+    """Keep the memory of tensors from reuse, once they are dropped, until `stream` has
+    run what was launched on it.  True if that lasts: a record made under capture is
+    for the capture's own allocations, and the graph's tensors have to outlive it."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return not torch.cuda.is_current_stream_capturing()
+
+
 def _dev(*ts):
     dev = None
     for t in ts:
@@ -150,6 +160,17 @@ def _dev(*ts):
             dev = t.device
         elif t.device != dev:
             raise ValueError(f"tensors on different devices ({dev} and {t.device})")
+
+
+def _empty(shape, dtype, device, stream):
+    """An output or workspace of a call on `stream`: from that stream's memory,
+    and kept from reuse while the current stream may still read it."""
+    if stream is None or stream == torch.cuda.current_stream(device):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _require(t, name: str, dtype, shape):
@@ -196,14 +217,16 @@ def mx_quantize(src: torch.Tensor, fmt: str, codes: torch.Tensor | None = None,
     nbytes = cols * FORMAT_BITS[fmt] // 8
     dev = src.device
     if codes is None:
-        codes = torch.empty(src.shape[:-1] + (nbytes,), dtype=torch.uint8, device=dev)
+        codes = _empty(src.shape[:-1] + (nbytes,), torch.uint8, dev, stream)
     if scales is None:
-        scales = torch.empty(src.shape[:-1] + (cols // 32,), dtype=torch.uint8, device=dev)
+        scales = _empty(src.shape[:-1] + (cols // 32,), torch.uint8, dev, stream)
     _require(codes, "codes", torch.uint8, src.shape[:-1] + (nbytes,))
     _require(scales, "scales", torch.uint8, src.shape[:-1] + (cols // 32,))
     _dev(src, codes, scales)
     _check(lib().mx_quantize(_ptr(src2), SRC_DTYPES[src.dtype], rows, cols, ld, MX_FORMATS[fmt],
                              _ptr(codes), _ptr(scales), _stream(stream)), "mx_quantize")
+    if stream is not None:
+        _hold(stream, src, codes, scales)
     return codes, scales
 
 
@@ -223,17 +246,19 @@ def moe_route(logits: torch.Tensor, k: int, workspace: torch.Tensor | None = Non
     if not 1 <= k <= E:
         raise ValueError(f"k = {k} outside [1, E = {E}]")
     dev = logits.device
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    off = torch.empty((E + 1,), dtype=torch.int32, device=dev)
-    sa = torch.empty((T * k,), dtype=torch.int32, device=dev)
+    ids = _empty((T, k), torch.int32, dev, stream)
+    w = _empty((T, k), torch.float32, dev, stream)
+    off = _empty((E + 1,), torch.int32, dev, stream)
+    sa = _empty((T * k,), torch.int32, dev, stream)
     need = moe_route_workspace_bytes(T, E, k)
     if workspace is None:
-        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=dev)
+        workspace = _empty((max(need, 1),), torch.uint8, dev, stream)
     _require_workspace(workspace, need)
     _dev(logits, workspace)
     _check(lib().moe_route(_ptr(logits), T, E, k, _ptr(ids), _ptr(w), _ptr(off), _ptr(sa),
                            _ptr(workspace), workspace.numel(), _stream(stream)), "moe_route")
+    if stream is not None:
+        _hold(stream, logits, ids, w, off, sa, workspace)
     return ids, w, off, sa
 
 
@@ -275,18 +300,10 @@ class _Plan:
         return self.result
 
     def _record(self, stream, handle):
-        """Keep the memory of the call's tensors from reuse, once they are dropped, until
-        the stream has run the calls made on it.  Once per stream is enough; a capture
-        does not run, and its graph's tensors have to outlive it anyway."""
-        if torch.cuda.is_current_stream_capturing():
-            return
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
+        # once per stream is enough
         outputs = self.result if isinstance(self.result, tuple) else (self.result,)
-        for t in (*outputs, *self.keep):
-            if t is not None:
-                t.record_stream(stream)
-        self.recorded.add(handle)
+        if _hold(torch.cuda.current_stream(self.device) if stream is None else stream, *outputs, *self.keep):
+            self.recorded.add(handle)
 
 
 _PLANNERS = {}  # operator -> function that plans a call of it
@@ -335,18 +352,6 @@ def _on_gpu(stream, *ts):
     if stream is not None and stream.device != device:
         raise ValueError(f"stream on {stream.device}, tensors on {device}")
     return device
-
-
-def _empty(shape, dtype, device, stream):
-    """An output or workspace of a call on `stream`: from that stream's memory,
-    and kept from reuse while the current stream may still read it."""
-    current = torch.cuda.current_stream(device)
-    if stream is None or stream == current:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(current)
-    return t
 
 
 def _require_rows(t, name: str, dtype, shape) -> int:
@@ -585,18 +590,20 @@ def mx_gemm(a: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, fmt: str, a
     _require(w, "w", torch.uint8, (N, K * b // 8))
     _require(w_scale, "w_scale", torch.uint8, (N, K // 32))
     if c is None:
-        c = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+        c = _empty((M, N), torch.bfloat16, a.device, stream)
     _require(c, "c", torch.bfloat16, (M, N))
     # MXFP8 from bf16: the quantized A; bf16 with few rows: the K split's partial sums
     need = mx_gemm_workspace_bytes(M, N, K, act, fmt) if a_scale is None else 0
     if workspace is None and need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=a.device)
+        workspace = _empty((need,), torch.uint8, a.device, stream)
     if workspace is not None:
         _require_workspace(workspace, need)
     _dev(a, a_scale, w, w_scale, c, workspace)
     _check(lib().mx_gemm(_ptr(a), _ptr(a_scale), M, N, K, ACTS[act], _ptr(w), _ptr(w_scale), MX_FORMATS[fmt],
                          alpha, _ptr(c), _ptr(workspace), 0 if workspace is None else workspace.numel(),
                          _stream(stream)), "mx_gemm")
+    if stream is not None:
+        _hold(stream, a, a_scale, w, w_scale, c, workspace)
     return c
 
 
@@ -805,10 +812,10 @@ def moe_fused(problem: MoeProblem, x: torch.Tensor, weights: MoeWeights, router_
     stage_events: optional ctypes array of MOE_NUM_STAGES + 1 hipEvent_t
     handles (see HipEvents) recorded at the stage boundaries."""
     if y is None:
-        y = torch.empty((problem.T, problem.H), dtype=torch.bfloat16, device=x.device)
+        y = _empty((problem.T, problem.H), torch.bfloat16, x.device, stream)
     need = moe_fused_workspace_bytes(problem)
     if workspace is None:
-        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=x.device)
+        workspace = _empty((max(need, 1),), torch.uint8, x.device, stream)
     check_fused_args(problem, x, weights, router_logits, topk_ids_in, topk_w_in, y, workspace,
                      topk_ids_out, topk_w_out)
     t = MoeTensors(*(None if v is None else v.data_ptr() for v in (
@@ -819,7 +826,15 @@ def moe_fused(problem: MoeProblem, x: torch.Tensor, weights: MoeWeights, router_
         t.stage_events = ctypes.cast(stage_events, ctypes.c_void_p)
     _check(lib().moe_fused(ctypes.byref(problem), ctypes.byref(t), _ptr(workspace), workspace.numel(),
                            _stream(stream)), "moe_fused")
+    if stream is not None:
+        _hold(stream, *_fused_tensors(x, weights, router_logits, topk_ids_in, topk_w_in, y, workspace, topk_ids_out,
+                                      topk_w_out))
     return y
+
+
+def _fused_tensors(x, weights, *rest):
+    return (x, weights.w1, weights.w1_scale, weights.w2, weights.w2_scale, weights.ws1, weights.ws1_scale, weights.ws2,
+            weights.ws2_scale, *rest)
 
 
 class FusedCall:
@@ -833,10 +848,10 @@ class FusedCall:
                  topk_ids_in=None, topk_w_in=None, y=None, workspace=None, topk_ids_out=None,
                  topk_w_out=None, stream=None):
         if y is None:
-            y = torch.empty((problem.T, problem.H), dtype=torch.bfloat16, device=x.device)
+            y = _empty((problem.T, problem.H), torch.bfloat16, x.device, stream)
         need = moe_fused_workspace_bytes(problem)
         if workspace is None:
-            workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=x.device)
+            workspace = _empty((max(need, 1),), torch.uint8, x.device, stream)
         check_fused_args(problem, x, weights, router_logits, topk_ids_in, topk_w_in, y, workspace,
                          topk_ids_out, topk_w_out)
         self.y = y
@@ -851,15 +866,21 @@ class FusedCall:
         self._tp = ctypes.byref(self._t)
         self._ws = _ptr(workspace)
         self._wsn = workspace.numel()
-        self._stream = None if stream is None else _stream(stream)
+        self._stream, self._handle = stream, None if stream is None else _stream(stream)
+        self._tensors = _fused_tensors(x, weights, router_logits, topk_ids_in, topk_w_in, y, workspace, topk_ids_out,
+                                       topk_w_out)
+        self._recorded = set()  # handles of the streams that the tensors' memory is kept for
         self._fn = lib().moe_fused
 
     def __call__(self, stage_events=None):
         self._t.stage_events = None if stage_events is None else ctypes.cast(stage_events, ctypes.c_void_p)
-        st = self._stream if self._stream is not None else _stream(None)
+        st = self._handle if self._handle is not None else _stream(None)
         status = self._fn(self._p, self._tp, self._ws, self._wsn, st)
         if status != MOE_OK:
             raise MoeError(status, "moe_fused")
+        if st.value not in self._recorded:
+            if _hold(torch.cuda.current_stream() if self._stream is None else self._stream, *self._tensors):
+                self._recorded.add(st.value)
         return self.y
 
 
@@ -876,6 +897,8 @@ def moe_fused_noalloc(problem: MoeProblem, x: torch.Tensor, weights: MoeWeights,
         weights.w2_scale, weights.ws1, weights.ws1_scale, weights.ws2, weights.ws2_scale, y,
         topk_ids_out, topk_w_out)), None)
     _check(lib().moe_fused_noalloc(ctypes.byref(problem), ctypes.byref(t), _stream(stream)), "moe_fused_noalloc")
+    if stream is not None:
+        _hold(stream, *_fused_tensors(x, weights, router_logits, topk_ids_in, topk_w_in, y, topk_ids_out, topk_w_out))
     return y
 
 

@@ -37,6 +37,22 @@ def _operators(m):
     }
 
 
+def _entry_points(m):
+    """name -> (entry point, inputs made anew on the current stream)"""
+    x, logits = gen.normal((T, H), 51, 31).to(BF16), gen.normal((T, E), 51, 30)
+    codes, scales = m.mx_quantize(gen.normal((1024, H), 51, 32, std=0.02).cuda(), "e2m1")
+    w1, s1 = m.mx_quantize(gen.normal((E, 2 * 512, H), 51, 33, std=0.02).cuda(), "e2m1")
+    w2, s2 = m.mx_quantize(gen.normal((E, H, 512), 51, 34, std=0.02).cuda(), "e2m1")
+    problem = m.make_problem(T, H, 512, E, K, "e2m1", "mxfp8")
+    torch.cuda.synchronize()
+    return {
+        "quantize": (m.mx_quantize, lambda: (x.cuda(), "e4m3")),
+        "route": (m.moe_route, lambda: (logits.cuda(), K)),
+        "gemm": (m.mx_gemm, lambda: (x.cuda(), codes.clone(), scales.clone(), "e2m1")),
+        "fused": (m.moe_fused, lambda: (problem, x.cuda(), m.MoeWeights(w1, s1, w2, s2, "e2m1"), logits.cuda())),
+    }
+
+
 def _ranges(*ts):
     return [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in ts if isinstance(t, torch.Tensor)]
 
@@ -78,11 +94,13 @@ def test_prepared_call_dropped_while_it_runs(name):
     del new
 
 
-@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("name", NAMES + ["quantize", "route", "gemm", "fused"])
 def test_stream_argument_with_inputs_dropped(name):
+    """Inputs, and workspaces that the call allocates and drops itself: what comes in
+    their place is filled at once, and the results are those of an undisturbed call."""
     from block_scaled_precision_amd import moe_mx as m
     print_flush(f"streams: argument {name}")
-    op, make = _operators(m)[name]
+    op, make = {**_operators(m), **_entry_points(m)}[name]
     side = torch.cuda.Stream()
     want = op(*make())
     args = make()
@@ -96,6 +114,8 @@ def test_stream_argument_with_inputs_dropped(name):
     del args
     for t in _free_of(used):
         t.fill_(0xFF)
+    for size in (1 << 16, 1 << 18, 1 << 20, 3 << 20, 8 << 20):
+        torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xFF)
     torch.cuda.current_stream().wait_stream(side)
     for got, ref in zip(out if isinstance(out, tuple) else (out,), want if isinstance(want, tuple) else (want,)):
         assert torch.equal(got, ref)
@@ -120,3 +140,46 @@ def test_prepared_call_captured_then_called_and_dropped():
     del graph, call, out
     torch.cuda.synchronize()
     assert torch.equal(op(*args), want)
+
+
+def test_prepared_layer_dropped_while_it_runs():
+    from block_scaled_precision_amd import moe_mx as m
+    make = _entry_points(m)["fused"][1]
+    args = make()
+    call = m.FusedCall(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(CYCLES)
+        y = call()
+    used = _ranges(args[1], args[3], y, call._keep[6])
+    assert not side.query()
+    del args, call, y
+    new = _free_of(used)
+    torch.cuda.synchronize()
+    del new
+
+
+def test_stream_argument_under_capture():
+    """A side stream forked inside a capture: inputs dropped there are not reused by
+    what the capture allocates next."""
+    from block_scaled_precision_amd import moe_mx as m
+    op, make = _operators(m)["linear"]
+    base = make()
+    want = op(base[0] * 2, *base[1:])
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    main.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        a = base[0] * 2
+        side.wait_stream(main)
+        out = op(a, *base[1:], stream=side)
+        del a
+        other = base[0] * 3  # of a's size, while the side stream reads a
+        main.wait_stream(side)
+    for _ in range(4):
+        out.zero_()
+        other.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(other, base[0] * 3)
