@@ -77,8 +77,9 @@ __device__ __forceinline__ float gelu(float v) {
   const float q = 0.5f * t * p * __builtin_amdgcn_exp2f(-0.72134752f * (v * v));  // exp(-v^2 / 2)
   return v * (v < 0.0f ? q : 1.0f - q);
 }
+// (a comparison, not a maximum, which would turn NaN into 0)
 __device__ __forceinline__ float relu2(float v) {
-  const float r = fmaxf(v, 0.0f);
+  const float r = v < 0.0f ? 0.0f : v;
   return r * r;
 }
 // (one choice for the eight values of a piece)

@@ -319,3 +319,28 @@ def test_many_rows_of_few_columns():
     out = m.mx_linear(a, w[0].cuda(), s[0].cuda(), "e2m1", "bf16")
     assert torch.equal(out[-40:], m.mx_linear(a[-40:].contiguous(), w[0].cuda(), s[0].cuda(), "e2m1", "bf16"))
     assert (out[:-40] == out[0]).all()
+
+
+@pytest.mark.parametrize("fn", ["none", "silu", "gelu", "relu2"])
+@pytest.mark.parametrize("M,N,K,G,fmt,act", [c[3:] for c in CASES if c[8] == "bf16"],
+                         ids=[n for n, c in zip(_NAMES, CASES) if c[8] == "bf16"])
+def test_nan_and_infinity_arrive(M, N, K, G, fmt, act, fn):
+    """A NaN in one row of A makes that row of out NaN whatever the function, a bias of
+    infinity its column infinite; the rest is as without them."""
+    from block_scaled_precision_amd import moe_mx as m
+    print_flush(f"mx_linear kernels: NaN {fn} M={M} N={N} K={K} G={G} {fmt}")
+    offsets, P, w, s, wd, sd, off = _problem(M, N, K, G, fmt, act, 39, scales=(116, 121))
+    a = gen.normal((M, K), 39, 25).to(BF16).cuda()
+    bias = gen.normal((max(G, 1), N), 39, 26).cuda()
+    call = lambda: m.mx_linear(a, wd, sd, fmt, act, bias=bias if G else bias[0], fn=fn, expert_offsets=off)[:P].clone()
+    plain = call()
+    row, col = P // 2, N - 3
+    a[row, K - 1] = float("nan")
+    bias[:, col] = float("inf")
+    out = call()
+    assert torch.isnan(out[row]).all()
+    keep = torch.ones(P, dtype=torch.bool, device="cuda")
+    keep[row] = False
+    assert (out[keep, col] == float("inf")).all()
+    plain[:, col] = float("inf")
+    assert torch.equal(out[keep], plain[keep])
