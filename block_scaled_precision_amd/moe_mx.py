@@ -263,6 +263,9 @@ def moe_route(logits: torch.Tensor, k: int, workspace: torch.Tensor | None = Non
 
 
 # ------------------------------------------------------- operator calls --
+#
+# The operators compute outside autograd.  Where gradients are on, they refuse a tensor
+# that requires one.
 
 class _Plan:
     """One checked and marshalled call of a C entry point: everything but the
@@ -392,6 +395,16 @@ def _disjoint(outputs: dict, inputs: dict):
         ranges.append((name, (lo, hi)))
 
 
+def _no_graph(op: str, gradient: str, **tensors):
+    """The operators record nothing for autograd: a tensor that waits for a gradient
+    would silently get none."""
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"{name} requires a gradient, which {op} does not record: call it under "
+                                 f"torch.no_grad() or in a torch.autograd.Function ({gradient})")
+
+
 # ------------------------------------------------------------- dispatch --
 
 def _row_dtype(t, name):
@@ -413,6 +426,7 @@ def _tokens_slots(row_of):
 
 def _plan_permute(x, sorted_assign, expert_offsets, k, local_offset=0, local_count=0, rows=None, row_of=None,
                   stream=None):
+    _no_graph("moe_permute", "its gradient: moe_permute_backward", x=x, rows=rows)
     dtype = _row_dtype(x, "x")
     T, H = x.shape
     x_ld = _require_rows(x, "x", dtype, (T, H))
@@ -456,6 +470,7 @@ def moe_permute(x: torch.Tensor, sorted_assign: torch.Tensor, expert_offsets: to
 
 
 def _plan_permute_backward(drows, row_of, dx=None, stream=None):
+    _no_graph("moe_permute_backward", "of the second order", drows=drows, dx=dx)
     dtype = _row_dtype(drows, "drows")
     (R, H), (T, k) = drows.shape, _tokens_slots(row_of)
     ld = _require_rows(drows, "drows", dtype, (R, H))
@@ -477,6 +492,7 @@ def moe_permute_backward(drows: torch.Tensor, row_of: torch.Tensor, dx: torch.Te
 
 
 def _plan_unpermute(rows, row_of, topk_w, residual=None, y=None, stream=None):
+    _no_graph("moe_unpermute", "its gradient: moe_unpermute_backward", rows=rows, topk_w=topk_w, residual=residual, y=y)
     dtype = _row_dtype(rows, "rows")
     (R, H), (T, k) = rows.shape, _tokens_slots(row_of)
     ld = _require_rows(rows, "rows", dtype, (R, H))
@@ -504,6 +520,7 @@ def moe_unpermute(rows: torch.Tensor, row_of: torch.Tensor, topk_w: torch.Tensor
 
 
 def _plan_unpermute_backward(dy, rows, row_of, topk_w, drows=None, dw=None, stream=None):
+    _no_graph("moe_unpermute_backward", "of the second order", dy=dy, rows=rows, topk_w=topk_w, drows=drows, dw=dw)
     dtype = _row_dtype(rows, "rows")
     (R, H), (T, k) = rows.shape, _tokens_slots(row_of)
     ld = _require_rows(rows, "rows", dtype, (R, H))
@@ -534,6 +551,7 @@ def moe_unpermute_backward(dy: torch.Tensor, rows: torch.Tensor, row_of: torch.T
 
 
 def _plan_route_backward(topk_ids, topk_w, dw, num_experts, dlogits=None, stream=None):
+    _no_graph("moe_route_backward", "of the second order", topk_w=topk_w, dw=dw, dlogits=dlogits)
     if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2 or topk_ids.shape[1] == 0:
         raise ValueError("topk_ids: expected [T, k] with k >= 1")
     T, k = topk_ids.shape
@@ -630,6 +648,8 @@ def _group_stride(t, name, shape, groups):
 
 def _plan_linear(a, w, w_scale, fmt, act="mxfp8", a_scale=None, bias=None, fn="none", mul=None, residual=None,
                  expert_offsets=None, out=None, workspace=None, stream=None):
+    _no_graph("mx_linear", "of the user's own: there is no gradient through packed weights here", a=a, bias=bias, mul=mul,
+              residual=residual, out=out)
     if fmt not in ("e2m1", "e3m2"):
         raise ValueError(f"weight format {fmt!r} is not e2m1 or e3m2")
     if act not in ACTS:
