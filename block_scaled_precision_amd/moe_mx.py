@@ -385,7 +385,8 @@ def _extent(t):
 
 
 def _disjoint(outputs: dict, inputs: dict):
-    """No output shares memory with an input or another output."""
+    """No output shares memory with an input or another output: refused from the first
+    to the last element of each, so also between columns of one buffer."""
     ranges = [(n, _extent(t)) for n, t in inputs.items() if t is not None]
     for name, t in outputs.items():
         lo, hi = _extent(t)
