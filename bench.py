@@ -54,9 +54,9 @@ BOUND = {
 FC1_KERNEL = {
     "tiny_w4a16": "k_fc_small_routed<1, 1>",  # 16 tokens: FC1 routes the batch itself
     "decode_w4a16": "k_fc_small<true, 4>",
-    "prefill_w4a8": "k_fc_wide<true, 0>",
-    "skew_w4a16": "k_fc_mid<true, 128>",
-    "w6a8_shared": "k_fc_tiled<true, 2, 128, false>",
+    "prefill_w4a8": "k_fc_wide<true, 0, false>",
+    "skew_w4a16": "k_fc_mid<true, 128, false>",
+    "w6a8_shared": "k_fc_tiled<true, 2, 128, false, false>",
 }
 
 # Sources of the GEMM kernels: a committed HBM-traffic summary counts only

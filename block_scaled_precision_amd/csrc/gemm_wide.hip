@@ -647,7 +647,7 @@ __device__ __forceinline__ void wave_main(const FcArgs& p, const Sched& sc, uint
     if (ci + 1 < sc.my_items) {
       it = item_geom(p, sc, ci + 1);
       nm = wave_subs(it.rows);
-        }
+    }
   }
   wait_vm_lgkm0<0>();
 }
