@@ -344,3 +344,60 @@ def test_nan_and_infinity_arrive(M, N, K, G, fmt, act, fn):
     assert (out[keep, col] == float("inf")).all()
     plain[:, col] = float("inf")
     assert torch.equal(out[keep], plain[keep])
+
+
+# (kernel, M, N, K, groups, fmt, act): outputs of more than 2^32 values, or activations
+# of more than 2^32 bytes; for wide, whose offsets into them have 32 bits, just fewer
+LONG = [
+    ("mid", (1 << 32) // 4104 + 1000, 4104, 512, 0, "e2m1", "bf16"),
+    ("mid", (1 << 32) // 4104 + 1000, 4104, 512, 5, "e2m1", "bf16"),
+    ("rows", (1 << 31) // 1024 + 1000, 264, 1024, 0, "e2m1", "bf16"),
+    ("rows", (1 << 31) // 1024 + 1000, 264, 1024, 5, "e3m2", "bf16"),
+    ("tiled", (1 << 32) // 4104 + 1000, 4104, 512, 0, "e3m2", "mxfp8"),
+    ("tiled", (1 << 32) // 1024 + 1000, 264, 1024, 0, "e2m1", "mxfp8"),
+    ("tiled", (1 << 32) // 1024 + 1000, 264, 1024, 5, "e3m2", "mxfp8"),
+    ("wide", (1 << 32) // 4096 - 100, 4160, 4096, 0, "e2m1", "mxfp8"),
+    ("wide", (1 << 32) // 4160 + 1000, 4160, 1024, 5, "e2m1", "mxfp8"),
+    ("tiled", (1 << 32) // 4096 + 100, 4160, 4096, 0, "e2m1", "mxfp8"),
+]
+
+
+@pytest.mark.parametrize("kernel,M,N,K,G,fmt,act", LONG, ids=[f"{c[0]}_{c[1]}x{c[2]}x{c[3]}_G{c[4]}_{c[5]}_{c[6]}" for c in LONG])
+def test_long_batches(kernel, M, N, K, G, fmt, act):
+    """Rows of ones, the last 40 of small integers: those against the same rows alone,
+    the others against the first of their group.  Every sum is exact."""
+    from block_scaled_precision_amd import moe_mx as m
+    print_flush(f"mx_linear kernels: long {kernel} M={M} N={N} K={K} G={G} {fmt}/{act}")
+    offsets, P, w, s, wd, sd, off = _problem(M, N, K, G, fmt, act, 40)
+    tail = gen.small_integers((40, K), 40, 20).to(BF16).cuda()
+    a = torch.ones((M, K), dtype=BF16, device="cuda")
+    a[P - 40:P] = tail
+    out = m.mx_linear(a, wd, sd, fmt, act, expert_offsets=off)
+    last = (wd[G - 1], sd[G - 1]) if G else (wd, sd)
+    assert torch.equal(out[P - 40:P], m.mx_linear(tail, *last, fmt, act))
+    bounds = [0, P] if offsets is None else [o - offsets[0] for o in offsets]
+    for g, (lo, hi) in enumerate(zip(bounds[:-1], bounds[1:])):
+        hi = min(hi, P - 40)
+        if lo < hi:
+            one = m.mx_linear(a[:1], *((wd[g], sd[g]) if G else (wd, sd)), fmt, act)
+            for i in range(lo, hi, 1 << 18):
+                assert (out[i:min(hi, i + (1 << 18))] == one).all(), f"group {g}, rows from {i}"
+
+
+@pytest.mark.parametrize("M,N,K,G,fmt,act", LARGE, ids=LARGE_IDS)
+def test_halves_slices_and_codes(M, N, K, G, fmt, act):
+    """The up half of [gate; up] weights, offsets that are a slice of a longer table,
+    and activations given as codes and scales: the same bits as copies and bf16 rows."""
+    from block_scaled_precision_amd import moe_mx as m
+    print_flush(f"mx_linear kernels: halves and codes M={M} N={N} K={K} G={G} {fmt}/{act}")
+    _, P, _, _, wd, sd, off = _problem(M, 2 * N, K, G, fmt, act, 41, scales=(116, 121))
+    a = gen.normal((M, K), 41, 25).to(BF16).cuda()
+    wu, su = wd[..., N:, :], sd[..., N:, :]
+    want = m.mx_linear(a, wu.contiguous(), su.contiguous(), fmt, act, fn="gelu", expert_offsets=off)[:P]
+    kw = dict(fn="gelu")
+    if G:
+        kw["expert_offsets"] = torch.cat([off.new_tensor([0, 3, 5]), off, off.new_tensor([M + 9])])[3:4 + G]
+    assert torch.equal(m.mx_linear(a, wu, su, fmt, act, **kw)[:P], want)
+    if act == "mxfp8":
+        codes, scales = m.mx_quantize(a, "e4m3")
+        assert torch.equal(m.mx_linear(codes, wu, su, fmt, act, a_scale=scales, **kw)[:P], want)

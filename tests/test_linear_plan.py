@@ -55,3 +55,9 @@ def test_kernel_cases_cover_every_choice():
         for fmt, act in TYPES:
             own = [c for c in CASES if c[0] == kernel and c[7:] == (fmt, act)]
             assert not own or any(c[5] % 512 for c in own), (kernel, fmt, act)
+
+
+def test_long_cases_take_the_kernels_they_name():
+    from tests.test_gpu_linear_kernels import LONG
+    got = plans([c[1:] for c in LONG])
+    assert [p.kernel for p in got] == [c[0] for c in LONG]
