@@ -60,4 +60,7 @@ hipError_t launch_route_permute_small(const float* logits, int T, int E, int k, 
 hipError_t launch_group_tiles(const int32_t* offsets, int groups, int64_t M, int bm, Tile* tiles,
                               int32_t* num_tiles, hipStream_t stream);
 
+// E4M3 codes of `bytes` bytes of E2M1 codes (bytes % 4 == 0), two bytes for one.
+hipError_t launch_mx4_expand(const uint8_t* codes, int64_t bytes, uint8_t* out, hipStream_t stream);
+
 }  // namespace moe_mx

@@ -25,8 +25,10 @@ ACT_FNS = {"silu": 0, "relu2": 1, "swiglu_oai": 2}
 
 # Every symbol include/moe_mx.h declares.
 EXPORTS = ("mx_quantize", "moe_route_workspace_bytes", "moe_route", "moe_permute", "moe_permute_backward",
-           "moe_unpermute", "moe_unpermute_backward", "moe_route_backward", "mx_gemm_workspace_bytes", "mx_gemm",
-           "mx_linear_workspace_bytes", "mx_linear",
+           "moe_unpermute", "moe_unpermute_backward", "moe_route_backward", "moe_balance_workspace_bytes", "moe_balance",
+           "moe_balance_backward", "mx_gemm_workspace_bytes", "mx_gemm",
+           "mx_linear_workspace_bytes", "mx_linear", "mx4_quantize", "mx4_dequantize", "mx4_linear_workspace_bytes",
+           "mx4_linear",
            "moe_fused_workspace_bytes", "moe_fused", "moe_fused_workspace_offset", "moe_fused_noalloc",
            "moe_status_str", "moe_mx_version")
 NOALLOC_SCRATCH_BYTES = 32 << 20  # MOE_NOALLOC_SCRATCH_BYTES
@@ -50,6 +52,12 @@ class MxLinearProblem(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("groups", ctypes.c_int32),
                 ("act", ctypes.c_int), ("w_fmt", ctypes.c_int), ("fn", ctypes.c_int), ("bias_dtype", ctypes.c_int),
                 ("w_stride", ctypes.c_int64), ("w_scale_stride", ctypes.c_int64)]
+
+
+class Mx4LinearProblem(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("groups", ctypes.c_int32),
+                ("fn", ctypes.c_int), ("bias_dtype", ctypes.c_int), ("w_stride", ctypes.c_int64),
+                ("w_scale_stride", ctypes.c_int64)]
 
 
 class MxLinearTensors(ctypes.Structure):
@@ -104,10 +112,24 @@ def lib() -> ctypes.CDLL:
         L.moe_unpermute_backward.restype = i
         L.moe_route_backward.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp]
         L.moe_route_backward.restype = i
+        L.moe_balance_workspace_bytes.argtypes = [i32, i32, i32]
+        L.moe_balance_workspace_bytes.restype = sz
+        L.moe_balance.argtypes = [vp, i64, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_balance.restype = i
+        L.moe_balance_backward.argtypes = [vp, vp, i64, vp, vp, vp, vp, i32, i32, i32, i32, vp, i64, vp, i64, vp]
+        L.moe_balance_backward.restype = i
         L.mx_linear_workspace_bytes.argtypes = [ctypes.POINTER(MxLinearProblem), i]
         L.mx_linear_workspace_bytes.restype = sz
         L.mx_linear.argtypes = [ctypes.POINTER(MxLinearProblem), ctypes.POINTER(MxLinearTensors), vp, sz, vp]
         L.mx_linear.restype = i
+        L.mx4_quantize.argtypes = [vp, i, i64, i64, i64, i64, i, vp, vp, vp, vp, vp]
+        L.mx4_quantize.restype = i
+        L.mx4_dequantize.argtypes = [vp, vp, i64, i64, vp, i, i64, vp]
+        L.mx4_dequantize.restype = i
+        L.mx4_linear_workspace_bytes.argtypes = [ctypes.POINTER(Mx4LinearProblem), i]
+        L.mx4_linear_workspace_bytes.restype = sz
+        L.mx4_linear.argtypes = [ctypes.POINTER(Mx4LinearProblem), ctypes.POINTER(MxLinearTensors), vp, sz, vp]
+        L.mx4_linear.restype = i
         L.moe_fused_noalloc.argtypes = [ctypes.POINTER(MoeProblem), ctypes.POINTER(MoeTensors), vp]
         L.moe_fused_noalloc.restype = ctypes.c_int
         L.moe_fused_workspace_offset.argtypes = [ctypes.POINTER(MoeProblem), ctypes.c_int]
@@ -578,6 +600,131 @@ def moe_route_backward(topk_ids: torch.Tensor, topk_w: torch.Tensor, dw: torch.T
     return _plan_route_backward(topk_ids, topk_w, dw, num_experts, dlogits, stream).launch(stream)
 
 
+# -------------------------------------------------------------- balance --
+
+def _require_router(logits, k):
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.shape[1] == 0:
+        raise ValueError("logits: expected [T, E]")
+    T, E = logits.shape
+    ld = _require_rows(logits, "logits", torch.float32, (T, E))
+    if not 1 <= k <= E:
+        raise ValueError(f"k = {k} outside [1, E = {E}]")
+    return T, E, ld
+
+
+def _require_sequences(seq_offsets):
+    """The number of sequences."""
+    if seq_offsets is None:
+        return 1
+    if not isinstance(seq_offsets, torch.Tensor) or seq_offsets.dim() != 1 or seq_offsets.numel() < 2:
+        raise ValueError("seq_offsets: expected [sequences + 1]")
+    _require(seq_offsets, "seq_offsets", torch.int32, seq_offsets.shape)
+    return seq_offsets.numel() - 1
+
+
+def _data_ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def moe_balance_workspace_bytes(T: int, E: int, sequences: int = 1) -> int:
+    return lib().moe_balance_workspace_bytes(T, E, sequences)
+
+
+def _plan_balance(logits, topk_ids, mask=None, seq_offsets=None, loss=None, counts=None, tokens=None, lse=None,
+                  workspace=None, stream=None):
+    _no_graph("moe_balance", "its gradient: moe_balance_backward", logits=logits, loss=loss, lse=lse)
+    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
+        raise ValueError("topk_ids: expected [T, k]")
+    k = topk_ids.shape[1]
+    T, E, ld = _require_router(logits, k)
+    _require(topk_ids, "topk_ids", torch.int32, (T, k))
+    if mask is not None:
+        if not isinstance(mask, torch.Tensor) or mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("mask: expected a bool or uint8 tensor")
+        _require(mask, "mask", mask.dtype, (T,))
+    S = _require_sequences(seq_offsets)
+    device = _on_gpu(stream, logits, topk_ids, mask, seq_offsets, loss, counts, tokens, lse, workspace)
+    if loss is None:
+        loss = _empty((2,), torch.float32, device, stream)
+    if counts is None:
+        counts = _empty((S, E), torch.int32, device, stream)
+    if tokens is None:
+        tokens = _empty((S + 2,), torch.int32, device, stream)
+    if lse is None:
+        lse = _empty((T,), torch.float32, device, stream)
+    _require(loss, "loss", torch.float32, (2,))
+    _require(counts, "counts", torch.int32, (S, E))
+    _require(tokens, "tokens", torch.int32, (S + 2,))
+    _require(lse, "lse", torch.float32, (T,))
+    need = moe_balance_workspace_bytes(T, E, S)
+    if workspace is None and need:
+        workspace = _empty((need,), torch.uint8, device, stream)
+    outputs = {"loss": loss, "counts": counts, "tokens": tokens, "lse": lse}
+    if workspace is not None:
+        _require_workspace(workspace, need)
+        outputs["workspace"] = workspace
+    _disjoint(outputs, {"logits": logits, "topk_ids": topk_ids, "mask": mask, "seq_offsets": seq_offsets})
+    return _Plan("moe_balance", (logits.data_ptr(), ld, topk_ids.data_ptr(), _data_ptr(mask), _data_ptr(seq_offsets),
+                                 T, E, k, S, loss.data_ptr(), counts.data_ptr(), tokens.data_ptr(), lse.data_ptr(),
+                                 _data_ptr(workspace), 0 if workspace is None else workspace.numel()),
+                 (loss, counts, tokens, lse), device, (logits, topk_ids, mask, seq_offsets, workspace))
+
+
+@_operator(_plan_balance)
+def moe_balance(logits: torch.Tensor, topk_ids: torch.Tensor, mask: torch.Tensor | None = None,
+                seq_offsets: torch.Tensor | None = None, loss: torch.Tensor | None = None,
+                counts: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+                lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """-> (loss [2] fp32: load balance and z-loss, counts [S, E] int32, tokens [S + 2]
+    int32, lse [T] fp32) of router logits [T, E] fp32 and topk_ids [T, k] (moe_route).
+
+    seq_offsets [S + 1] int32 are the sequences of a packed batch (None: one, of all
+    tokens), mask [T] bool or uint8 the tokens that count; a token outside every
+    sequence or with all logits -inf does not.  The balance loss is the mean over the
+    sequences of E sum_e f_e P_e, f_e the share of assignments to expert e and P_e its mean
+    probability; the z-loss the mean of lse^2.  tokens: each sequence's, all, and
+    the number of sequences with one."""
+    return _plan_balance(logits, topk_ids, mask, seq_offsets, loss, counts, tokens, lse, workspace,
+                         stream).launch(stream)
+
+
+def _plan_balance_backward(dloss, logits, counts, tokens, lse, k, seq_offsets=None, add=None, dlogits=None,
+                           stream=None):
+    _no_graph("moe_balance_backward", "of the second order", dloss=dloss, logits=logits, lse=lse, add=add,
+              dlogits=dlogits)
+    T, E, ld = _require_router(logits, k)
+    S = _require_sequences(seq_offsets)
+    _require(dloss, "dloss", torch.float32, (2,))
+    _require(counts, "counts", torch.int32, (S, E))
+    _require(tokens, "tokens", torch.int32, (S + 2,))
+    _require(lse, "lse", torch.float32, (T,))
+    add_ld = 0 if add is None else _require_rows(add, "add", torch.float32, (T, E))
+    device = _on_gpu(stream, dloss, logits, counts, tokens, lse, seq_offsets, add, dlogits)
+    if dlogits is None:
+        dlogits = _empty((T, E), torch.float32, device, stream)
+    out_ld = _require_rows(dlogits, "dlogits", torch.float32, (T, E))
+    in_place = add is not None and add.data_ptr() == dlogits.data_ptr() and add_ld == out_ld
+    _disjoint({"dlogits": dlogits}, {"dloss": dloss, "logits": logits, "counts": counts, "tokens": tokens, "lse": lse,
+                                     "seq_offsets": seq_offsets, "add": None if in_place else add})
+    return _Plan("moe_balance_backward", (dloss.data_ptr(), logits.data_ptr(), ld, counts.data_ptr(),
+                                          tokens.data_ptr(), lse.data_ptr(), _data_ptr(seq_offsets), T, E, k, S,
+                                          _data_ptr(add), add_ld, dlogits.data_ptr(), out_ld),
+                 dlogits, device, (dloss, logits, counts, tokens, lse, seq_offsets, add))
+
+
+@_operator(_plan_balance_backward)
+def moe_balance_backward(dloss: torch.Tensor, logits: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor,
+                         lse: torch.Tensor, k: int, seq_offsets: torch.Tensor | None = None,
+                         add: torch.Tensor | None = None, dlogits: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """Gradient of moe_balance's losses: dlogits [T, E] fp32 from dloss [2] fp32 and what
+    moe_balance returned, plus add [T, E] (another gradient of the logits, such as
+    moe_route_backward's; dlogits may be add itself).  The counts are constants; a token
+    that does not count gets add, or 0."""
+    return _plan_balance_backward(dloss, logits, counts, tokens, lse, k, seq_offsets, add, dlogits,
+                                  stream).launch(stream)
+
+
 # ---------------------------------------------------------------- gemm ---
 
 def mx_gemm_workspace_bytes(M: int, N: int, K: int, act: str, w_fmt: str) -> int:
@@ -647,14 +794,13 @@ def _group_stride(t, name, shape, groups):
     return t.stride(0) if groups > 1 else 0
 
 
-def _plan_linear(a, w, w_scale, fmt, act="mxfp8", a_scale=None, bias=None, fn="none", mul=None, residual=None,
-                 expert_offsets=None, out=None, workspace=None, stream=None):
-    _no_graph("mx_linear", "of the user's own: there is no gradient through packed weights here", a=a, bias=bias, mul=mul,
+def _call_linear(name, problem_of, a, a_bits, w, w_scale, fmt, a_scale, bias, fn, mul, residual, expert_offsets, out,
+                 workspace, stream):
+    """The checked call of entry point `name`: activations a [M, K] bf16, or with a_scale
+    codes of a_bits bits; problem_of(M, N, K, groups, bias dtype, strides) -> its
+    problem structure."""
+    _no_graph(name, "of the user's own: there is no gradient through packed weights here", a=a, bias=bias, mul=mul,
               residual=residual, out=out)
-    if fmt not in ("e2m1", "e3m2"):
-        raise ValueError(f"weight format {fmt!r} is not e2m1 or e3m2")
-    if act not in ACTS:
-        raise ValueError(f"unknown activation precision {act!r}")
     if fn not in LINEAR_FNS:
         raise ValueError(f"unknown activation function {fn!r}")
     grouped = expert_offsets is not None
@@ -663,6 +809,8 @@ def _plan_linear(a, w, w_scale, fmt, act="mxfp8", a_scale=None, bias=None, fn="n
     if not isinstance(w, torch.Tensor) or w.dim() != (3 if grouped else 2):
         raise ValueError("w: expected [groups, N, K*b/8] with expert_offsets, [N, K*b/8] without")
     M, K = a.shape
+    if a_scale is not None:
+        K = K * 8 // a_bits
     N, G = w.shape[-2], w.shape[0] if grouped else 0
     if N == 0 or N % 8 or K == 0 or K % 128:
         raise ValueError(f"N = {N} must be a positive multiple of 8, K = {K} of 128")
@@ -671,9 +819,7 @@ def _plan_linear(a, w, w_scale, fmt, act="mxfp8", a_scale=None, bias=None, fn="n
     if a_scale is None:
         _require(a, "a", torch.bfloat16, (M, K))
     else:
-        if act != "mxfp8":
-            raise ValueError("a_scale goes with act='mxfp8'")
-        _require(a, "a", torch.uint8, (M, K))
+        _require(a, "a", torch.uint8, (M, K * a_bits // 8))
         _require(a_scale, "a_scale", torch.uint8, (M, K // 32))
     w_stride = _group_stride(w, "w", (N, K * FORMAT_BITS[fmt] // 8), G)
     s_stride = _group_stride(w_scale, "w_scale", (N, K // 32), G)
@@ -683,16 +829,15 @@ def _plan_linear(a, w, w_scale, fmt, act="mxfp8", a_scale=None, bias=None, fn="n
         if not isinstance(bias, torch.Tensor) or bias.dtype not in SRC_DTYPES:
             raise ValueError("bias: expected a bfloat16 or float32 tensor")
         _require(bias, "bias", bias.dtype, (G, N) if grouped else (N,))
-    for name, t in (("mul", mul), ("residual", residual)):
+    for what, t in (("mul", mul), ("residual", residual)):
         if t is not None:
-            _require(t, name, torch.bfloat16, (M, N))
+            _require(t, what, torch.bfloat16, (M, N))
     device = _on_gpu(stream, a, a_scale, w, w_scale, bias, mul, residual, expert_offsets, out, workspace)
     if out is None:
         out = _empty((M, N), torch.bfloat16, device, stream)
     _require(out, "out", torch.bfloat16, (M, N))
-    problem = MxLinearProblem(M, N, K, G, ACTS[act], MX_FORMATS[fmt], LINEAR_FNS[fn],
-                              0 if bias is None else SRC_DTYPES[bias.dtype], w_stride, s_stride)
-    need = lib().mx_linear_workspace_bytes(ctypes.byref(problem), a_scale is not None)
+    problem = problem_of(M, N, K, G, 0 if bias is None else SRC_DTYPES[bias.dtype], w_stride, s_stride)
+    need = getattr(lib(), name + "_workspace_bytes")(ctypes.byref(problem), a_scale is not None)
     if workspace is None and need:
         workspace = _empty((need,), torch.uint8, device, stream)
     if workspace is not None:
@@ -706,10 +851,25 @@ def _plan_linear(a, w, w_scale, fmt, act="mxfp8", a_scale=None, bias=None, fn="n
         _disjoint({"workspace": workspace}, {"mul": mul, "residual": residual})
     tensors = MxLinearTensors(*(None if t is None else t.data_ptr() for t in (
         a, a_scale, w, w_scale, bias, mul, residual, expert_offsets, out)))
-    return _Plan("mx_linear", (ctypes.byref(problem), ctypes.byref(tensors),
-                               None if workspace is None else workspace.data_ptr(),
-                               0 if workspace is None else workspace.numel()),
+    return _Plan(name, (ctypes.byref(problem), ctypes.byref(tensors),
+                        None if workspace is None else workspace.data_ptr(),
+                        0 if workspace is None else workspace.numel()),
                  out, device, (a, a_scale, w, w_scale, bias, mul, residual, expert_offsets, workspace))
+
+
+def _plan_linear(a, w, w_scale, fmt, act="mxfp8", a_scale=None, bias=None, fn="none", mul=None, residual=None,
+                 expert_offsets=None, out=None, workspace=None, stream=None):
+    if fmt not in ("e2m1", "e3m2"):
+        raise ValueError(f"weight format {fmt!r} is not e2m1 or e3m2")
+    if act not in ACTS:
+        raise ValueError(f"unknown activation precision {act!r}")
+    if a_scale is not None and act != "mxfp8":
+        raise ValueError("a_scale goes with act='mxfp8'")
+
+    def problem(M, N, K, G, bias_dtype, w_stride, s_stride):
+        return MxLinearProblem(M, N, K, G, ACTS[act], MX_FORMATS[fmt], LINEAR_FNS[fn], bias_dtype, w_stride, s_stride)
+    return _call_linear("mx_linear", problem, a, 8, w, w_scale, fmt, a_scale, bias, fn, mul, residual, expert_offsets,
+                        out, workspace, stream)
 
 
 @_operator(_plan_linear)
@@ -730,6 +890,114 @@ def mx_linear(a: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, fmt: str,
     offsets."""
     return _plan_linear(a, w, w_scale, fmt, act, a_scale, bias, fn, mul, residual, expert_offsets, out, workspace,
                         stream).launch(stream)
+
+
+# ------------------------------------------------------------------ mx4 --
+
+def _plan_quantize4(src, transpose=False, signs=None, random=None, codes=None, scales=None, stream=None):
+    _no_graph("mx4_quantize", "of the user's own: rounding has none", src=src)
+    if not isinstance(src, torch.Tensor) or src.dim() not in (2, 3):
+        raise ValueError("src: expected [rows, cols] or [batch, rows, cols]")
+    if src.dtype not in SRC_DTYPES:
+        raise ValueError(f"src: dtype {src.dtype}, expected bfloat16 or float32")
+    rows, cols = src.shape[-2:]
+    if cols == 0:
+        raise ValueError("src: needs at least one column")
+    if src.dim() == 2:
+        batch, ld = 1, _require_rows(src, "src", src.dtype, (rows, cols))
+    else:
+        _require(src, "src", src.dtype, src.shape)
+        batch, ld = src.shape[0], cols
+    if signs is not None:
+        _require(signs, "signs", torch.float32, (32,))
+    if random is not None:
+        _require(random, "random", torch.uint8, src.shape)
+    out, K = (cols, rows) if transpose else (rows, cols)
+    K = -(-K // 128) * 128
+    device = _on_gpu(stream, src, signs, random, codes, scales)
+    lead = src.shape[:-2]
+    if codes is None:
+        codes = _empty((*lead, out, K // 2), torch.uint8, device, stream)
+    if scales is None:
+        scales = _empty((*lead, out, K // 32), torch.uint8, device, stream)
+    _require(codes, "codes", torch.uint8, (*lead, out, K // 2))
+    _require(scales, "scales", torch.uint8, (*lead, out, K // 32))
+    _disjoint({"codes": codes, "scales": scales}, {"src": src, "signs": signs, "random": random})
+    return _Plan("mx4_quantize", (src.data_ptr(), SRC_DTYPES[src.dtype], batch, rows, cols, ld, int(bool(transpose)),
+                                  _data_ptr(signs), _data_ptr(random), codes.data_ptr(), scales.data_ptr()),
+                 (codes, scales), device, (src, signs, random))
+
+
+@_operator(_plan_quantize4)
+def mx4_quantize(src: torch.Tensor, transpose: bool = False, signs: torch.Tensor | None = None,
+                 random: torch.Tensor | None = None, codes: torch.Tensor | None = None,
+                 scales: torch.Tensor | None = None, stream=None):
+    """src [rows, cols] or [batch, rows, cols] (bf16 or fp32) as an operand of mx4_linear
+    -> (codes [.., rows, K/2], scales [.., rows, K/32]) uint8, quantized to E2M1 along the
+    columns, K their number rounded up to a multiple of 128 (zeros); with transpose,
+    along the rows: (codes [.., cols, K/2], scales [.., cols, K/32]).
+
+    signs [32] fp32 of +1 and -1 rotates every block of 32 by a Hadamard matrix (both
+    operands of a product alike); random, uint8 of src's shape, rounds stochastically and
+    saturates nothing; without it the nearest code is taken, as mx_quantize does."""
+    return _plan_quantize4(src, transpose, signs, random, codes, scales, stream).launch(stream)
+
+
+def _plan_dequantize4(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
+    if not isinstance(codes, torch.Tensor) or codes.dim() < 2 or codes.dtype != torch.uint8:
+        raise ValueError("codes: expected uint8 [.., rows, K/2]")
+    lead, K = codes.shape[:-1], codes.shape[-1] * 2
+    if K == 0 or K % 32:
+        raise ValueError(f"codes: K = {K} is not a positive multiple of 32")
+    if dtype not in SRC_DTYPES:
+        raise ValueError(f"dtype {dtype}, expected bfloat16 or float32")
+    _require(codes, "codes", torch.uint8, codes.shape)
+    _require(scales, "scales", torch.uint8, (*lead, K // 32))
+    _no_graph("mx4_dequantize", "of the user's own: codes have none", out=out)
+    device = _on_gpu(stream, codes, scales, out)
+    rows = codes.numel() // (K // 2)
+    if out is None:
+        out = _empty((*lead, K), dtype, device, stream)
+    if codes.dim() == 2:
+        ld = _require_rows(out, "out", dtype, (rows, K))
+    else:
+        _require(out, "out", dtype, (*lead, K))
+        ld = K
+    _disjoint({"out": out}, {"codes": codes, "scales": scales})
+    return _Plan("mx4_dequantize", (codes.data_ptr(), scales.data_ptr(), rows, K, out.data_ptr(), SRC_DTYPES[dtype],
+                                    ld), out, device, (codes, scales))
+
+
+@_operator(_plan_dequantize4)
+def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values [.., rows, K] of E2M1 codes [.., rows, K/2] and scales [.., rows, K/32] as
+    bf16 or fp32 (exact in both)."""
+    return _plan_dequantize4(codes, scales, dtype, out, stream).launch(stream)
+
+
+def _plan_linear4(a, w, w_scale, a_scale=None, bias=None, fn="none", mul=None, residual=None, expert_offsets=None,
+                  out=None, workspace=None, stream=None):
+    def problem(M, N, K, G, bias_dtype, w_stride, s_stride):
+        return Mx4LinearProblem(M, N, K, G, LINEAR_FNS[fn], bias_dtype, w_stride, s_stride)
+    return _call_linear("mx4_linear", problem, a, 4, w, w_scale, "e2m1", a_scale, bias, fn, mul, residual,
+                        expert_offsets, out, workspace, stream)
+
+
+@_operator(_plan_linear4)
+def mx4_linear(a: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, a_scale: torch.Tensor | None = None,
+               bias: torch.Tensor | None = None, fn: str = "none", mul: torch.Tensor | None = None,
+               residual: torch.Tensor | None = None, expert_offsets: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """mx_linear with MXFP4 on both sides: out [M, N] bf16 = fn(A W^T + bias) * mul + residual.
+
+    a: [M, K] bf16, quantized to E2M1 on the device, or E2M1 codes [M, K/2] uint8 with
+    a_scale [M, K/32] (mx4_quantize).  w [N, K/2] + w_scale [N, K/32] E2M1 weights, with
+    expert_offsets [G+1] one matrix per group; the other arguments are mx_linear's.
+    Gradients of such a product are products of operands quantized transposed: dX of dY
+    and W, dW of dY and X."""
+    return _plan_linear4(a, w, w_scale, a_scale, bias, fn, mul, residual, expert_offsets, out, workspace,
+                         stream).launch(stream)
 
 
 # ---------------------------------------------------------------- fused --

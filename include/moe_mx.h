@@ -194,6 +194,53 @@ moe_status_t moe_route_backward(const int32_t* topk_ids, const float* topk_w, co
                                 int32_t k, float* dlogits, hipStream_t stream);
 
 /*
+ * Balance of the router over a batch of T tokens in S sequences, for its training
+ * next to moe_route_backward.
+ *
+ * moe_balance -- load-balance loss, z-loss and tokens per expert.
+ *   logits   [T, E] fp32, rows logits_ld apart (>= E); topk_ids [T, k] as moe_route
+ *            writes them.
+ *   mask     [T] bytes, or NULL: a token with 0 (padding) does not count, nor does
+ *            one outside every sequence or one whose logits are all -inf; what
+ *            such a token holds is not used (NaN included).
+ *   seq_offsets [S + 1] int32, ascending: sequence s is the tokens [o[s], o[s+1]).
+ *            NULL: one sequence (S = 1) of all T tokens.  Offsets outside [0, T] are
+ *            cut to it; others that do not ascend give unspecified results (no
+ *            access out of bounds).
+ *   counts   [S, E] int32 out: (token, slot) assignments of the sequence's counted
+ *            tokens to each expert; ids outside [0, E) are left out.
+ *   tokens   [S + 2] int32 out: counted tokens n_s of each sequence, their sum n, and
+ *            the number S' of sequences that have one.
+ *   lse      [T] fp32 out: log sum_e exp(logits[t, e]), -inf where t does not count.
+ *   loss     [2] fp32 out, with p the softmax over all E logits of a token:
+ *              loss[0] = E / S' sum_s sum_e (counts[s, e] / (k n_s)) (sum_t p[t, e] / n_s)
+ *              loss[1] = 1 / n sum_t lse[t]^2
+ *            (1 where tokens and probabilities are spread evenly; 0 without a counted
+ *            token).  A counted token with NaN or +inf makes both NaN.
+ * moe_balance_backward -- dlogits of both losses, from dloss [2] fp32 on the device:
+ *     dlogits[t, e] = dloss[0] E / (S' n_s) p_e (f_e - sum_j f_j p_j)
+ *                     + dloss[1] 2 / n lse[t] p_e + add[t, e],  f_e = counts[s, e] / (k n_s),
+ *   the counts taken as constants; add[t, e] alone where t does not count.  add [T, E]
+ *   fp32 or NULL (0): another gradient of the logits, as moe_route_backward's; dlogits
+ *   may be add itself.  counts, tokens, lse, seq_offsets and k are moe_balance's.
+ *
+ * Requires 0 <= T, 1 <= k <= E <= 1024, 1 <= S, T*k and S*E <= 2^30, addresses that are
+ * multiples of the element size, and (moe_balance) moe_balance_workspace_bytes(T, E, S)
+ * bytes, 256-byte aligned, whose contents need not be set; calls that may run at the same
+ * time need one each.  T = 0 gives zeros.  Sums over a few dozen rows are held in fp32, sums
+ * of those in fp64, in an order that the sizes fix: results repeat bit for bit.
+ */
+size_t moe_balance_workspace_bytes(int32_t T, int32_t E, int32_t S);
+moe_status_t moe_balance(const float* logits, int64_t logits_ld, const int32_t* topk_ids, const uint8_t* mask,
+                         const int32_t* seq_offsets, int32_t T, int32_t E, int32_t k, int32_t S, float* loss,
+                         int32_t* counts, int32_t* tokens, float* lse, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+moe_status_t moe_balance_backward(const float* dloss, const float* logits, int64_t logits_ld, const int32_t* counts,
+                                  const int32_t* tokens, const float* lse, const int32_t* seq_offsets, int32_t T,
+                                  int32_t E, int32_t k, int32_t S, const float* add, int64_t add_ld, float* dlogits,
+                                  int64_t dlogits_ld, hipStream_t stream);
+
+/*
  * mx_gemm -- dense MX GEMM with bf16 output (mxfp6-sm120 page, table of
  * paths, "Dense" row; "Execution model" figure: bf16 activations quantized
  * on the device to E4M3 with one UE8M0 scale per 32 K values, packed MX
@@ -296,6 +343,64 @@ typedef struct {
 size_t mx_linear_workspace_bytes(const mx_linear_problem_t* p, int has_a_scale);
 moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_tensors_t* t, void* workspace,
                        size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * MXFP4 operands: E2M1 codes on both sides of a product, packed along the contraction
+ * with one E8M0 scale per 32 values (the canonical layouts above).
+ *
+ * mx4_quantize -- a matrix as an operand of a product.
+ *   src      [batch, rows, cols] of src_dtype, rows src_ld elements apart (>= cols),
+ *            matrices rows * src_ld apart; finite.
+ *   transpose 0: the contraction is the columns: codes [batch, rows, K/2], scales
+ *            [batch, rows, K/32] with K = cols rounded up to a multiple of 128.
+ *            1: the contraction is the rows: codes [batch, cols, K/2], scales [batch, cols,
+ *            K/32] with K = rows rounded up: src's transpose.  Values past the end count
+ *            as zeros, so that mx4_linear takes the operand as it is.
+ *   signs    [32] fp32, each +1 or -1, or NULL.  With them every block v of 32 values is
+ *            rotated first: v <- H (signs * v) / sqrt(32) with the 32-point Hadamard matrix
+ *            (butterflies at distance 1, 2, 4, 8, 16 in fp32, then the factor, rounded to
+ *            fp32).  Operands rotated with the same signs have the product of the unrotated
+ *            ones; a few large values no longer set the scale of their whole block.
+ *   random   [batch, rows, cols] bytes (rows cols apart), or NULL.
+ *            Without: as mx_quantize with MX_E2M1: scale 2^s, s = floor(log2 amax) - 2 (at
+ *            least -127), nearest code, ties to even, saturating.
+ *            With: s one more where 6 * 2^s < amax, so that nothing saturates, and |v| / 2^s
+ *            = x between the neighbouring values lo and hi becomes hi where
+ *            256 (x - lo) / (hi - lo) > random + 1/2, else lo: with bytes spread evenly, x on
+ *            average to within 1/512 of hi - lo.
+ * mx4_dequantize -- dst [rows, cols] (bf16 or fp32, rows dst_ld apart) = the values of codes
+ *   [rows, cols/2] with scales [rows, cols/32]; exact in both types but for 4 and 6 times
+ *   2^127, which are infinite; a scale code of 255 gives NaN.  cols % 32 == 0.
+ * mx4_linear -- mx_linear with MXFP4 on both sides:
+ *     v[m, n]   = sum_k A'[m, k] * W'[g, n, k] + bias[g, n]     (fp32 accumulation)
+ *     out[m, n] = bf16_RNE(fn(v[m, n]) * mul[m, n] + residual[m, n])
+ *   A' the values of E2M1 codes a [M, K/2] with a_scale [M, K/32] (mx4_quantize or
+ *   mx_quantize), or, a_scale NULL, bf16 a [M, K] quantized on the device as mx_quantize
+ *   does with MX_E2M1.  Everything else is as mx_linear says: w E2M1, groups and
+ *   expert_offsets, bias, fn, mul, residual, out, alignment, limits and workspace
+ *   (mx4_linear_workspace_bytes).  For a weight's gradients: dX = dY W is mx4_linear of dY
+ *   and W quantized transposed, dW = dY^T X that of dY and X both quantized transposed.
+ * Requires 16-byte aligned codes, scales and random on a multiple of 4 bytes and 1, src and
+ * dst on a multiple of their element size; rows, cols and batch up to 2^30.  Empty
+ * matrices are no-ops.
+ */
+typedef struct {
+  int64_t M, N, K;        /* rows, output columns (% 8 == 0), contraction (% 128 == 0) */
+  int32_t groups;         /* 0: one weight matrix; else matrices w holds (<= 1024)      */
+  mx_fn_t fn;
+  moe_src_t bias_dtype;   /* type of bias, where there is one                           */
+  int64_t w_stride;       /* bytes between the groups' matrices in w (% 16 == 0;        */
+  int64_t w_scale_stride; /* and in w_scale); 0: one right behind the other             */
+} mx4_linear_problem_t;
+
+moe_status_t mx4_quantize(const void* src, moe_src_t src_dtype, int64_t batch, int64_t rows, int64_t cols,
+                          int64_t src_ld, int transpose, const float* signs, const uint8_t* random, uint8_t* codes,
+                          uint8_t* scales, hipStream_t stream);
+moe_status_t mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* dst,
+                            moe_src_t dst_dtype, int64_t dst_ld, hipStream_t stream);
+size_t mx4_linear_workspace_bytes(const mx4_linear_problem_t* p, int has_a_scale);
+moe_status_t mx4_linear(const mx4_linear_problem_t* p, const mx_linear_tensors_t* t, void* workspace,
+                        size_t workspace_bytes, hipStream_t stream);
 
 /* Problem description of one fused MoE layer call. */
 typedef struct {
