@@ -85,6 +85,17 @@ struct FcArgs {
   Epilogue epi;
 };
 
+// The checks that mx_linear and mx4_linear share (everything but the workspace and the device;
+// M == 0 passes without its tensors), and the kernel arguments they begin with: epilogue,
+// weights, activations as given.
+struct LinearCall {
+  int64_t w_stride, s_stride;  // bytes between the groups' matrices and scales
+};
+moe_status_t check_linear(const mx_linear_problem_t& p, const mx_linear_tensors_t& t, LinearCall& call);
+FcArgs linear_args(const mx_linear_problem_t& p, const mx_linear_tensors_t& t, const LinearCall& call);
+// compute units of the current device, for persistent grids
+int device_cus();
+
 // Columns of N covered by one wave of the stream kernels.
 constexpr int kStreamColsFc1 = 32;
 constexpr int kStreamColsFc2 = 64;
@@ -141,6 +152,9 @@ hipError_t launch_splitk_reduce(const float* part, int ksplit, int64_t n4, float
 // quantized to MXFP8 on the way.
 constexpr int kFewCols = 16;
 hipError_t launch_linear_few(const FcArgs& p, bool mx_act, bool quant, int wfmt, hipStream_t st);
+// mx4_linear with a handful of rows, the same way: E2M1 codes, or (quant) bf16 rows quantized
+// to them on the way.
+hipError_t launch_mx4_few(const FcArgs& p, bool quant, hipStream_t st);
 // mx_linear with weights through LDS (gemm_rows.hip): `grid` persistent
 // workgroups, items of `rows` (16 or 64) rows and kRowsCols columns (nchunks column blocks),
 // any K % 128 == 0.  Dense calls may split K's stages in
@@ -162,5 +176,14 @@ constexpr int kMidRows = 64;
 constexpr int kMidRowsHigh = 128;
 constexpr int kMidK = 512;
 hipError_t launch_fc_mid(const FcArgs& p, bool fc1, int rows, int grid, hipStream_t st);
+
+// mx4_linear with many rows (gemm_fp4.hip): `grid` persistent workgroups (rounded
+// down to a multiple of 8, at least 8), items of `rows` (64, 128 or 256) rows and
+// kFp4Cols columns.  Requires K % 128 == 0, K >= kFp4K (16 bytes of scales per row) and N <=
+// kFp4MaxN (32-bit offsets into the 256 rows of a tile of out).
+constexpr int kFp4Cols = 256;
+constexpr int kFp4K = 512;
+constexpr int64_t kFp4MaxN = (int64_t)1 << 22;
+hipError_t launch_linear_fp4(const FcArgs& p, int rows, int grid, hipStream_t st);
 
 }  // namespace moe_mx

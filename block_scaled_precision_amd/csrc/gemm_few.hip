@@ -21,6 +21,9 @@
 // blocks g/2 and 2 + g/2, so a block's largest magnitude is one exchange away;
 // the MFMA takes from lane g the scale of block g.  (A launch to quantize costs
 // 2.5 us.)
+//
+// mx4_linear: E2M1 activations, as codes or quantized on the way as mx4_quantize does.
+// Lane g of a row then holds block g of a chunk as a whole, as it does of the weights.
 #include <hip/hip_runtime.h>
 
 #include "epilogue.h"
@@ -38,12 +41,13 @@ typedef uint32_t u32x4_a8 __attribute__((ext_vector_type(4), aligned(8)));
 constexpr int kAhead = 4;  // chunks in flight per wave
 constexpr int W = 8;       // waves
 
-// activations: bf16 as given, E4M3 codes with scales, bf16 quantized here
-enum Act { kBf16 = 0, kMx = 1, kQuant = 2 };
+// activations: bf16 as given, E4M3 codes with scales, bf16 quantized here; E2M1 codes with
+// scales, bf16 quantized to E2M1 here
+enum Act { kBf16 = 0, kMx = 1, kQuant = 2, kMx4 = 3, kQuant4 = 4 };
 
 struct Chunk {
-  uint4 a[4];         // kBf16: 32 values; kQuant: 2 x 16 values; kMx: a[0], a[1] codes
-  uint32_t as;        // kMx: the chunk's four scale bytes
+  uint4 a[4];         // kBf16, kQuant4: 32 values; kQuant: 2 x 16 values; kMx: a[0], a[1] codes; kMx4: a[0]
+  uint32_t as;        // kMx, kMx4: the chunk's four scale bytes
   uint32_t b[6];      // weights; E2M1: 4 dwords, E3M2: 6
   uint32_t bs;        // the chunk's four scale bytes
 };
@@ -63,7 +67,10 @@ __device__ __forceinline__ void load_chunk(Chunk& f, const uint8_t* arow, const 
   }
   f.bs = *(const uint32_t*)(bsrow + 4 * c);
   if (arow == nullptr) return;  // a row past the tile: zeros, set once
-  if (ACT == kBf16) {
+  if (ACT == kMx4) {
+    f.a[0] = *(const uint4*)(arow + 64 * (int64_t)c + 16 * g);
+    f.as = *(const uint32_t*)(asrow + 4 * c);
+  } else if (ACT == kBf16 || ACT == kQuant4) {
     const uint4* q = (const uint4*)(arow + 2 * (128 * (int64_t)c + 32 * g));
 #pragma unroll
     for (int i = 0; i < 4; ++i) f.a[i] = q[i];
@@ -88,6 +95,14 @@ __device__ __forceinline__ uint4 quant16(const uint4& lo, const uint4& hi, float
            (e4m3_pair(__uint_as_float(w[2 * q + 1] << 16) * inv, __uint_as_float(w[2 * q + 1] & 0xffff0000u) * inv)
             << 16);
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// 8 bf16 values to 8 E2M1 codes, divided by 2^s
+__device__ __forceinline__ uint32_t quant8_e2m1(const uint4& v, float inv) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) * inv;
+  return e2m1_codes(q);
 }
 // largest magnitude (fp32 bits) of 16 bf16 values
 __device__ __forceinline__ uint32_t amax16(const uint4& lo, const uint4& hi) {
@@ -124,6 +139,21 @@ __device__ __forceinline__ void mul_chunk(v4f& acc, const Chunk& f, int g, int r
       __builtin_memcpy(&av, &f.a[s], 16);
       acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv, av, acc, 0, 0, 0);
     }
+    return;
+  }
+  if (ACT == kMx4 || ACT == kQuant4) {
+    uint4 q = f.a[0];
+    int asc = (int)((f.as >> (8 * g)) & 0xffu);
+    if (ACT == kQuant4) {
+      const int s = block_exponent<1>(max(amax16(f.a[0], f.a[1]), amax16(f.a[2], f.a[3])));
+      const float inv = exp2_neg(s);
+      q = make_uint4(quant8_e2m1(f.a[0], inv), quant8_e2m1(f.a[1], inv), quant8_e2m1(f.a[2], inv),
+                     quant8_e2m1(f.a[3], inv));
+      asc = s + 127;
+    }
+    const v8i av = {(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
+    const v8i bv = {(int)f.b[0], (int)f.b[1], (int)f.b[2], (int)f.b[3], 0, 0, 0, 0};
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv, av, acc, 4, 4, 0, wsc, 0, asc);
     return;
   }
   uint4 lo = f.a[0], hi = f.a[1];
@@ -226,8 +256,8 @@ __global__ __launch_bounds__(64 * W) void k_linear_few(FcArgs p) {
   const uint8_t* asrow = nullptr;
   if (r < t.rows) {
     const int64_t row = t.p0 + r;
-    arow = (const uint8_t*)p.a + row * (ACT == kMx ? K : 2 * (int64_t)K);
-    if (ACT == kMx) asrow = p.a_scale + row * (K / 32);
+    arow = (const uint8_t*)p.a + row * (ACT == kMx ? K : ACT == kMx4 ? K / 2 : 2 * (int64_t)K);
+    if (ACT == kMx || ACT == kMx4) asrow = p.a_scale + row * (K / 32);
   }
   // columns past N read the last weight row and are not stored
   const int64_t wrow = min(col0 + r, N - 1);
@@ -278,6 +308,14 @@ void launch_few_t(const FcArgs& p, int ntiles, hipStream_t st) {
 }
 
 }  // namespace
+
+hipError_t launch_mx4_few(const FcArgs& p, bool quant, hipStream_t st) {
+  const int ntiles = p.dense_rows > 0 ? (p.dense_rows + 15) / 16 : p.max_tiles;
+  if (ntiles == 0) return hipSuccess;
+  if (quant) launch_few_t<kQuant4, 1>(p, ntiles, st);
+  else launch_few_t<kMx4, 1>(p, ntiles, st);
+  return hipGetLastError();
+}
 
 hipError_t launch_linear_few(const FcArgs& p, bool mx_act, bool quant, int wfmt, hipStream_t st) {
   const int ntiles = p.dense_rows > 0 ? (p.dense_rows + 15) / 16 : p.max_tiles;

@@ -1,0 +1,505 @@
+// mx4_linear with many rows: tiles of 64 MSUB rows by 256 columns on the block-scaled
+// MFMA v_mfma_scale_f32_32x32x64_f8f6f4 with E2M1 on both sides (mxfp6-sm120 page,
+// "Execution model"; TokenSpeed SiTU page, "Supported contract": MxE2m1).
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+#include <utility>
+
+#include "copy_ring.h"
+#include "epilogue.h"
+#include "gemm.h"
+#include "mx_device.h"
+
+namespace moe_mx {
+
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads4 = 256;
+constexpr int TN = kFp4Cols;
+constexpr int ROW = 128;  // bytes of a row per stage: 256 K
+
+template <int MSUB> struct Lay4 {
+  static constexpr int TM = 64 * MSUB;
+  static constexpr int NBUF = MSUB == 1 ? 3 : 2;
+  static constexpr int SA = TM * ROW, SB = TN * ROW, STAGE = SA + SB;
+  static constexpr int GA = TM * 16, GROUP = GA + TN * 16;  // scales of two stages
+  static constexpr int GBUFS = NBUF == 2 ? 2 : 4;
+  static constexpr int SCALES = NBUF * STAGE;
+  static constexpr int TOTAL = SCALES + GBUFS * GROUP;
+  static constexpr int ACOP = TM / 32, BCOP = TN / 32;  // 1-KB copies per wave and stage
+  static_assert(TOTAL <= 160 * 1024, "LDS");
+};
+
+struct Item4 {
+  int expert, p0, rows, nb;
+};
+// The items of an XCD, q, q + Q, ... for its workgroup q: patches of kPatchM row tiles
+// by kPatchN column blocks one after the other, so that workgroups that run at the
+// same time share what they read in the XCD's L2.  Row tiles go to the XCDs in blocks
+// of kPatchM; those behind the last 8 whole blocks are shared out item by item.
+constexpr int kPatchM = 4, kPatchN = 8;
+struct Sched4 {
+  int xcd, full, tail0, q, Q, NB, ntiles, nk, items;
+  bool odd;  // K % 256 == 128: the last stage is half of one
+};
+
+template <int TM>
+__device__ __forceinline__ Item4 item_at(const FcArgs& p, const Sched4& sc, int li) {
+  const int j = sc.q + li * sc.Q, block = kPatchM * sc.NB;
+  int u, t0;  // item within a run of blocks that begins with tile t0
+  if (j < sc.full * block) {
+    u = j % block;
+    t0 = kPatchM * (8 * (j / block) + sc.xcd);
+  } else {
+    u = sc.tail0 + j - sc.full * block;
+    t0 = 8 * kPatchM * sc.full + kPatchM * (u / block);
+    u %= block;
+  }
+  const int rows = min(kPatchM, sc.ntiles - t0), nb0 = u / (rows * kPatchN) * kPatchN;
+  u -= rows * nb0;
+  const int width = min(kPatchN, sc.NB - nb0), ti = __builtin_amdgcn_readfirstlane(t0 + u / width);
+  Item4 it;
+  it.nb = __builtin_amdgcn_readfirstlane(nb0 + u % width);
+  if (p.dense_rows > 0) {
+    it.expert = 0;
+    it.p0 = TM * ti;
+    it.rows = min(TM, p.dense_rows - TM * ti);
+  } else {
+    const Tile t = load_tile(p.tiles, ti);
+    it.expert = t.expert;
+    it.p0 = t.p0;
+    it.rows = t.rows;
+  }
+  return it;
+}
+
+// A matrix for buffer loads: byte offsets from `base` below 2^31 are read, others give zeros.
+constexpr uint32_t kOutside = 0x80000000u;
+__device__ __forceinline__ v4i buffer_of(const void* base) {
+  const uint64_t a = (uint64_t)base;
+  return (v4i){__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+               __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xffff), (int)kOutside, 0x00020000};
+}
+// Lane i's 16 bytes at off + soff of the buffer to LDS at lds + 16 i
+__device__ __forceinline__ void lds_copy16_b(v4i buffer, uint32_t off, uint32_t soff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
+                   __builtin_amdgcn_readfirstlane(lds)),
+               "v"(off), "s"(buffer), "s"(__builtin_amdgcn_readfirstlane(soff))
+               : "memory");
+}
+
+// The copies of one wave: stages in order, each in COPIES parts that the caller
+// spreads between its MFMAs.
+template <int MSUB> struct Copier {
+  using L = Lay4<MSUB>;
+  static constexpr int COPIES = L::ACOP + L::BCOP;
+  const FcArgs& p;
+  const Sched4& sc;
+  uint32_t lds0;
+  int w, lane;
+  // cursor: items begun, stage of the last, LDS offsets of its stage and scale group
+  int li = 0, ls, slot = 0, group = 0;
+  // the item and stage that parts belong to
+  v4i abuf, wbuf;
+  const uint8_t *asb, *wsb;
+  uint32_t aoff[L::ACOP], boff[L::BCOP], asoff, wsoff, outside[2], soff, dst;
+
+  // The block that copy i of this lane brings to its place of a row: block c of row r lies at
+  // place c ^ (r >> 1 & 7), so that 16 rows read at the same block meet all of the banks.
+  // (Rows 8 i + lane / 8; a wave's copies begin at an even i.)
+  __device__ __forceinline__ int chunk(int i) const { return (lane & 7) ^ (lane >> 4 | (i & 1) << 2); }
+  __device__ __forceinline__ void set_item() {
+    const Item4 it = item_at<L::TM>(p, sc, li);
+    const int K = p.K, kb = K / 2, ks = K / 32, n0 = it.nb * TN, last = p.N - 1 - n0;
+    const int r8 = lane >> 3;
+    abuf = buffer_of((const uint8_t*)p.a + (int64_t)it.p0 * kb);
+    wbuf = buffer_of(p.w + (int64_t)it.expert * p.w_estride + (int64_t)n0 * kb);
+    asb = p.a_scale + (int64_t)it.p0 * ks;
+    wsb = p.w_scale + (int64_t)it.expert * p.ws_estride + (int64_t)n0 * ks;
+#pragma unroll
+    for (int i = 0; i < L::ACOP; ++i)
+      aoff[i] = (uint32_t)min(8 * (L::ACOP * w + i) + r8, it.rows - 1) * (uint32_t)kb + 16 * chunk(i);
+#pragma unroll
+    for (int i = 0; i < L::BCOP; ++i)
+      boff[i] = (uint32_t)min(epi_row32(8 * (L::BCOP * w + i) + r8), last) * (uint32_t)kb + 16 * chunk(i);
+    asoff = (uint32_t)min(64 * min(w, MSUB - 1) + lane, it.rows - 1) * (uint32_t)ks;
+    wsoff = (uint32_t)min(epi_row32(64 * w + lane), last) * (uint32_t)ks;
+  }
+  // Goes to the next stage.  Past the last stage of the last item that stage goes out
+  // again, into a slot that nothing reads any more: without a branch around them the
+  // copies can stand between the MFMAs.
+  // (In four pieces, to stand between MFMAs: each is computed where it is called, not where
+  // it is used.)
+  __device__ __forceinline__ void advance(int piece) {
+    if (piece == 0) {
+      dst = lds0 + slot;
+      asm volatile("" : "+s"(dst));
+    } else if (piece == 1) {
+      slot = slot == (L::NBUF - 1) * L::STAGE ? 0 : slot + L::STAGE;
+      asm volatile("" : "+s"(slot));
+    } else if (piece == 2) {
+      ls = min(ls + 1, sc.nk - 1);
+      soff = ROW * ls;
+      asm volatile("" : "+s"(ls), "+s"(soff));
+    } else {
+      // the half stage at the end of K: zeros for the second half
+      const bool half = sc.odd && ls == sc.nk - 1;
+      outside[0] = half && chunk(0) >= 4 ? kOutside : 0;
+      outside[1] = half && chunk(1) >= 4 ? kOutside : 0;
+      asm volatile("" : "+v"(outside[0]), "+v"(outside[1]));
+    }
+  }
+  __device__ __forceinline__ bool ends_item() const { return ls == sc.nk - 1 && li < sc.items; }
+  __device__ __forceinline__ void next_item() {
+    set_item();
+    ++li;
+    ls = -1;
+  }
+  __device__ __forceinline__ bool scales() const { return (ls & 1) == 0; }
+  // the stage's scale group, where it is the first of two
+  __device__ __forceinline__ void begin() {
+    if (scales()) {
+      const int s0 = min(8 * ls, p.K / 32 - 16);
+      const uint32_t g = lds0 + L::SCALES + group;
+      lds_copy16_s(asb + s0, asoff, g + 1024 * min(w, MSUB - 1));
+      lds_copy16_s(wsb + s0, wsoff, g + L::GA + 1024 * w);
+      group = group == (L::GBUFS - 1) * L::GROUP ? 0 : group + L::GROUP;
+    }
+  }
+  __device__ __forceinline__ void part(int i) {
+    if (i < L::ACOP) lds_copy16_b(abuf, aoff[i] | outside[i & 1], soff, dst + 1024 * (L::ACOP * w + i));
+    else lds_copy16_b(wbuf, boff[i - L::ACOP] | outside[i & 1], soff, dst + L::SA + 1024 * (L::BCOP * w + i - L::ACOP));
+  }
+};
+
+// f(0), f(1), ... with compile-time arguments
+template <int N> using Int = std::integral_constant<int, N>;
+template <class F, int... I>
+__device__ __forceinline__ void each(std::integer_sequence<int, I...>, F f) {
+  (f(Int<I>()), ...);
+}
+
+// Epilogue of a wave, 32 rows by 64 columns at a time: part (h, m) holds row 32 (wm + 2m) + l32
+// of the tile and in each lane four pieces of eight columns, at col + 64 h + 16 q.  IN: there
+// is a second factor or a residual.
+//
+// A wave has its SIMD to itself, so this costs what its instructions cost, some 4.5 cycles
+// each: 10000 of them (32 pieces one behind the other, each with its bounds, bias and
+// function) took 47000 cycles an item, half of a K loop of 8192.  So the parts of a half run in
+// a loop, with branches around what is absent; the accumulators are picked by a branch
+// too, read by assembly, which the compiler cannot turn into selections over all of them.
+// Stores count on the same in-order counter as loads and copies, and take microseconds
+// while every workgroup writes.  Nothing here waits for one: loads go out a part ahead, and
+// no branch stands around a store or a load, so that the compiler can count those behind the
+// one it waits for (pieces outside the tile or N: an offset outside the buffer).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ float acc_read(float a) {
+  float v;
+  asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
+  return v;
+}
+template <int MSUB, bool IN>
+__device__ __forceinline__ void finish(v16f (&acc)[MSUB][4], const Item4& it, int N, int wm, int l32, int col) {
+  // the last MFMAs' results, for the assembly below
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  const Epilogue e = epi_load();
+  const int64_t tile = (int64_t)it.p0 * N;
+  auto buffer = [&](const void* q) {
+    return __builtin_amdgcn_make_buffer_rsrc(q ? (uint16_t*)q + tile : nullptr, 0, q ? (int)kOutside : 0, 0x00020000);
+  };
+  const auto out = buffer(e.out), mul = buffer(e.mul), res = buffer(e.residual);
+  const bool has_mul = e.mul != nullptr, has_bias = e.bias_kind != kBiasNone;
+  EpiBias bias[2][4];
+  if (has_bias) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      bias[j >> 2][j & 3] = epi_bias(e, N, it.expert, min(col + 64 * (j >> 2) + 16 * (j & 3), N - 8));
+  }
+  const int rows = it.rows - 32 * wm - l32, cols = N - col;  // of this lane's first row and column on
+  const int first = (int)(2 * ((uint32_t)(32 * wm + l32) * (uint32_t)N + col));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int side[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) side[q] = 64 * h + 16 * q < cols ? 0 : (int)kOutside;
+    auto at = [&](int m, int q) {
+      return ((64 * m < rows ? first + 128 * h + m * (128 * N) : (int)kOutside) | side[q]) + 32 * q;
+    };
+    u32x4 nm[4], nr[4];
+    auto request = [&](int m) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        nm[q] = __builtin_amdgcn_raw_buffer_load_b128(mul, at(m, q), 0, 0);
+        nr[q] = __builtin_amdgcn_raw_buffer_load_b128(res, at(m, q), 0, 0);
+      }
+    };
+    if constexpr (IN) request(0);
+#pragma unroll 1
+    for (int m = 0; m < MSUB; ++m) {
+      float v[4][8];
+      each(std::make_integer_sequence<int, MSUB>(), [&](auto M) {
+        if (m == M.value) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              v[q][i] = acc_read(acc[M.value][2 * h + (i >> 2)][4 * q + (i & 3)]);
+        }
+      });
+      if (has_bias) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[q][i] += epi_bias_at(e, bias[h][q], i);
+      }
+      if (e.fn != MX_FN_NONE) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) epi_fn(e.fn, v[q]);
+      }
+      if constexpr (IN) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float f = __uint_as_float(i & 1 ? nm[q][i / 2] & 0xffff0000u : nm[q][i / 2] << 16);
+            v[q][i] *= has_mul ? f : 1.0f;
+            v[q][i] += __uint_as_float(i & 1 ? nr[q][i / 2] & 0xffff0000u : nr[q][i / 2] << 16);
+          }
+        request(min(m + 1, MSUB - 1));
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const v2bf o2 = {(__bf16)v[q][2 * i], (__bf16)v[q][2 * i + 1]};
+          uint32_t w;
+          __builtin_memcpy(&w, &o2, 4);
+          o[i] = w;
+        }
+        __builtin_amdgcn_raw_buffer_store_b128(o, out, at(m, q), 0, 0);
+      }
+    }
+  }
+}
+
+template <int MSUB, bool IN>
+__global__ __launch_bounds__(kThreads4, 1) void k_linear_fp4(FcArgs p) {
+  using L = Lay4<MSUB>;
+  using C = Copier<MSUB>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[L::TOTAL];
+  Sched4 sc;
+  sc.nk = (p.K + 255) / 256;
+  sc.odd = p.K % 256 != 0;
+  sc.NB = p.nchunks;
+  sc.ntiles = p.dense_rows > 0 ? (p.dense_rows + L::TM - 1) / L::TM : *p.num_tiles;
+  sc.xcd = blockIdx.x & 7;
+  sc.q = blockIdx.x >> 3;
+  sc.Q = gridDim.x >> 3;
+  sc.full = sc.ntiles / (8 * kPatchM);
+  const int tail = sc.ntiles % (8 * kPatchM) * sc.NB;
+  sc.tail0 = tail * sc.xcd / 8;
+  const int nitems = sc.full * kPatchM * sc.NB + tail * (sc.xcd + 1) / 8 - sc.tail0;
+  sc.items = nitems > sc.q ? (nitems - sc.q + sc.Q - 1) / sc.Q : 0;
+  if (sc.items == 0) return;
+
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = w >> 1, wn = w & 1, l32 = lane & 31, g = lane >> 5;
+  C copy{p, sc, lds_addr(smem), w, lane};
+
+  // offsets of this lane's fragment of step s: row l32, block 4g + s at its place (Copier::chunk)
+  int off[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) off[s] = l32 * ROW + 16 * ((4 * g + s) ^ (l32 >> 1 & 7));
+
+  // fragments of two steps and scales of two stages: those in use and the next
+  v4i fa[2][MSUB], fb[2][4];
+  uint32_t sa[MSUB], sb[4], ta[MSUB], tb[4];
+  v16f acc[MSUB][4];
+  constexpr int READS = 4 + MSUB, SLOTS = 4 * MSUB;
+  // fragment i of a step (offset o) of the stage at st
+  auto read = [&](int f, const uint8_t* st, int o, int i) {
+    if (i < 4) fb[f][i] = *(const v4i*)(st + L::SA + (4 * wn + i) * (32 * ROW) + o);
+    else fa[f][i - 4] = *(const v4i*)(st + (wm + 2 * (i - 4)) * (32 * ROW) + o);
+  };
+  // scales of fragment i of the stage whose scales lie at gs
+  auto read_scale = [&](const uint8_t* gs, int i) {
+    if (i < 4) tb[i] = *(const uint32_t*)(gs + L::GA + 512 * (4 * wn + i));
+    else ta[i - 4] = *(const uint32_t*)(gs + 512 * (wm + 2 * (i - 4)));
+  };
+  int cgroup = (L::GBUFS - 1) * L::GROUP;  // LDS offset of the scale group of the stage last read
+  auto scales_at = [&](int ks) {
+    if ((ks & 1) == 0) cgroup = cgroup == (L::GBUFS - 1) * L::GROUP ? 0 : cgroup + L::GROUP;
+    const bool h = sc.odd && ks == sc.nk - 1;
+    const int so = 8 * ks - min(8 * (ks & ~1), p.K / 32 - 16);
+    return (uint32_t)(L::SCALES + cgroup + so + (16 * l32 + (h ? 0 : 4 * g)));
+  };
+  auto take_scales = [&]() {
+#pragma unroll
+    for (int m = 0; m < MSUB; ++m) sa[m] = ta[m];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) sb[n] = tb[n];
+  };
+  // The branches of copy.begin() end a basic block; without this the compiler moves the
+  // MFMAs before it, whose results are only used after it, behind it and each other.
+  auto pin = [&]() {
+#pragma unroll
+    for (int m = 0; m < MSUB; ++m)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) asm volatile("" : "+a"(acc[m][n]));
+  };
+  // MFMA k of step S on fragment set F
+  auto mfma = [&](auto F, auto S, auto K) {
+    constexpr int f = F.value, m = K.value / 4, n = K.value % 4, s = S.value;
+    const v8i av = {fa[f][m][0], fa[f][m][1], fa[f][m][2], fa[f][m][3], 0, 0, 0, 0};
+    const v8i bv = {fb[f][n][0], fb[f][n][1], fb[f][n][2], fb[f][n][3], 0, 0, 0, 0};
+    acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bv, av, acc[m][n], 4, 4, s, (int)sb[n], s, (int)sa[m]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // those of N operations f that come after MFMA K when they are spread over MFMAs [K0, K1)
+  auto among = [&](auto K, auto N, auto K0, auto K1, auto f) {
+    constexpr int n = N.value, k0 = K0.value, span = K1.value - K0.value;
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      if (k0 + i * span / n == K.value) f(i);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr std::make_integer_sequence<int, SLOTS> slots;
+  constexpr Int<0> i0;
+  constexpr Int<1> i1;
+  constexpr Int<2> i2;
+  constexpr Int<3> i3;
+  constexpr Int<4> i4;
+  constexpr Int<READS> reads;
+  constexpr Int<C::COPIES / 2> half;
+  constexpr Int<C::COPIES - C::COPIES / 2> rest;
+  constexpr Int<SLOTS / 2> mid;
+  constexpr Int<SLOTS * 3 / 4> late;
+  constexpr Int<SLOTS> end;
+
+  copy.next_item();
+  for (int s = 0; s < L::NBUF; ++s) {
+    if (copy.ends_item()) copy.next_item();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) copy.advance(i);
+    copy.begin();
+#pragma unroll
+    for (int i = 0; i < C::COPIES; ++i) copy.part(i);
+  }
+  wait_vm_lgkm0<0>();
+  barrier();
+  {
+    const uint8_t* gs = smem + scales_at(0);
+#pragma unroll
+    for (int i = 0; i < READS; ++i) {
+      read_scale(gs, i);
+      read(0, smem, off[0], i);
+    }
+  }
+  take_scales();
+  const uint8_t* st = smem;
+  int slot = 0;
+  for (int ci = 0; ci < sc.items; ++ci) {
+    const Item4 it = item_at<L::TM>(p, sc, ci);
+#pragma unroll
+    for (int m = 0; m < MSUB; ++m)
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.f;
+    for (int ks = 0; ks < sc.nk; ++ks) {
+      each(slots, [&](auto k) {
+        mfma(i0, i0, k);
+        among(k, reads, i0, mid, [&](int i) { read(1, st, off[1], i); });
+        among(k, rest, i0, end, [&](int i) { copy.part(half + i); });
+      });
+      each(slots, [&](auto k) {
+        mfma(i1, i1, k);
+        among(k, reads, i0, mid, [&](int i) { read(0, st, off[2], i); });
+      });
+      pin();
+      const bool behind = copy.scales();  // (of the stage begun last)
+      if (copy.ends_item()) copy.next_item();
+      const int kn = ks + 1 == sc.nk ? 0 : ks + 1;
+      uint32_t so = 0;
+      __builtin_amdgcn_sched_barrier(0);
+      each(slots, [&](auto k) {
+        mfma(i0, i2, k);
+        among(k, reads, i0, mid, [&](int i) { read(1, st, off[3], i); });
+        // the next stage's places
+        among(k, i4, i0, end, [&](int i) { copy.advance(i); });
+        if constexpr (k.value == SLOTS / 2) {
+          slot = slot == (L::NBUF - 1) * L::STAGE ? 0 : slot + L::STAGE;
+          asm volatile("" : "+s"(slot));
+          __builtin_amdgcn_sched_barrier(0);
+        } else if constexpr (k.value == SLOTS - 1) {
+          so = scales_at(kn);
+          asm volatile("" : "+v"(so));
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      });
+      const uint8_t* gs = smem + so;
+      pin();
+      // every read of the stage has landed in this wave; the next stage has landed as a
+      // whole once every wave passes the barrier, and this one's slot is free
+      // (behind the copies of the item's first stages the epilogue before it has left 8
+      // MSUB stores, and the first stage has sent the second half of the last once more)
+      constexpr int kBehind = 8 * MSUB + rest;
+      const bool stored = ks == 0 && ci > 0;
+      if (L::NBUF == 2) {
+        if (stored) wait_vm_lgkm0<kBehind>();
+        else wait_vm_lgkm0<0>();
+      } else if (behind) {  // and the stage after the next, begun last, is on its way
+        if (stored) wait_vm_lgkm0<kBehind + C::COPIES + 2>();
+        else wait_vm_lgkm0<C::COPIES + 2>();
+      } else {
+        if (stored) wait_vm_lgkm0<kBehind + C::COPIES>();
+        else wait_vm_lgkm0<C::COPIES>();
+      }
+      barrier();
+      st = smem + slot;
+      copy.begin();
+      __builtin_amdgcn_sched_barrier(0);
+      each(slots, [&](auto k) {
+        mfma(i1, i3, k);
+        among(k, reads, i0, mid, [&](int i) { read(0, st, off[0], i); });
+        among(k, reads, i1, late, [&](int i) { read_scale(gs, i); });
+        among(k, half, i0, end, [&](int i) { copy.part(i); });
+      });
+      take_scales();
+      pin();
+    }
+    // The rest of the begun stage goes out before the stores, which the wait for it then need
+    // not cover (the next item's first step sends it again: the same bytes, into a slot that is
+    // not begun again before a wait for all of them).
+#pragma unroll
+    for (int i = half; i < C::COPIES; ++i) copy.part(i);
+    // the lane holds row 32 (wm + 2m) + l32 of the tile, eight columns of each piece
+    finish<MSUB, IN>(acc, it, p.N, wm, l32, it.nb * TN + 128 * wn + 8 * g);
+  }
+  wait_vm_lgkm0<0>();  // no copy may land in LDS that is no longer this workgroup's
+}
+
+}  // namespace
+
+template <int MSUB>
+static void launch_fp4_t(const FcArgs& p, int grid, hipStream_t st) {
+  if (p.epi.mul || p.epi.residual) k_linear_fp4<MSUB, true><<<grid, kThreads4, 0, st>>>(p);
+  else k_linear_fp4<MSUB, false><<<grid, kThreads4, 0, st>>>(p);
+}
+
+hipError_t launch_linear_fp4(const FcArgs& p, int rows, int grid, hipStream_t st) {
+  if (grid < 8) grid = 8;
+  grid &= ~7;
+  if (rows == 256) launch_fp4_t<4>(p, grid, st);
+  else if (rows == 128) launch_fp4_t<2>(p, grid, st);
+  else if (rows == 64) launch_fp4_t<1>(p, grid, st);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+}  // namespace moe_mx

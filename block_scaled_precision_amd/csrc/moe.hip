@@ -41,7 +41,7 @@ moe_status_t check_arch() {
 }
 
 // Compute units of the current device (cached per device), for persistent grids.
-static int device_cus() {
+int device_cus() {
   static std::atomic<int> cache[256];
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 256;
@@ -572,28 +572,66 @@ extern "C" size_t mx_linear_workspace_bytes(const mx_linear_problem_t* p, int ha
   return linear_plan(*p, has_a_scale != 0).total;
 }
 
+namespace moe_mx {
+
+moe_status_t check_linear(const mx_linear_problem_t& p, const mx_linear_tensors_t& t, LinearCall& call) {
+  if (!linear_sizes_ok(p)) return MOE_ERR_INVALID_ARG;
+  if (p.act != MOE_ACT_BF16 && p.act != MOE_ACT_MXFP8) return MOE_ERR_INVALID_ARG;
+  if (p.w_fmt != MX_E2M1 && p.w_fmt != MX_E3M2 && p.w_fmt != MX_E4M3) return MOE_ERR_INVALID_ARG;
+  if (p.fn != MX_FN_NONE && p.fn != MX_FN_SILU && p.fn != MX_FN_GELU && p.fn != MX_FN_RELU2)
+    return MOE_ERR_INVALID_ARG;
+  if (p.bias_dtype != MOE_SRC_BF16 && p.bias_dtype != MOE_SRC_FP32) return MOE_ERR_INVALID_ARG;
+  if (p.act != MOE_ACT_MXFP8 && t.a_scale) return MOE_ERR_INVALID_ARG;
+  const int64_t wbytes = p.N * (p.K / 32) * wbits(p.w_fmt) * 4, sbytes = p.N * (p.K / 32);
+  call.w_stride = p.w_stride ? p.w_stride : wbytes;
+  call.s_stride = p.w_scale_stride ? p.w_scale_stride : sbytes;
+  if (!linear_supported(p)) return MOE_ERR_UNSUPPORTED;
+  if (p.groups > 1 && (call.w_stride < wbytes || call.s_stride < sbytes || call.w_stride % 16 || call.s_stride % 16))
+    return MOE_ERR_INVALID_ARG;
+  if (p.M == 0) return MOE_OK;
+  if (!t.a || !t.w || !t.w_scale || !t.out || (p.groups > 0) != (t.expert_offsets != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  for (const void* q : {t.a, (const void*)t.a_scale, (const void*)t.w, (const void*)t.w_scale, t.mul, t.residual,
+                        (const void*)t.out})
+    if (!aligned16(q)) return MOE_ERR_INVALID_ARG;
+  if (t.bias && (uintptr_t)t.bias % (p.bias_dtype == MOE_SRC_BF16 ? 2 : 4)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+FcArgs linear_args(const mx_linear_problem_t& p, const mx_linear_tensors_t& t, const LinearCall& call) {
+  FcArgs g = {};
+  g.linear = true;
+  g.epi.bias = t.bias;
+  // (a bias row is N elements, N % 8 == 0: every row is as aligned as the first)
+  g.epi.bias_kind = !t.bias ? kBiasNone
+                    : p.bias_dtype == MOE_SRC_FP32 ? (aligned16(t.bias) ? kBiasF32 : kBiasF32Any)
+                                                   : (aligned16(t.bias) ? kBiasBf16 : kBiasBf16Any);
+  g.epi.fn = p.fn;
+  g.epi.mul = (const uint16_t*)t.mul;
+  g.epi.residual = (const uint16_t*)t.residual;
+  g.epi.out = (__bf16*)t.out;
+  g.k = 1;
+  g.a = t.a;
+  g.a_scale = t.a_scale;
+  g.w = t.w;
+  g.w_scale = t.w_scale;
+  g.w_estride = call.w_stride;
+  g.ws_estride = call.s_stride;
+  g.K = (int)p.K;
+  g.N = (int)p.N;
+  return g;
+}
+
+}  // namespace moe_mx
+
 extern "C" moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_tensors_t* t, void* workspace,
                                   size_t workspace_bytes, hipStream_t stream) {
-  if (!p || !t || !linear_sizes_ok(*p)) return MOE_ERR_INVALID_ARG;
-  if (p->act != MOE_ACT_BF16 && p->act != MOE_ACT_MXFP8) return MOE_ERR_INVALID_ARG;
-  if (p->w_fmt != MX_E2M1 && p->w_fmt != MX_E3M2 && p->w_fmt != MX_E4M3) return MOE_ERR_INVALID_ARG;
-  if (p->fn != MX_FN_NONE && p->fn != MX_FN_SILU && p->fn != MX_FN_GELU && p->fn != MX_FN_RELU2)
-    return MOE_ERR_INVALID_ARG;
-  if (p->bias_dtype != MOE_SRC_BF16 && p->bias_dtype != MOE_SRC_FP32) return MOE_ERR_INVALID_ARG;
+  if (!p || !t) return MOE_ERR_INVALID_ARG;
+  LinearCall call;
+  const moe_status_t v = check_linear(*p, *t, call);
+  if (v != MOE_OK || p->M == 0) return v;
   const bool mx = p->act == MOE_ACT_MXFP8;
-  if (!mx && t->a_scale) return MOE_ERR_INVALID_ARG;
   const int64_t M = p->M, N = p->N, K = p->K;
-  const int64_t wbytes = N * (K / 32) * wbits(p->w_fmt) * 4, sbytes = N * (K / 32);
-  const int64_t wstride = p->w_stride ? p->w_stride : wbytes, sstride = p->w_scale_stride ? p->w_scale_stride : sbytes;
-  if (!linear_supported(*p)) return MOE_ERR_UNSUPPORTED;
-  if (p->groups > 1 && (wstride < wbytes || sstride < sbytes || wstride % 16 || sstride % 16)) return MOE_ERR_INVALID_ARG;
-  if (M == 0) return MOE_OK;
-  if (!t->a || !t->w || !t->w_scale || !t->out || (p->groups > 0) != (t->expert_offsets != nullptr))
-    return MOE_ERR_INVALID_ARG;
-  for (const void* q : {t->a, (const void*)t->a_scale, (const void*)t->w, (const void*)t->w_scale, t->mul, t->residual,
-                        (const void*)t->out})
-    if (!aligned16(q)) return MOE_ERR_INVALID_ARG;
-  if (t->bias && (uintptr_t)t->bias % (p->bias_dtype == MOE_SRC_BF16 ? 2 : 4)) return MOE_ERR_INVALID_ARG;
   const LinearPlan f = linear_plan(*p, t->a_scale != nullptr);
   const size_t need = f.total;
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
@@ -602,19 +640,7 @@ extern "C" moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_
   if (st != MOE_OK) return st;
 
   char* ws = (char*)workspace;
-  FcArgs g = {};
-  g.linear = true;
-  g.epi.bias = t->bias;
-  // (a bias row is N elements, N % 8 == 0: every row is as aligned as the first)
-  g.epi.bias_kind = !t->bias ? kBiasNone
-                    : p->bias_dtype == MOE_SRC_FP32 ? (aligned16(t->bias) ? kBiasF32 : kBiasF32Any)
-                                                    : (aligned16(t->bias) ? kBiasBf16 : kBiasBf16Any);
-  g.epi.fn = p->fn;
-  g.epi.mul = (const uint16_t*)t->mul;
-  g.epi.residual = (const uint16_t*)t->residual;
-  g.k = 1;
-  g.a = t->a;
-  g.a_scale = t->a_scale;
+  FcArgs g = linear_args(*p, *t, call);
   const bool quant = mx && !t->a_scale;
   if (quant && f.kind != Fc::kFew) {
     uint8_t* qc = (uint8_t*)ws + f.quant;
@@ -639,15 +665,8 @@ extern "C" moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_
   } else {
     g.dense_rows = (int)M;
   }
-  g.w = t->w;
-  g.w_scale = t->w_scale;
-  g.w_estride = wstride;
-  g.ws_estride = sstride;
-  g.K = (int)K;
-  g.N = (int)N;
   const int cols = fc_cols(f.kind, false, f.rows);
   g.nchunks = (int)((N + cols - 1) / cols);
-  g.epi.out = (__bf16*)t->out;
   const int wf = p->w_fmt == MX_E2M1 ? 1 : 2;
   const int cus = device_cus();
   hipError_t e;

@@ -48,22 +48,6 @@ __device__ __forceinline__ int exponent4(uint32_t amax) {
   return s;
 }
 
-// Codes (bits 0-3 and 4-7) of a pair of values already divided by 2^s, nearest: the
-// hardware conversion, which rounds ties to the even code, saturates at 6 and keeps
-// the sign of zeros, as encode<1> does.  The scale operand 1.0 leaves the values as
-// they are.
-template <int BYTE>
-__device__ __forceinline__ uint32_t pair4(uint32_t old, float a, float b) {
-  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, a, b, 1.0f, BYTE);
-}
-__device__ __forceinline__ uint32_t codes4(const float (&q)[8]) {
-  uint32_t w = 0;
-  w = pair4<0>(w, q[0], q[1]);
-  w = pair4<1>(w, q[2], q[3]);
-  w = pair4<2>(w, q[4], q[5]);
-  w = pair4<3>(w, q[6], q[7]);
-  return w;
-}
 // Code of q = v / 2^s, |q| <= 6, with random byte r
 __device__ __forceinline__ uint32_t random4(float q, uint32_t r) {
   const float x = fabsf(q);
@@ -194,7 +178,7 @@ __global__ __launch_bounds__(kThreadsQ) void k_mx4_rows(RowsArgs a) {
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] *= inv;
-      w = codes4(x);
+      w = e2m1_codes(x);
     }
     if (row[j] < a.rows) {
       const int64_t u = row[j] * a.units + (col[j] >> 3);
@@ -299,7 +283,7 @@ __global__ __launch_bounds__(kThreadsQ) void k_mx4_cols(ColsArgs a) {
         for (int i = 0; i < 8; ++i)
           w[g] |= random4(y[i], (rnd[h][2 * g + i / 4] >> (8 * (i % 4))) & 255u) << (4 * i);
       } else {
-        w[g] = codes4(y);
+        w[g] = e2m1_codes(y);
       }
     }
     sc[2 * pc + h][rb] = make_uint4(w[0], w[1], w[2], w[3]);

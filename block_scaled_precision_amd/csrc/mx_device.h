@@ -94,6 +94,16 @@ __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
   return (uint32_t)(uint16_t)r[0];
 }
 
+// E2M1 codes of eight values already divided by their block scale, the first in bits 0-3,
+// by the hardware conversion: nearest, ties to the even code, saturating at 6, signed zeros
+// kept, the same as encode<1>.
+__device__ __forceinline__ uint32_t e2m1_codes(const float (&q)[8]) {
+  uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, q[0], q[1], 1.0f, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[2], q[3], 1.0f, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[4], q[5], 1.0f, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[6], q[7], 1.0f, 3);
+}
+
 // SiLU(g) * u in fp32.
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
