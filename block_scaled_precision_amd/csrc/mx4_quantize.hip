@@ -40,12 +40,13 @@ constexpr float kHadamard = 0.17677669529663687f;  // 1 / sqrt(32)
 
 __device__ __forceinline__ int round_up128(int v) { return (v + 127) & ~127; }
 
-// Shared exponent of a block with largest magnitude amax (fp32 bits)
+// Shared exponent of a block with largest magnitude amax (fp32 bits); RANDOM: one more from
+// 1.5 times a power of two on, 6 * 2^s being 1.5 * 2^(s + 2)
 template <bool RANDOM>
 __device__ __forceinline__ int exponent4(uint32_t amax) {
-  int s = block_exponent<1>(amax);
-  if (RANDOM && (amax & 0x7fffffu) > 0x400000u && amax >= 0x00800000u) ++s;
-  return s;
+  if (!RANDOM) return block_exponent<1>(amax);
+  const int E = (int)(amax >> 23);
+  return E == 0 ? -127 : max(E - 129 + ((amax & 0x7fffffu) > 0x400000u ? 1 : 0), -127);
 }
 
 // Code of q = v / 2^s, |q| <= 6, with random byte r

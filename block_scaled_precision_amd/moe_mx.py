@@ -643,6 +643,10 @@ def _plan_balance(logits, topk_ids, mask=None, seq_offsets=None, loss=None, coun
             raise ValueError("mask: expected a bool or uint8 tensor")
         _require(mask, "mask", mask.dtype, (T,))
     S = _require_sequences(seq_offsets)
+    for name, t, dtype, shape in (("loss", loss, torch.float32, (2,)), ("counts", counts, torch.int32, (S, E)),
+                                  ("tokens", tokens, torch.int32, (S + 2,)), ("lse", lse, torch.float32, (T,))):
+        if t is not None:
+            _require(t, name, dtype, shape)
     device = _on_gpu(stream, logits, topk_ids, mask, seq_offsets, loss, counts, tokens, lse, workspace)
     if loss is None:
         loss = _empty((2,), torch.float32, device, stream)
@@ -652,10 +656,6 @@ def _plan_balance(logits, topk_ids, mask=None, seq_offsets=None, loss=None, coun
         tokens = _empty((S + 2,), torch.int32, device, stream)
     if lse is None:
         lse = _empty((T,), torch.float32, device, stream)
-    _require(loss, "loss", torch.float32, (2,))
-    _require(counts, "counts", torch.int32, (S, E))
-    _require(tokens, "tokens", torch.int32, (S + 2,))
-    _require(lse, "lse", torch.float32, (T,))
     need = moe_balance_workspace_bytes(T, E, S)
     if workspace is None and need:
         workspace = _empty((need,), torch.uint8, device, stream)
