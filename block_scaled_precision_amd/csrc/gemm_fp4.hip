@@ -22,14 +22,17 @@ constexpr int kThreads4 = 256;
 constexpr int TN = kFp4Cols;
 constexpr int ROW = 128;  // bytes of a row per stage: 256 K
 
-template <int MSUB> struct Lay4 {
+template <int MSUB, int SLOTS_> struct Lay4 {
   static constexpr int TM = 64 * MSUB;
-  static constexpr int NBUF = MSUB == 1 ? 3 : 2;
+  static constexpr int NBUF = SLOTS_;
   static constexpr int SA = TM * ROW, SB = TN * ROW, STAGE = SA + SB;
   static constexpr int GA = TM * 16, GROUP = GA + TN * 16;  // scales of two stages
-  static constexpr int GBUFS = NBUF == 2 ? 2 : 4;
+  static constexpr int GBUFS = MSUB == 1 ? 4 : 2;
   static constexpr int SCALES = NBUF * STAGE;
-  static constexpr int TOTAL = SCALES + GBUFS * GROUP;
+  // Biases of the items that have a stage under way (K >= 512: two stages an item), 256
+  // columns each.
+  static constexpr int BIAS = SCALES + GBUFS * GROUP, BBUFS = 3;
+  static constexpr int TOTAL = BIAS + BBUFS * 4 * TN;
   static constexpr int ACOP = TM / 32, BCOP = TN / 32;  // 1-KB copies per wave and stage
   static_assert(TOTAL <= 160 * 1024, "LDS");
 };
@@ -94,19 +97,21 @@ __device__ __forceinline__ void lds_copy16_b(v4i buffer, uint32_t off, uint32_t 
 
 // The copies of one wave: stages in order, each in COPIES parts that the caller
 // spreads between its MFMAs.
-template <int MSUB> struct Copier {
-  using L = Lay4<MSUB>;
+template <int MSUB, int NBUF, bool BIAS> struct Copier {
+  using L = Lay4<MSUB, NBUF>;
   static constexpr int COPIES = L::ACOP + L::BCOP;
   const FcArgs& p;
   const Sched4& sc;
   uint32_t lds0;
   int w, lane;
   // cursor: items begun, stage of the last, LDS offsets of its stage and scale group
-  int li = 0, ls, slot = 0, group = 0;
+  int li = 0, ls, slot = 0, group = 0, bbuf = 0;
   // the item and stage that parts belong to
   v4i abuf, wbuf;
   const uint8_t *asb, *wsb;
   uint32_t aoff[L::ACOP], boff[L::BCOP], asoff, wsoff, outside[2], soff, dst;
+  int64_t bias_at;  // of the bias, in elements
+  int cols;         // columns from the item's first one on
 
   // The block that copy i of this lane brings to its place of a row: block c of row r lies at
   // place c ^ (r >> 1 & 7), so that 16 rows read at the same block meet all of the banks.
@@ -128,6 +133,8 @@ template <int MSUB> struct Copier {
       boff[i] = (uint32_t)min(epi_row32(8 * (L::BCOP * w + i) + r8), last) * (uint32_t)kb + 16 * chunk(i);
     asoff = (uint32_t)min(64 * min(w, MSUB - 1) + lane, it.rows - 1) * (uint32_t)ks;
     wsoff = (uint32_t)min(epi_row32(64 * w + lane), last) * (uint32_t)ks;
+    bias_at = (int64_t)it.expert * p.N + n0;
+    cols = last + 1;
   }
   // Goes to the next stage.  Past the last stage of the last item that stage goes out
   // again, into a slot that nothing reads any more: without a branch around them the
@@ -169,6 +176,16 @@ template <int MSUB> struct Copier {
       lds_copy16_s(wsb + s0, wsoff, g + L::GA + 1024 * w);
       group = group == (L::GBUFS - 1) * L::GROUP ? 0 : group + L::GROUP;
     }
+    if (BIAS && ls == 0) bias();
+  }
+  // the item's bias as it is, a dword a lane; bf16 from the dword on that holds its first value
+  __device__ __forceinline__ void bias() {
+    const Epilogue e = epi_load();
+    const bool f32 = e.bias_kind == kBiasF32 || e.bias_kind == kBiasF32Any;
+    const uint64_t at = (uint64_t)e.bias + (f32 ? 4 : 2) * bias_at;
+    const int last = f32 ? cols - 1 : (cols - 1 + ((int)at >> 1 & 1)) >> 1;
+    lds_copy4_s((const uint8_t*)(at & ~(uint64_t)3), 4 * min(64 * w + lane, last), lds0 + L::BIAS + bbuf + 256 * w);
+    bbuf = bbuf == (L::BBUFS - 1) * 4 * TN ? 0 : bbuf + 4 * TN;
   }
   __device__ __forceinline__ void part(int i) {
     if (i < L::ACOP) lds_copy16_b(abuf, aoff[i] | outside[i & 1], soff, dst + 1024 * (L::ACOP * w + i));
@@ -202,8 +219,24 @@ __device__ __forceinline__ float acc_read(float a) {
   asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(a));
   return v;
 }
-template <int MSUB, bool IN>
-__device__ __forceinline__ void finish(v16f (&acc)[MSUB][4], const Item4& it, int N, int wm, int l32, int col) {
+// silu of epilogue.h with the hardware's exponential: t is off by |v| + 2 half steps of fp32 for
+// a few, which v t, at most 0.28, leaves below half a step of 1 in the result.  (12 instructions
+// for 30; with silu and a second factor the rows of 128 experts took 446 us, now 392.)
+__device__ __forceinline__ void fn_of(int fn, float (&v)[8]) {
+  if (fn == MX_FN_SILU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = __builtin_amdgcn_exp2f(fabsf(v[i]) * -1.44269504f);
+      v[i] = v[i] * (v[i] < 0.0f ? t : 1.0f) * __builtin_amdgcn_rcpf(1.0f + t);
+    }
+  } else {
+    epi_fn(fn, v);
+  }
+}
+
+template <int MSUB, bool IN, bool BIAS>
+__device__ __forceinline__ void finish(v16f (&acc)[MSUB][4], const Item4& it, int N, int wm, int l32, int col,
+                                       const uint8_t* biases) {
   // the last MFMAs' results, for the assembly below
   asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
   const Epilogue e = epi_load();
@@ -212,34 +245,58 @@ __device__ __forceinline__ void finish(v16f (&acc)[MSUB][4], const Item4& it, in
     return __builtin_amdgcn_make_buffer_rsrc(q ? (uint16_t*)q + tile : nullptr, 0, q ? (int)kOutside : 0, 0x00020000);
   };
   const auto out = buffer(e.out), mul = buffer(e.mul), res = buffer(e.residual);
-  const bool has_mul = e.mul != nullptr, has_bias = e.bias_kind != kBiasNone;
-  EpiBias bias[2][4];
-  if (has_bias) {
+  const bool has_mul = e.mul != nullptr;
+  float bias[2][4][8];
+  if constexpr (BIAS) {
+    const int c = col % TN;
+    auto each_bias = [&](auto f) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      bias[j >> 2][j & 3] = epi_bias(e, N, it.expert, min(col + 64 * (j >> 2) + 16 * (j & 3), N - 8));
+      for (int j = 0; j < 8; ++j) f(bias[j >> 2][j & 3], c + 16 * j);
+    };
+    if (e.bias_kind == kBiasF32 || e.bias_kind == kBiasF32Any) {
+      each_bias([&](float (&b)[8], int i) {
+        *(float4*)b = *(const float4*)(biases + 4 * i);
+        *(float4*)(b + 4) = *(const float4*)(biases + 4 * i + 16);
+      });
+    } else if (e.bias_kind == kBiasBf16) {
+      each_bias([&](float (&b)[8], int i) {
+        const uint4 x = *(const uint4*)(biases + 2 * i);
+        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) b[k] = __uint_as_float(k & 1 ? v[k / 2] & 0xffff0000u : v[k / 2] << 16);
+      });
+    } else {
+      const uint8_t* first = biases + ((uint64_t)e.bias & 2);
+      each_bias([&](float (&b)[8], int i) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) b[k] = __uint_as_float((uint32_t) * (const uint16_t*)(first + 2 * (i + k)) << 16);
+      });
+    }
   }
   const int rows = it.rows - 32 * wm - l32, cols = N - col;  // of this lane's first row and column on
   const int first = (int)(2 * ((uint32_t)(32 * wm + l32) * (uint32_t)N + col));
+  auto at = [&](int h, int m, int q) {
+    const int side = 64 * h + 16 * q < cols ? 0 : (int)kOutside;
+    return ((64 * m < rows ? first + 128 * h + m * (128 * N) : (int)kOutside) | side) + 32 * q;
+  };
+  // what a part takes in goes out AHEAD parts before it
+  constexpr int AHEAD = MSUB <= 2 ? 2 * MSUB : 1;
+  u32x4 nm[AHEAD][4], nr[AHEAD][4];
+  auto request = [&](int slot, int h, int m) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      nm[slot][q] = __builtin_amdgcn_raw_buffer_load_b128(mul, at(h, m, q), 0, 0);
+      nr[slot][q] = __builtin_amdgcn_raw_buffer_load_b128(res, at(h, m, q), 0, 0);
+    }
+  };
+  if constexpr (IN && AHEAD > 1) {
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) request(j, j / MSUB, j % MSUB);
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    int side[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) side[q] = 64 * h + 16 * q < cols ? 0 : (int)kOutside;
-    auto at = [&](int m, int q) {
-      return ((64 * m < rows ? first + 128 * h + m * (128 * N) : (int)kOutside) | side[q]) + 32 * q;
-    };
-    u32x4 nm[4], nr[4];
-    auto request = [&](int m) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        nm[q] = __builtin_amdgcn_raw_buffer_load_b128(mul, at(m, q), 0, 0);
-        nr[q] = __builtin_amdgcn_raw_buffer_load_b128(res, at(m, q), 0, 0);
-      }
-    };
-    if constexpr (IN) request(0);
-#pragma unroll 1
-    for (int m = 0; m < MSUB; ++m) {
+    if constexpr (IN && AHEAD == 1) request(0, h, 0);
+    auto part = [&](int m, int slot) {
       float v[4][8];
       each(std::make_integer_sequence<int, MSUB>(), [&](auto M) {
         if (m == M.value) {
@@ -250,26 +307,26 @@ __device__ __forceinline__ void finish(v16f (&acc)[MSUB][4], const Item4& it, in
               v[q][i] = acc_read(acc[M.value][2 * h + (i >> 2)][4 * q + (i & 3)]);
         }
       });
-      if (has_bias) {
+      if constexpr (BIAS) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[q][i] += epi_bias_at(e, bias[h][q], i);
+          for (int i = 0; i < 8; ++i) v[q][i] += bias[h][q][i];
       }
       if (e.fn != MX_FN_NONE) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) epi_fn(e.fn, v[q]);
+        for (int q = 0; q < 4; ++q) fn_of(e.fn, v[q]);
       }
       if constexpr (IN) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float f = __uint_as_float(i & 1 ? nm[q][i / 2] & 0xffff0000u : nm[q][i / 2] << 16);
-            v[q][i] *= has_mul ? f : 1.0f;
-            v[q][i] += __uint_as_float(i & 1 ? nr[q][i / 2] & 0xffff0000u : nr[q][i / 2] << 16);
+            const uint32_t x = nm[slot][q][i / 2], y = nr[slot][q][i / 2];
+            v[q][i] *= has_mul ? __uint_as_float(i & 1 ? x & 0xffff0000u : x << 16) : 1.0f;
+            v[q][i] += __uint_as_float(i & 1 ? y & 0xffff0000u : y << 16);
           }
-        request(min(m + 1, MSUB - 1));
+        if constexpr (AHEAD == 1) request(0, h, min(m + 1, MSUB - 1));
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -281,16 +338,23 @@ __device__ __forceinline__ void finish(v16f (&acc)[MSUB][4], const Item4& it, in
           __builtin_memcpy(&w, &o2, 4);
           o[i] = w;
         }
-        __builtin_amdgcn_raw_buffer_store_b128(o, out, at(m, q), 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(o, out, at(h, m, q), 0, 0);
       }
+    };
+    if constexpr (MSUB <= 2) {
+#pragma unroll
+      for (int m = 0; m < MSUB; ++m) part(m, h * MSUB + m);
+    } else {
+#pragma unroll 1
+      for (int m = 0; m < MSUB; ++m) part(m, 0);
     }
   }
 }
 
-template <int MSUB, bool IN>
+template <int MSUB, int NBUF, bool IN, bool BIAS>
 __global__ __launch_bounds__(kThreads4, 1) void k_linear_fp4(FcArgs p) {
-  using L = Lay4<MSUB>;
-  using C = Copier<MSUB>;
+  using L = Lay4<MSUB, NBUF>;
+  using C = Copier<MSUB, NBUF, BIAS>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[L::TOTAL];
   Sched4 sc;
   sc.nk = (p.K + 255) / 256;
@@ -402,7 +466,7 @@ __global__ __launch_bounds__(kThreads4, 1) void k_linear_fp4(FcArgs p) {
   }
   take_scales();
   const uint8_t* st = smem;
-  int slot = 0;
+  int slot = 0, bbuf = 0;
   for (int ci = 0; ci < sc.items; ++ci) {
     const Item4 it = item_at<L::TM>(p, sc, ci);
 #pragma unroll
@@ -422,7 +486,7 @@ __global__ __launch_bounds__(kThreads4, 1) void k_linear_fp4(FcArgs p) {
         among(k, reads, i0, mid, [&](int i) { read(0, st, off[2], i); });
       });
       pin();
-      const bool behind = copy.scales();  // (of the stage begun last)
+      const bool behind = copy.scales(), first = copy.ls == 0;  // (of the stage begun last)
       if (copy.ends_item()) copy.next_item();
       const int kn = ks + 1 == sc.nk ? 0 : ks + 1;
       uint32_t so = 0;
@@ -453,7 +517,10 @@ __global__ __launch_bounds__(kThreads4, 1) void k_linear_fp4(FcArgs p) {
       if (L::NBUF == 2) {
         if (stored) wait_vm_lgkm0<kBehind>();
         else wait_vm_lgkm0<0>();
-      } else if (behind) {  // and the stage after the next, begun last, is on its way
+      } else if (BIAS && first) {  // and the stage after the next, begun last, is on its way
+        if (stored) wait_vm_lgkm0<kBehind + C::COPIES + 3>();
+        else wait_vm_lgkm0<C::COPIES + 3>();
+      } else if (behind) {
         if (stored) wait_vm_lgkm0<kBehind + C::COPIES + 2>();
         else wait_vm_lgkm0<C::COPIES + 2>();
       } else {
@@ -479,25 +546,30 @@ __global__ __launch_bounds__(kThreads4, 1) void k_linear_fp4(FcArgs p) {
 #pragma unroll
     for (int i = half; i < C::COPIES; ++i) copy.part(i);
     // the lane holds row 32 (wm + 2m) + l32 of the tile, eight columns of each piece
-    finish<MSUB, IN>(acc, it, p.N, wm, l32, it.nb * TN + 128 * wn + 8 * g);
+    finish<MSUB, IN, BIAS>(acc, it, p.N, wm, l32, it.nb * TN + 128 * wn + 8 * g, smem + L::BIAS + bbuf);
+    bbuf = bbuf == (L::BBUFS - 1) * 4 * TN ? 0 : bbuf + 4 * TN;
   }
   wait_vm_lgkm0<0>();  // no copy may land in LDS that is no longer this workgroup's
 }
 
 }  // namespace
 
-template <int MSUB>
+template <int MSUB, int NBUF>
 static void launch_fp4_t(const FcArgs& p, int grid, hipStream_t st) {
-  if (p.epi.mul || p.epi.residual) k_linear_fp4<MSUB, true><<<grid, kThreads4, 0, st>>>(p);
-  else k_linear_fp4<MSUB, false><<<grid, kThreads4, 0, st>>>(p);
+  const bool in = p.epi.mul || p.epi.residual, bias = p.epi.bias_kind != kBiasNone;
+  auto kernel = in ? (bias ? k_linear_fp4<MSUB, NBUF, true, true> : k_linear_fp4<MSUB, NBUF, true, false>)
+                   : (bias ? k_linear_fp4<MSUB, NBUF, false, true> : k_linear_fp4<MSUB, NBUF, false, false>);
+  kernel<<<grid, kThreads4, 0, st>>>(p);
 }
 
 hipError_t launch_linear_fp4(const FcArgs& p, int rows, int grid, hipStream_t st) {
   if (grid < 8) grid = 8;
   grid &= ~7;
-  if (rows == 256) launch_fp4_t<4>(p, grid, st);
-  else if (rows == 128) launch_fp4_t<2>(p, grid, st);
-  else if (rows == 64) launch_fp4_t<1>(p, grid, st);
+  const bool pairs = (p.K + 255) / 256 % 2 == 0;
+  if (rows == 256) launch_fp4_t<4, 2>(p, grid, st);
+  else if (rows == 128 && pairs) launch_fp4_t<2, 3>(p, grid, st);
+  else if (rows == 128) launch_fp4_t<2, 2>(p, grid, st);
+  else if (rows == 64) launch_fp4_t<1, 3>(p, grid, st);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }

@@ -191,6 +191,28 @@ def test_nan_scales_and_infinite_results(M, N, K):
         assert np.isinf(got[0, 1])
 
 
+@pytest.mark.parametrize("M,N,K,G", [(3, 72, 256, 0), (300, 2056, 640, 0), (1500, 4104, 512, 0), (3000, 4104, 512, 0), (3000, 520, 640, 40),
+                                     (3000, 2056, 512, 6), (300, 4104, 512, 40)])
+def test_biases_of_any_alignment(M, N, K, G):
+    """Either type, from every address of the type; the bias differs in every column and group,
+    and NaN stands before and behind it."""
+    from block_scaled_precision_amd import moe_mx as m
+    w, s = (t.cuda() for t in _codes((G, N) if G else (N,), K, 50))
+    a, asc = _codes((M,), K, 51)
+    off = _offsets(M, G, M)
+    kw = dict(a_scale=asc.cuda(), expert_offsets=None if off is None else torch.from_numpy(off).int().cuda())
+    n = max(G, 1) * N
+    values = ((torch.arange(n) * 37) % 509 - 254).float()
+    for dtype, step in ((torch.float32, 4), (BF16, 2)):
+        ref, _, _ = mx4.mx4_linear(a.numpy(), w.cpu().numpy(), s.cpu().numpy(), a_scale=asc.numpy(), offsets=off,
+                                   bias=values.to(dtype).double().numpy().reshape((G, N) if G else (N,)))
+        for at in range(0, 16, step):
+            buf = torch.full((n + 16,), float("nan"), dtype=dtype, device="cuda")
+            view = buf[at // step:at // step + n]
+            view.copy_(values)
+            _same_bits(m.mx4_linear(a.cuda(), w, s, bias=view.view((G, N) if G else (N,)), **kw), ref, f"{dtype} at {at}")
+
+
 def test_no_rows_and_aliases():
     from block_scaled_precision_amd import moe_mx as m
     a, (w, s) = _ints((0, 256), 9, 20), _codes((64,), 256, 9)
