@@ -38,16 +38,23 @@ inline mx_linear_problem_t as_mxfp8(const mx4_linear_problem_t& p) {
 }
 
 // The smallest of the estimated times in microseconds, as linear_kind chooses
-// (linear_plan.h; N = 4096, K = 7168 on an MI355X, from codes unless said, with the
-// launches in front):
-//   few rows: 1 row 7.9, 16 rows 9.5, 32 rows 15.5; from bf16 9.7, 14.1, 25.7
-//   tiles of 64, 128 and 256 rows: up to 64 rows 18.5, 25, 38; 256 rows 23, 31, 40; 1024 rows
-//     26, 35, 45; 4096 rows 88, 73, 62; 8192 rows 166, 142, 120: a stage of 256 K takes 0.6, 0.85
-//     and 1.3 where few workgroups have an item and 0.75, 1.25 and 2.1 where all do
-//   widened: 16 rows 12.9, 32 rows 12.7, 64 rows 17, 256 rows 26, 1024 rows 54, 8192 rows 260
-// Experts: 512 rows over 384, 7168 x 2048: widened 359, 64-row tiles 370, 128 449; 16384 rows
-// over 256, 1536 x 5120: 324, 268, 261, 256-row tiles 292; 65536 over 128, 1536 x 4096: 529,
-// 405, 352, 309.
+// (linear_plan.h).  Over 82 measured shapes (1 to 76800 rows, dense and 8 to 384 groups) the
+// choice costs 0.8 % more than the best kernel each time, 19 % at most.
+//   few rows in place (a step of 1024 K): from codes 0.45 to 0.65, from bf16 0.68 to 1.23; twice
+//     that with groups (N = 4096, K = 7168: 1 row 7.9, 16 rows 9.5, 32 rows 15.5; from bf16
+//     9.7, 14.1, 25.7)
+//   tiles of 64, 128 and 256 rows: a stage of 256 K 0.6, 0.85 and 1.3 where few workgroups
+//     have an item and 0.76, 1.12 and 2.05 where all do, 15 and 8 % more for the smaller ones
+//     with groups, which share no weights; 1.4, 3.3 and 9 an item beside its stages.  N = 4096,
+//     K = 7168: 64 rows 20, 25, 39; 1024 rows 27, 32, 47; 8192 rows 183, 143, 121; 65536 rows
+//     of 128 groups, 1536 x 4096: 420, 307, 287; 512 rows of 384 groups, 7168 x 2048: 378, 425, 587
+//   widened: 64 rows 17, 256 rows 26, 1024 rows 54, 8192 rows 260; the two grouped 469 and 368
+struct Fp4Cost {
+  double few, all, group, item;
+};
+constexpr Fp4Cost kFp4Cost[3] = {{0.6, 0.76, 1.15, 1.4}, {0.85, 1.12, 1.08, 3.3}, {1.3, 2.05, 1.0, 9.0}};
+constexpr double kFp4WeightRate = 5.5e6;  // bytes per microsecond from HBM
+
 inline Mx4Plan mx4_plan(const mx4_linear_problem_t& p, bool has_a_scale) {
   const mx_linear_problem_t q = as_mxfp8(p);
   const LinearCost c(q, true);
@@ -62,15 +69,24 @@ inline Mx4Plan mx4_plan(const mx4_linear_problem_t& p, bool has_a_scale) {
   const double before = p.groups > 0 ? 4.0 : 0.0;
   const double quant = has_a_scale ? 0.0 : 3.0 + (double)p.M * p.K * 2.53 / 4.5e6;
   const double stages = std::ceil(p.K / 256.0), own = p.groups > 0 ? 1.15 : 1.0;
-  const double widen = 3.0 + (double)p.M * p.K * 1.5 / 4.5e6 + before + quant;
-  take(Fc4::kWiden, 0, widen + std::min(c.time(16, kRowsCols, stages, own * 0.6), c.time(64, kRowsCols, stages, own * 0.75)));
+  double rows8 = -1.0;  // of the kernels for few rows of E4M3, in K ranges as linear_kind has them
+  const int most = p.groups > 0 ? 1 : (int)std::min(16.0, std::max(1.0, std::floor(stages / 2.0)));
+  for (int s = 1; s <= most; ++s) {
+    const double t = std::min(c.time(16, kRowsCols, stages, own * 0.55, s), c.time(64, kRowsCols, stages, own * 0.75, s)) +
+                     c.join_time(s);
+    if (rows8 < 0.0 || t < rows8) rows8 = t;
+  }
+  take(Fc4::kWiden, 0, 3.0 + (double)p.M * p.K * 1.5 / 4.5e6 + before + quant + rows8);
   if (p.K >= kFp4K && p.N <= kFp4MaxN) {
-    const double few[3] = {0.6, 0.85, 1.3}, all[3] = {0.75, 1.25, 2.1};
+    const double weights = c.active * p.N * (double)p.K * (0.5 + 1.0 / 32.0) / kFp4WeightRate;
     for (int i = 0; i < 3; ++i) {
-      const int rows = 64 << i;
-      const double items = c.tiles(rows) * std::ceil(p.N / (double)kFp4Cols);
-      const double t = few[i] + (all[i] - few[i]) * std::min(1.0, items / kLinearWgs);
-      take(Fc4::kTile, rows, c.time(rows, kFp4Cols, stages, t) + before + quant);
+      const Fp4Cost& f4 = kFp4Cost[i];
+      const double items = c.tiles(64 << i) * std::ceil(p.N / (double)kFp4Cols);
+      double rounds = items / kLinearWgs;
+      const double t = f4.few + (f4.all - f4.few) * std::min(1.0, rounds);
+      if (p.groups == 0 || rounds < 8.0) rounds = std::ceil(rounds);
+      const double tiles = rounds * (stages * t * (p.groups > 0 ? f4.group : 1.0) + f4.item);
+      take(Fc4::kTile, 64 << i, 1.5 + std::max(tiles, weights) + before + quant);
     }
   }
   const int64_t blocks = (p.N + kFewCols - 1) / kFewCols;

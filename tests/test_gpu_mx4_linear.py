@@ -42,14 +42,16 @@ def _offsets(M, G, seed):
 CASES = [
     ("few", 16, 1, 8, 128, 0), ("few", 16, 1, 4096, 7168, 0), ("few", 16, 5, 264, 384, 0), ("few", 16, 16, 1032, 1152, 0),
     ("few", 16, 33, 520, 640, 6), ("few", 16, 3, 72, 128, 2), ("few", 16, 20, 136, 896, 40), ("few", 16, 100, 40, 256, 1),
-    ("tile", 64, 300, 2056, 512, 0), ("tile", 64, 700, 1032, 1152, 0), ("tile", 64, 4200, 1544, 640, 0),
-    ("tile", 64, 700, 4104, 1152, 1), ("tile", 64, 3000, 520, 640, 40), ("tile", 64, 1500, 1032, 2048, 6),
-    ("tile", 128, 1500, 4104, 512, 0), ("tile", 128, 9000, 1288, 640, 0), ("tile", 128, 3000, 2056, 512, 6),
-    ("tile", 128, 9000, 264, 1152, 40), ("tile", 128, 4200, 1032, 640, 1),
-    ("tile", 256, 3000, 4104, 512, 0), ("tile", 256, 6000, 2056, 1152, 0), ("tile", 256, 9000, 4104, 640, 0),
-    ("tile", 256, 6000, 2056, 640, 1), ("tile", 256, 9300, 4104, 512, 3),
-    ("widen", 0, 700, 1032, 128, 0), ("widen", 0, 40, 4096, 1152, 0), ("widen", 0, 1500, 520, 384, 0),
-    ("widen", 0, 300, 4104, 512, 40), ("widen", 0, 3000, 1032, 128, 6),
+    ("tile", 64, 300, 2056, 512, 0), ("tile", 64, 700, 1032, 1152, 0), ("tile", 64, 4200, 2056, 640, 0),
+    ("tile", 64, 700, 4104, 1152, 1), ("tile", 64, 4200, 1032, 512, 40), ("tile", 64, 1500, 1032, 2048, 6),
+    ("tile", 64, 300, 4104, 512, 40),
+    ("tile", 128, 1500, 4104, 512, 0), ("tile", 128, 9000, 1288, 640, 0), ("tile", 128, 9000, 1288, 896, 0),
+    ("tile", 128, 4200, 1544, 640, 0), ("tile", 128, 9000, 4104, 640, 0), ("tile", 128, 3000, 2056, 512, 6),
+    ("tile", 128, 9000, 264, 1152, 40), ("tile", 128, 4200, 1032, 640, 1), ("tile", 128, 9300, 4104, 512, 3),
+    ("tile", 256, 3000, 4104, 1920, 0), ("tile", 256, 6000, 2056, 2176, 0), ("tile", 256, 9300, 2568, 3200, 0),
+    ("tile", 256, 1900, 4104, 1920, 1), ("tile", 256, 6000, 4104, 1664, 3),
+    ("widen", 0, 700, 1032, 128, 0), ("widen", 0, 64, 1032, 7168, 0), ("widen", 0, 1500, 520, 384, 0),
+    ("widen", 0, 3000, 1032, 128, 6),
 ]
 IDS = [f"{k}{r}_{M}x{N}x{K}_g{G}" for k, r, M, N, K, G in CASES]
 
