@@ -13,21 +13,31 @@
 // exp(logit - lse), the gradient needs one pass over the logits and no second pass
 // over what the loss computed.
 //
-// Both directions are bound by reading the logits once (and writing their gradient
-// once).  A row is held in registers by a group of 16, 32 or 64 neighbouring lanes,
-// pieces of 16 bytes each where lengths, strides and addresses allow, single values
-// elsewhere, so that a maximum and two sums over the group are all that a row costs.
+// Both directions read the logits once (and write their gradient once).  A row is held in
+// registers by a group of 16, 32 or 64 neighbouring lanes, pieces of 16 bytes each where
+// lengths, strides and addresses allow, single values elsewhere, so that a maximum and a sum
+// over the group are all that a row costs beside its values.
 // A loss over few tokens takes one launch of one workgroup.  Otherwise workgroups
 // take chunks of consecutive rows and leave, for each sequence that a chunk meets,
 // its sums in a slot; a second launch adds the slots in order, and the workgroup of it
 // that is last to arrive adds up what the others left, in order again: no result
 // depends on scheduling, and results repeat bit for bit.  Sums over the rows of a
 // chunk are held in fp32, sums over chunks and sequences in fp64.
+//
+// Measured (MI355X, warm; bytes at 5 TB/s in brackets): 65536 x 256 and what is added to its
+// gradient 37 us [40]: bound by memory.  The loss is bound by what follows one after the
+// other, memory's latencies of about a microsecond in both launches: 65536 x 128 13 + 6
+// us [7], 8192 x 384 in 13 sequences 7.5 + 7 [2.6], 64 x 384 7 in one launch, of which a launch
+// that does nothing takes 2.  On the way there: the offsets through LDS and rows without regard
+// to sequences 9.0 -> 7.5 us (8192 x 384), 16 lanes a row and a cheaper exponential 15.5 -> 12.5
+// (65536 x 128), no fences in the second launch 16.6 -> 11.3, fewer workgroups in it where
+// there are many sequences -> 8.2, sums over lanes by register moves -> 7.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <type_traits>
 
+#include "copy_ring.h"
 #include "internal.h"
 
 namespace moe_mx {
@@ -36,9 +46,20 @@ namespace {
 
 constexpr int kThreadsB = 256;
 constexpr int kOneThreads = 1024;
+// Tokens up to which the loss takes one launch of one workgroup, for up to
+// kOneSeqs sequences
+constexpr int kOneTokens = 128, kOneSeqs = 4;
 constexpr float kNegInf = -__builtin_inff();
 
 typedef float v4 __attribute__((ext_vector_type(4)));
+
+// A barrier for what lies in LDS: __syncthreads also waits for every store to memory, a
+// microsecond each time.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  wait_lgkm0();
+  barrier();
+}
 
 // ------------------------------------------------------- rows in registers --
 
@@ -63,6 +84,17 @@ struct Sum {
 struct Max {
   __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
+
+// exp(d) for d <= 0, 0 for NaN: d log2(e) in two parts and the hardware's exp2, off by 1.3 |d| + 4
+// half steps of fp32; a value below 2^-126 may become 0.  (7 instructions for expf's 12, of
+// which the loss has little else.)
+__device__ __forceinline__ float exp_below(float d) {
+  constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+  d = fmaxf(d, -200.0f);
+  const float t = d * kLog2e, rest = fmaf(d, kLog2e, -t);
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, rest * kLn2, e);
+}
 
 // P pieces of V values of a row, piece q of lane c at value (q L + c) V.
 template <int V, int P> struct RowRegs {
@@ -95,15 +127,30 @@ __device__ __forceinline__ float row_max(const float (&v)[N]) {
 
 // -------------------------------------------------------------- sequences --
 
+// Offsets of up to so many sequences are held in LDS: one load by all threads in place of a
+// chain of them.
+constexpr int kSeqLds = 1024;
+struct Offsets {
+  const int32_t* mem;
+  const int32_t* lds;  // or nullptr
+  __device__ __forceinline__ int operator()(int i) const { return lds ? lds[i] : mem[i]; }
+};
+template <int TH>
+__device__ __forceinline__ Offsets load_offsets(const int32_t* off, int S, int32_t* lds) {
+  if (!off || S > kSeqLds) return {off, nullptr};
+  for (int i = threadIdx.x; i <= S; i += TH) lds[i] = off[i];
+  lds_barrier();
+  return {off, lds};
+}
 // Rows [lo, hi) of sequence s, within [0, T)
-__device__ __forceinline__ void seq_rows(const int32_t* off, int s, int T, int& lo, int& hi) {
-  if (!off) {
+__device__ __forceinline__ void seq_rows(const Offsets& off, int s, int T, int& lo, int& hi) {
+  if (!off.mem) {
     lo = 0;
     hi = T;
     return;
   }
-  lo = min(max(off[s], 0), T);
-  hi = min(max(off[s + 1], lo), T);
+  lo = min(max(off(s), 0), T);
+  hi = min(max(off(s + 1), lo), T);
 }
 // The last sequence that begins at or before row t, 0 if none does
 template <class Off>
@@ -143,92 +190,139 @@ struct BalanceArgs {
   uint32_t* arrived;
 };
 
-// What a workgroup of TH threads gathers of the rows [lo, hi) of one sequence
+// What a workgroup of TH threads gathers of the rows of one sequence
 template <int V, int L, int P, int TH> struct Gathered {
   static constexpr int GROUPS = TH / L;
-  float p[GROUPS][V * L * P];  // one row of sums per group (GROUPS V L P <= 16 KiB of them)
+  float p[GROUPS][V * L * P];  // one row of sums per group (4 TH V P bytes: 128 KiB at most)
   int32_t c[kMaxExperts];
   float z[GROUPS];
   int32_t n[GROUPS];
 };
 
-// Rows [lo, hi): their lse, and into g each group's sums of p, lse^2 and tokens
-// and all groups' counts.  g.c is zero at the start.
-template <int V, int L, int P, int TH>
-__device__ __forceinline__ void gather_rows(const BalanceArgs& a, int lo, int hi, Gathered<V, L, P, TH>& g) {
+// Rows [t0, t1), which lie in sequences: their lse, and for each sequence s that they meet, in
+// order, into g each group's sums of p, lse^2 and tokens and all groups' counts, and
+// flush(s) between two barriers.  Rows are loaded and their softmax is taken without regard to
+// the sequences, which a batch of rows may meet several of: a pass over the rows for each
+// of them took 3 us more where one chunk met two.
+template <int V, int L, int P, int TH, class Flush>
+__device__ __forceinline__ void gather_rows(const BalanceArgs& a, const Offsets& off, int t0, int t1,
+                                            Gathered<V, L, P, TH>& g, Flush flush) {
+  if (t0 >= t1) return;
   constexpr int G = TH / L;
+  // as many rows at once as 32 registers hold, up to 4: a load takes as long as all of them
+  // (one where the whole loss has one workgroup, whose lanes cover most of its rows)
+  constexpr int U = TH == kOneThreads ? 1 : P * V <= 8 ? 4 : P * V <= 16 ? 2 : 1;
   const int c = threadIdx.x & (L - 1), grp = threadIdx.x / L;
-  float acc[P * V];
+  float acc[P * V], z = 0.f;
+  int n = 0;
 #pragma unroll
   for (int i = 0; i < P * V; ++i) acc[i] = 0.f;
-  float z = 0.f;
-  int n = 0;
-  for (int t = lo + grp; t < hi; t += G) {
-    RowRegs<V, P> r;
-    load_row<V, L, P>(r, a.logits + (int64_t)t * a.ld, a.E, c, kNegInf);
-    const int32_t id0 = c < a.k ? a.ids[(int64_t)t * a.k + c] : -1;
-    const bool live = !a.mask || a.mask[t] != 0;
-    const float m = row_max<L>(r.v);
-    const bool counted = live && m != kNegInf;
-    if (!counted) {
-      if (c == 0) a.lse[t] = kNegInf;
-      continue;
-    }
-    float s = 0.f;
+  for (int e = threadIdx.x; e < a.E; e += TH) g.c[e] = 0;
+  int t = t0, s = -1, end = t0;  // the first row that is not gathered, its sequence, where that ends
+  for (int b = t0; b < t1; b += U * G) {
+    RowRegs<V, P> rows[U];
+    int32_t ids[U];
+    float l[U], inv[U];
+    bool counted[U];
 #pragma unroll
-    for (int i = 0; i < P * V; ++i) {
-      r.v[i] = expf(r.v[i] - m);
-      s += r.v[i];
+    for (int u = 0; u < U; ++u) {
+      const int r = b + grp + u * G;
+      const bool in = r < t1;
+      load_row<V, L, P>(rows[u], a.logits + (int64_t)r * a.ld, in ? a.E : 0, c, kNegInf);
+      ids[u] = in && c < a.k ? a.ids[(int64_t)r * a.k + c] : -1;
+      counted[u] = in && (!a.mask || a.mask[r] != 0);
     }
-    s = group_reduce<L>(s, Sum());
-    const float inv = 1.0f / s, l = m + logf(s);
+    if (s < 0) {
+      s = a.off ? seq_search(off, a.S, t) : 0;
+      int lo;
+      seq_rows(off, s, a.T, lo, end);
+      lds_barrier();  // the counts are zero
+    }
 #pragma unroll
-    for (int i = 0; i < P * V; ++i) acc[i] = fmaf(r.v[i], inv, acc[i]);
-    if (id0 >= 0 && id0 < a.E) atomicAdd(&g.c[id0], 1);
-    for (int j = c + L; j < a.k; j += L) {
-      const int32_t id = a.ids[(int64_t)t * a.k + j];
-      if (id >= 0 && id < a.E) atomicAdd(&g.c[id], 1);
+    for (int u = 0; u < U; ++u) {
+      if (b + u * G >= t1) break;
+      const float m = row_max<L>(rows[u].v);
+      counted[u] = counted[u] && m != kNegInf;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < P * V; ++i) {
+        rows[u].v[i] = exp_below(rows[u].v[i] - m);
+        sum += rows[u].v[i];
+      }
+      sum = m < -kNegInf ? group_reduce<L>(sum, Sum()) : __builtin_nanf("");
+      inv[u] = 1.0f / sum;
+      l[u] = counted[u] ? m + logf(sum) : kNegInf;
+      const int r = b + grp + u * G;
+      if (c == 0 && r < t1) a.lse[r] = l[u];
     }
-    z = fmaf(l, l, z);
-    ++n;
-    if (c == 0) a.lse[t] = l;
+    const int bend = min(t1, b + U * G);
+    while (t < bend) {
+      if (end <= t) return;  // offsets that do not ascend
+      const int to = min(bend, end);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = b + grp + u * G;
+        if (b + u * G >= t1) break;
+        if (!counted[u] || r < t || r >= to) continue;
+#pragma unroll
+        for (int i = 0; i < P * V; ++i) acc[i] = fmaf(rows[u].v[i], inv[u], acc[i]);
+        if (ids[u] >= 0 && ids[u] < a.E) atomicAdd(&g.c[ids[u]], 1);
+        for (int j = c + L; j < a.k; j += L) {
+          const int32_t id = a.ids[(int64_t)r * a.k + j];
+          if (id >= 0 && id < a.E) atomicAdd(&g.c[id], 1);
+        }
+        z = fmaf(l[u], l[u], z);
+        ++n;
+      }
+      t = to;
+      if (t != end && t != t1) continue;
+#pragma unroll
+      for (int q = 0; q < P; ++q)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          g.p[grp][(q * L + c) * V + i] = acc[q * V + i];
+          acc[q * V + i] = 0.f;
+        }
+      if (c == 0) {
+        g.z[grp] = z;
+        g.n[grp] = n;
+      }
+      z = 0.f;
+      n = 0;
+      lds_barrier();
+      flush(s);
+      if (t == t1) return;
+      lds_barrier();
+      for (int e = threadIdx.x; e < a.E; e += TH) g.c[e] = 0;
+      s = seq_search(off, a.S, t);
+      int lo;
+      seq_rows(off, s, a.T, lo, end);
+      lds_barrier();
+    }
   }
-#pragma unroll
-  for (int q = 0; q < P; ++q)
-#pragma unroll
-    for (int i = 0; i < V; ++i) g.p[grp][(q * L + c) * V + i] = acc[q * V + i];
-  if (c == 0) {
-    g.z[grp] = z;
-    g.n[grp] = n;
-  }
+}
+
+// The rows of [t0, t1) that lie in sequences; the others' lse is written.
+template <int TH>
+__device__ __forceinline__ void clip_rows(const BalanceArgs& a, const Offsets& off, int& t0, int& t1) {
+  if (!a.off) return;
+  const int lo = min(max(off(0), 0), a.T), hi = min(max(off(a.S), 0), a.T);
+  for (int t = t0 + threadIdx.x; t < t1; t += TH)
+    if (t < lo || t >= hi) a.lse[t] = kNegInf;
+  t0 = max(t0, lo);
+  t1 = min(t1, hi);
 }
 
 template <int V, int L, int P>
 __global__ __launch_bounds__(kThreadsB) void k_balance_rows(BalanceArgs a) {
   using Gt = Gathered<V, L, P, kThreadsB>;
   __shared__ Gt g;
-  const int t0 = blockIdx.x * a.rows, t1 = min(a.T, t0 + a.rows);
+  __shared__ int32_t lds[kSeqLds + 1];
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.arrived = 0;
-  auto begins = [&](int i) { return a.off[i]; };
-  int lo0 = 0, hi0 = a.T;
-  if (a.off) {
-    lo0 = min(max(a.off[0], 0), a.T);
-    hi0 = min(max(a.off[a.S], 0), a.T);
-    // rows of no sequence
-    for (int t = t0 + threadIdx.x; t < t1; t += kThreadsB)
-      if (t < lo0 || t >= hi0) a.lse[t] = kNegInf;
-  }
-  int t = max(t0, lo0);
-  int s = a.off && t < t1 ? seq_search(begins, a.S, t) : 0;
-  while (t < min(t1, hi0)) {
-    int lo, hi;
-    seq_rows(a.off, s, a.T, lo, hi);
-    const int end = min(t1, hi);
-    if (end <= t) break;  // offsets that do not ascend
-    for (int e = threadIdx.x; e < a.E; e += kThreadsB) g.c[e] = 0;
-    __syncthreads();
-    gather_rows<V, L, P, kThreadsB>(a, t, end, g);
-    __syncthreads();
+  const Offsets off = load_offsets<kThreadsB>(a.off, a.S, lds);
+  int t0 = blockIdx.x * a.rows, t1 = min(a.T, t0 + a.rows);
+  clip_rows<kThreadsB>(a, off, t0, t1);
+  gather_rows<V, L, P, kThreadsB>(a, off, t0, t1, g, [&](int s) {
     const int64_t slot = (int64_t)blockIdx.x + s;
     for (int e = threadIdx.x; e < a.E; e += kThreadsB) {
       float p = 0.f;
@@ -247,108 +341,145 @@ __global__ __launch_bounds__(kThreadsB) void k_balance_rows(BalanceArgs a) {
       a.sum_z[slot] = z;
       a.sum_n[slot] = n;
     }
-    __syncthreads();
-    t = end;
-    if (t < min(t1, hi0)) s = seq_search(begins, a.S, t);
-  }
+  });
 }
 
-// Sum over a workgroup's threads, in every thread; the order is fixed.  sh: a value
-// per wave.
-template <int TH, class T>
-__device__ __forceinline__ T block_sum(T v, T* sh) {
+// What the losses are made of: the terms of both, tokens, sequences with one
+struct Sums {
+  double balance, z;
+  int32_t n, used;
+};
+__device__ __forceinline__ Sums operator+(const Sums& x, const Sums& y) {
+  return {x.balance + y.balance, x.z + y.z, x.n + y.n, x.used + y.used};
+}
+// Sum over 16 neighbouring lanes, in each of them: by moves within the row of lanes, which
+// cost an instruction each where a shuffle costs a hundred cycles
+template <int CTRL> __device__ __forceinline__ int32_t moved(int32_t v) {
+  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true);
+}
+template <int CTRL> __device__ __forceinline__ double moved(double v) {
+  return __hiloint2double(moved<CTRL>(__double2hiint(v)), moved<CTRL>(__double2loint(v)));
+}
+template <int CTRL> __device__ __forceinline__ Sums add_moved(const Sums& v) {
+  return v + Sums{moved<CTRL>(v.balance), moved<CTRL>(v.z), moved<CTRL>(v.n), moved<CTRL>(v.used)};
+}
+__device__ __forceinline__ Sums sum16(Sums v) {
+  v = add_moved<0xb1>(v);      // quad_perm 1,0,3,2
+  v = add_moved<0x4e>(v);      // quad_perm 2,3,0,1
+  v = add_moved<0x141>(v);     // row_half_mirror
+  return add_moved<0x140>(v);  // row_mirror
+}
+// Sums over a workgroup's 1024 threads, in every thread; the order is fixed.  sh: one per
+// wave, which nothing reads any more.
+constexpr int kSumWaves = 16;
+__device__ __forceinline__ Sums block_sum(Sums v, Sums* sh) {
+  v = sum16(v);
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  __syncthreads();
+  for (int d = 16; d < 64; d <<= 1)
+    v = v + Sums{__shfl_xor(v.balance, d), __shfl_xor(v.z, d), __shfl_xor(v.n, d), __shfl_xor(v.used, d)};
   if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-  __syncthreads();
-  T s = sh[0];
-#pragma unroll
-  for (int w = 1; w < TH / 64; ++w) s += sh[w];
-  return s;
+  lds_barrier();
+  return sum16(sh[threadIdx.x & (kSumWaves - 1)]);
+}
+__device__ __forceinline__ void write_losses(const BalanceArgs& a, const Sums& s) {
+  a.tokens[a.S] = s.n;
+  a.tokens[a.S + 1] = s.used;
+  a.loss[0] = (float)(s.used > 0 ? s.balance * a.E / s.used : 0.0);
+  a.loss[1] = (float)(s.n > 0 ? s.z / s.n : 0.0);
 }
 
-// One workgroup per kFinishCols experts and sequence: 16 lanes along the
-// experts, 16 along the sequence's chunks.
-constexpr int kFinishCols = 16, kFinishChunks = kThreadsB / kFinishCols;
-__global__ __launch_bounds__(kThreadsB) void k_balance_finish(BalanceArgs a) {
-  __shared__ double sp[kFinishChunks][kFinishCols];
-  __shared__ int32_t scn[kFinishChunks][kFinishCols];
-  __shared__ double sh[kThreadsB / 64];
-  __shared__ int32_t shi[kThreadsB / 64];
+// What workgroups leave for the last of them goes through the point that all dies share,
+// value by value: a fence would write back and empty a die's whole cache, for each
+// workgroup.
+template <class T> __device__ __forceinline__ void give(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class T> __device__ __forceinline__ T take(T* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// One workgroup of 1024 threads per COLS experts and sequence, the other lanes along the
+// sequence's chunks.  All it does is wait: for the offsets, the
+// slots, the others and what those left, each once.
+constexpr int kFinishThreads = 1024;
+static_assert(kFinishThreads == 64 * kSumWaves && kOneThreads == 64 * kSumWaves, "block_sum");
+template <int COLS>
+__global__ __launch_bounds__(kFinishThreads) void k_balance_finish(BalanceArgs a) {
+  constexpr int CHUNKS = kFinishThreads / COLS;
+  constexpr int W = kFinishThreads / 64;
+  __shared__ double sp[W][COLS];
+  __shared__ int32_t scn[W][COLS];
+  __shared__ Sums sh[W];
   __shared__ int32_t last;
-  const int nb = (a.E + kFinishCols - 1) / kFinishCols;
-  const int s = blockIdx.x / nb, b = blockIdx.x % nb;
-  const int col = threadIdx.x % kFinishCols, ch = threadIdx.x / kFinishCols, e = b * kFinishCols + col;
+  const int nb = (a.E + COLS - 1) / COLS;
+  const int s = blockIdx.x / nb, b = blockIdx.x % nb, w = threadIdx.x >> 6;
+  const int col = threadIdx.x % COLS, ch = threadIdx.x / COLS, e = b * COLS + col;
   int lo, hi;
-  seq_rows(a.off, s, a.T, lo, hi);
+  seq_rows(Offsets{a.off, nullptr}, s, a.T, lo, hi);
   const int c0 = lo / a.rows, c1 = hi > lo ? (hi - 1) / a.rows + 1 : c0;
   double p = 0.0;
   int32_t cnt = 0;
+  Sums mine = {};
+  for (int c = c0 + threadIdx.x; c < c1; c += kFinishThreads) {
+    mine.n += a.sum_n[c + s];
+    mine.z += (double)a.sum_z[c + s];
+  }
   if (e < a.E) {
-#pragma unroll 4
-    for (int c = c0 + ch; c < c1; c += kFinishChunks) {
+#pragma unroll 8
+    for (int c = c0 + ch; c < c1; c += CHUNKS) {
       const int64_t i = ((int64_t)c + s) * a.E + e;
       p += (double)a.sum_p[i];
       cnt += a.sum_c[i];
     }
   }
-  int32_t n = 0;
-  double z = 0.0;
-  for (int c = c0 + threadIdx.x; c < c1; c += kThreadsB) {
-    n += a.sum_n[c + s];
-    z += (double)a.sum_z[c + s];
-  }
-  sp[ch][col] = p;
-  scn[ch][col] = cnt;
-  n = block_sum<kThreadsB>(n, shi);
-  double term = 0.0;
-  if (threadIdx.x < kFinishCols && e < a.E) {
-    p = 0.0;
-    cnt = 0;
 #pragma unroll
-    for (int q = 0; q < kFinishChunks; ++q) {
+  for (int d = COLS; d < 64; d <<= 1) {
+    p += __shfl_xor(p, d);
+    cnt += __shfl_xor(cnt, d);
+  }
+  if ((threadIdx.x & 63) < COLS) {
+    sp[w][col] = p;
+    scn[w][col] = cnt;
+  }
+  const Sums all = block_sum(mine, sh);
+  if (threadIdx.x < COLS) {
+    p = sp[0][col];
+    cnt = scn[0][col];
+#pragma unroll
+    for (int q = 1; q < W; ++q) {
       p += sp[q][col];
       cnt += scn[q][col];
     }
-    a.counts[(int64_t)s * a.E + e] = cnt;
-    if (n > 0) term = (double)cnt * p / ((double)a.k * n * n);
-  }
-  term = block_sum<kThreadsB>(term, sh);
-  if (b == 0) {
-    z = block_sum<kThreadsB>(z, sh);
+    double term = 0.0;
+    if (e < a.E) {
+      a.counts[(int64_t)s * a.E + e] = cnt;
+      if (all.n > 0) term = (double)cnt * p / ((double)a.k * all.n * all.n);
+    }
+    term = sum16({term, 0.0, 0, 0}).balance;
+#pragma unroll
+    for (int d = 16; d < COLS; d <<= 1) term += __shfl_xor(term, d);
     if (threadIdx.x == 0) {
-      a.tokens[s] = n;
-      a.part_z[s] = z;
+      if (b == 0) {
+        give(&a.tokens[s], all.n);
+        give(&a.part_z[s], all.z);
+      }
+      give(&a.part[blockIdx.x], term);
+      __builtin_amdgcn_s_waitcnt(0);  // they have arrived, then this counts
+      last = __hip_atomic_fetch_add(a.arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
     }
   }
-  if (threadIdx.x == 0) {
-    a.part[blockIdx.x] = term;
-    __threadfence();
-    last = atomicAdd(a.arrived, 1u) == gridDim.x - 1;
-  }
-  __syncthreads();
+  lds_barrier();
   if (!last) return;
-  __threadfence();  // the other workgroups' sums, across the dies' caches
-  double balance = 0.0, zs = 0.0;
-  int32_t total = 0, used = 0;
-  for (int64_t i = threadIdx.x; i < (int64_t)gridDim.x; i += kThreadsB) balance += a.part[i];
-  for (int i = threadIdx.x; i < a.S; i += kThreadsB) {
-    const int32_t m = a.tokens[i];
-    zs += a.part_z[i];
-    total += m;
-    used += m > 0;
+  mine = {};
+  for (int64_t i = threadIdx.x; i < (int64_t)gridDim.x; i += kFinishThreads) mine.balance += take(&a.part[i]);
+  for (int i = threadIdx.x; i < a.S; i += kFinishThreads) {
+    const int32_t m = take(&a.tokens[i]);
+    mine.z += take(&a.part_z[i]);
+    mine.n += m;
+    mine.used += m > 0;
   }
-  balance = block_sum<kThreadsB>(balance, sh);
-  zs = block_sum<kThreadsB>(zs, sh);
-  total = block_sum<kThreadsB>(total, shi);
-  used = block_sum<kThreadsB>(used, shi);
-  if (threadIdx.x == 0) {
-    a.tokens[a.S] = total;
-    a.tokens[a.S + 1] = used;
-    a.loss[0] = (float)(used > 0 ? balance * a.E / used : 0.0);
-    a.loss[1] = (float)(total > 0 ? zs / total : 0.0);
-  }
+  mine = block_sum(mine, sh);
+  if (threadIdx.x == 0) write_losses(a, mine);
 }
 
 // All of it in one workgroup, one sequence after the other
@@ -356,46 +487,40 @@ template <int V, int L, int P>
 __global__ __launch_bounds__(kOneThreads) void k_balance_one(BalanceArgs a) {
   using Gt = Gathered<V, L, P, kOneThreads>;
   __shared__ Gt g;
-  __shared__ double sh[kOneThreads / 64];
-  __shared__ int32_t shi[kOneThreads / 64];
-  double balance = 0.0, zs = 0.0;
-  int total = 0, used = 0;
-  if (a.off) {
-    const int lo0 = min(max(a.off[0], 0), a.T), hi0 = min(max(a.off[a.S], 0), a.T);
-    for (int t = threadIdx.x; t < a.T; t += kOneThreads)
-      if (t < lo0 || t >= hi0) a.lse[t] = kNegInf;
-  }
-  for (int s = 0; s < a.S; ++s) {
-    int lo, hi;
-    seq_rows(a.off, s, a.T, lo, hi);
-    for (int e = threadIdx.x; e < a.E; e += kOneThreads) g.c[e] = 0;
-    __syncthreads();
-    gather_rows<V, L, P, kOneThreads>(a, lo, hi, g);
-    __syncthreads();
-    const int n = block_sum<kOneThreads>(threadIdx.x < Gt::GROUPS ? g.n[threadIdx.x] : 0, shi);
-    const double z = block_sum<kOneThreads>(threadIdx.x < Gt::GROUPS ? (double)g.z[threadIdx.x] : 0.0, sh);
-    double term = 0.0;
+  __shared__ Sums sh[kOneThreads / 64];
+  __shared__ int32_t lds[kOneSeqs + 1];
+  const Offsets off = load_offsets<kOneThreads>(a.off, a.S, lds);
+  Sums total = {};
+  int t0 = 0, t1 = a.T;
+  clip_rows<kOneThreads>(a, off, t0, t1);
+  gather_rows<V, L, P, kOneThreads>(a, off, t0, t1, g, [&](int s) {
+    Sums v = {};
+    if (threadIdx.x < Gt::GROUPS) {
+      v.n = g.n[threadIdx.x];
+      v.z = (double)g.z[threadIdx.x];
+    }
     for (int e = threadIdx.x; e < a.E; e += kOneThreads) {
       const int32_t cnt = g.c[e];
       a.counts[(int64_t)s * a.E + e] = cnt;
       double p = 0.0;
 #pragma unroll 8
       for (int q = 0; q < Gt::GROUPS; ++q) p += (double)g.p[q][e];
-      if (n > 0) term += (double)cnt * p / ((double)a.k * n * n);
+      v.balance += (double)cnt * p;
     }
-    term = block_sum<kOneThreads>(term, sh);
-    balance += term;
-    zs += z;
-    total += n;
-    used += n > 0;
-    if (threadIdx.x == 0) a.tokens[s] = n;
+    v = block_sum(v, sh);
+    if (threadIdx.x == 0) {
+      a.tokens[s] = v.n;
+      if (v.n > 0) total = total + Sums{v.balance / ((double)a.k * v.n * v.n), v.z, v.n, 1};
+    }
+  });
+  for (int s = 0; s < a.S; ++s) {  // without rows
+    int lo, hi;
+    seq_rows(off, s, a.T, lo, hi);
+    if (lo < hi) continue;
+    for (int e = threadIdx.x; e < a.E; e += kOneThreads) a.counts[(int64_t)s * a.E + e] = 0;
+    if (threadIdx.x == 0) a.tokens[s] = 0;
   }
-  if (threadIdx.x == 0) {
-    a.tokens[a.S] = total;
-    a.tokens[a.S + 1] = used;
-    a.loss[0] = (float)(used > 0 ? balance * a.E / used : 0.0);
-    a.loss[1] = (float)(total > 0 ? zs / total : 0.0);
-  }
+  if (threadIdx.x == 0) write_losses(a, total);
 }
 
 // --------------------------------------------------------------- backward --
@@ -416,21 +541,14 @@ struct BalanceGradArgs {
   int64_t dlogits_ld;
 };
 
-constexpr int kSeqLds = 1024;  // offsets that are searched in LDS
-
 // A group of L lanes takes `per` consecutive rows, so that the f of their sequence
 // stay in registers from row to row.  STREAM: the gradient and what is added to it
 // bypass the caches' retention.
 template <int V, int L, int P, bool STREAM>
 __global__ __launch_bounds__(kThreadsB) void k_balance_grad(BalanceGradArgs a) {
-  __shared__ int32_t soff[kSeqLds + 1];
+  __shared__ int32_t lds[kSeqLds + 1];
   const int c = threadIdx.x & (L - 1), grp = threadIdx.x / L;
-  const bool in_lds = a.off && a.S <= kSeqLds;
-  if (in_lds) {
-    for (int i = threadIdx.x; i <= a.S; i += kThreadsB) soff[i] = a.off[i];
-    __syncthreads();
-  }
-  auto begins = [&](int i) { return in_lds ? soff[i] : a.off[i]; };
+  const Offsets off = load_offsets<kThreadsB>(a.off, a.S, lds);
   const float d0 = a.dloss[0], d1 = a.dloss[1];
   const int total = a.tokens[a.S], used = a.tokens[a.S + 1];
   const float kz = total > 0 ? d1 * (2.0f / (float)total) : 0.f;
@@ -462,7 +580,7 @@ __global__ __launch_bounds__(kThreadsB) void k_balance_grad(BalanceGradArgs a) {
       for (int i = 0; i < P * V; ++i) ad.v[i] = 0.f;
     }
     if (l != kNegInf) {
-      const int s = !a.off ? 0 : seq >= 0 && t < begins(seq + 1) ? seq : seq_search(begins, a.S, t);
+      const int s = !a.off ? 0 : seq >= 0 && t < off(seq + 1) ? seq : seq_search(off, a.S, t);
       if (s != seq) {
         seq = s;
         const int n = a.tokens[s];
@@ -506,17 +624,26 @@ __global__ __launch_bounds__(kThreadsB) void k_balance_grad(BalanceGradArgs a) {
 // ------------------------------------------------------------------- host --
 
 constexpr int kMaxChunks = 512;
-// Tokens up to which the loss takes one launch of one workgroup, for up to
-// kOneSeqs sequences
-constexpr int kOneTokens = 128, kOneSeqs = 4;
 
-// Lanes per row and pieces per lane: calls F with them as compile-time constants.
-template <class F>
+// Lanes per row and pieces per lane: calls F with them as compile-time constants.  The loss
+// spends its time on what a row costs beside its values, reductions and a logarithm, so that
+// 16 lanes a row, four rows a wave, take it as far as their registers reach (65536 x 128: 16
+// lanes 12.4 us, 32 lanes 15.5); the gradient moves more bytes and wants more loads under way.
+template <bool LOSS, class F>
 void for_row_shape(bool vec, int E, F f) {
 #define MOE_ROW_SHAPE(V, L, P) \
   if (E <= V * L * P) return f(std::integral_constant<int, V>(), std::integral_constant<int, L>(), \
                                std::integral_constant<int, P>())
-  if (vec) {
+  if (vec && LOSS) {
+    MOE_ROW_SHAPE(4, 16, 1);
+    MOE_ROW_SHAPE(4, 16, 2);
+    MOE_ROW_SHAPE(4, 16, 3);
+    MOE_ROW_SHAPE(4, 16, 4);
+    MOE_ROW_SHAPE(4, 16, 6);
+    MOE_ROW_SHAPE(4, 32, 4);
+    MOE_ROW_SHAPE(4, 32, 6);
+    MOE_ROW_SHAPE(4, 32, 8);
+  } else if (vec) {
     MOE_ROW_SHAPE(4, 16, 1);
     MOE_ROW_SHAPE(4, 32, 1);
     MOE_ROW_SHAPE(4, 16, 3);
@@ -540,6 +667,7 @@ void for_row_shape(bool vec, int E, F f) {
 struct BalancePlan {
   bool one;
   int rows, chunks;
+  int cols, blocks;  // experts of a workgroup of the second launch, workgroups per sequence
   size_t sum_p, sum_c, sum_z, sum_n, part, part_z, arrived, total;
 };
 
@@ -547,9 +675,10 @@ BalancePlan balance_plan(int32_t T, int32_t E, int32_t S) {
   BalancePlan f = {};
   f.one = T <= kOneTokens && S <= kOneSeqs;
   if (f.one) return f;
-  // chunks of whole rounds of a workgroup's groups (16 of them at most)
   f.rows = (int)align_up(std::max<size_t>(((size_t)T + kMaxChunks - 1) / kMaxChunks, 1), 16);
   f.chunks = (T + f.rows - 1) / f.rows;
+  f.cols = f.chunks / S <= 64 ? 64 : 16;
+  f.blocks = (E + f.cols - 1) / f.cols;
   const size_t slots = (size_t)f.chunks + S;
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -561,7 +690,7 @@ BalancePlan balance_plan(int32_t T, int32_t E, int32_t S) {
   f.sum_c = take(slots * E * 4);
   f.sum_z = take(slots * 4);
   f.sum_n = take(slots * 4);
-  f.part = take((size_t)S * ((E + kFinishCols - 1) / kFinishCols) * 8);
+  f.part = take((size_t)S * f.blocks * 8);
   f.part_z = take((size_t)S * 8);
   f.arrived = take(4);
   f.total = o;
@@ -571,8 +700,10 @@ BalancePlan balance_plan(int32_t T, int32_t E, int32_t S) {
 bool sizes_valid(int32_t T, int32_t E, int32_t k, int32_t S) {
   return T >= 0 && E >= 1 && E <= kMaxExperts && k >= 1 && k <= E && S >= 1;
 }
+// (the second launch has S + S E / 64 workgroups of 1024 threads at most, and a launch fewer
+// than 2^32 threads)
 bool sizes_supported(int32_t T, int32_t E, int32_t k, int32_t S) {
-  return (int64_t)T * k <= (int64_t)1 << 30 && (int64_t)S * E <= (int64_t)1 << 30 && T <= 1 << 30;
+  return (int64_t)T * k <= (int64_t)1 << 30 && T <= 1 << 30 && S <= 1 << 20 && (int64_t)S * E <= (int64_t)1 << 27;
 }
 bool aligned_b(const void* p, uintptr_t n) { return (uintptr_t)p % n == 0; }
 bool matrix16(const float* p, int64_t ld, int32_t E) { return aligned_b(p, 16) && ld % 4 == 0 && E % 4 == 0; }
@@ -625,7 +756,7 @@ extern "C" moe_status_t moe_balance(const float* logits, int64_t logits_ld, cons
   a.lse = lse;
   const bool vec = T > 0 && matrix16(logits, logits_ld, E);
   if (f.one) {
-    for_row_shape(vec, E, [&](auto V, auto L, auto P) {
+    for_row_shape<true>(vec, E, [&](auto V, auto L, auto P) {
       k_balance_one<V.value, L.value, P.value><<<1, kOneThreads, 0, stream>>>(a);
     });
     return launched_b();
@@ -640,12 +771,14 @@ extern "C" moe_status_t moe_balance(const float* logits, int64_t logits_ld, cons
   a.part = (double*)(ws + f.part);
   a.part_z = (double*)(ws + f.part_z);
   a.arrived = (uint32_t*)(ws + f.arrived);
-  for_row_shape(vec, E, [&](auto V, auto L, auto P) {
+  for_row_shape<true>(vec, E, [&](auto V, auto L, auto P) {
     k_balance_rows<V.value, L.value, P.value><<<(unsigned)std::max(f.chunks, 1), kThreadsB, 0, stream>>>(a);
   });
   const moe_status_t r = launched_b();
   if (r != MOE_OK) return r;
-  k_balance_finish<<<(unsigned)((int64_t)S * ((E + kFinishCols - 1) / kFinishCols)), kThreadsB, 0, stream>>>(a);
+  const unsigned finish = (unsigned)S * (unsigned)f.blocks;
+  if (f.cols == 64) k_balance_finish<64><<<finish, kFinishThreads, 0, stream>>>(a);
+  else k_balance_finish<16><<<finish, kFinishThreads, 0, stream>>>(a);
   return launched_b();
 }
 
@@ -670,7 +803,7 @@ extern "C" moe_status_t moe_balance_backward(const float* dloss, const float* lo
   const bool vec = matrix16(logits, logits_ld, E) && matrix16(dlogits, dlogits_ld, E) &&
                    (!add || matrix16(add, add_ld, E));
   const bool stream_out = (int64_t)T * E * 4 >= kStreamGrad;
-  for_row_shape(vec, E, [&](auto V, auto L, auto P) {
+  for_row_shape<false>(vec, E, [&](auto V, auto L, auto P) {
     constexpr int G = kThreadsB / L.value;
     // rows per group: one where that leaves the chip room, more once there are
     // workgroups enough

@@ -224,12 +224,13 @@ moe_status_t moe_route_backward(const int32_t* topk_ids, const float* topk_w, co
  *   fp32 or NULL (0): another gradient of the logits, as moe_route_backward's; dlogits
  *   may be add itself.  counts, tokens, lse, seq_offsets and k are moe_balance's.
  *
- * Requires 0 <= T, 1 <= k <= E <= 1024, 1 <= S, T*k and S*E <= 2^30, addresses that are
- * multiples of the element size, and (moe_balance) moe_balance_workspace_bytes(T, E, S)
- * bytes, 256-byte aligned, whose contents need not be set; calls that may run at the same
- * time need one each.  T = 0 gives zeros.  Sums over a few dozen rows are held in fp32, sums
- * of those in fp64, in an order that sizes, row distances and addresses (multiples of 16
- * bytes or not) fix: the same call repeats bit for bit.
+ * Requires 0 <= T, 1 <= k <= E <= 1024, 1 <= S <= 2^20, T*k <= 2^30, S*E <= 2^27,
+ * addresses that are multiples of the element size, and (moe_balance)
+ * moe_balance_workspace_bytes(T, E, S) bytes, 256-byte aligned, whose contents need not be
+ * set; calls that may run at the same time need one each.  T = 0 gives zeros.  Sums over a
+ * few dozen rows are held in fp32, sums of those in fp64, in an order that sizes, row
+ * distances and addresses (multiples of 16 bytes or not) fix: the same call repeats bit for
+ * bit.
  */
 size_t moe_balance_workspace_bytes(int32_t T, int32_t E, int32_t S);
 moe_status_t moe_balance(const float* logits, int64_t logits_ld, const int32_t* topk_ids, const uint8_t* mask,

@@ -49,7 +49,8 @@ def test_valid_calls_reach_the_architecture_check(name):
     (n, c, s) for n in sorted(CALLS) for c, s in [
         (dict(T=-1), INVALID), (dict(E=0), INVALID), (dict(E=1025, ld=1025), INVALID), (dict(k=0), INVALID),
         (dict(k=9), INVALID), (dict(S=0), INVALID), (dict(S=-1), INVALID), (dict(offsets=None), INVALID),
-        (dict(T=1 << 30), UNSUPPORTED), (dict(S=1 << 28), UNSUPPORTED), (dict(ld=7), INVALID), (dict(add_ld=7), INVALID),
+        (dict(T=1 << 30), UNSUPPORTED), (dict(S=1 << 28), UNSUPPORTED), (dict(S=(1 << 20) + 1), UNSUPPORTED),
+        (dict(ld=7), INVALID), (dict(add_ld=7), INVALID),
         (dict(dlogits_ld=7), INVALID), (dict(dlogits_ld=-8), INVALID),
         *((dict([(p, None)]), INVALID) for p in ("logits", "ids", "loss", "counts", "tokens", "lse", "dloss", "dlogits")),
         *((dict([(p, A + 2)]), INVALID) for p in ("logits", "ids", "offsets", "loss", "counts", "tokens", "lse", "dloss",

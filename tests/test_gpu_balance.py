@@ -260,6 +260,31 @@ def test_results_repeat_and_calls_at_once_and_captured():
             assert all(torch.equal(a, b) for a, b in zip(other, want[1 - i]))
 
 
+def test_most_sequences():
+    """2^20 sequences of 3 tokens, more than are held in LDS, each with an expert of its own."""
+    from block_scaled_precision_amd import moe_mx as m
+    S, E = 1 << 20, 4
+    T = 3 * S
+    s = torch.arange(T, device="cuda") // 3
+    x = torch.zeros((T, E), device="cuda")
+    ids = (s % E).int()[:, None].contiguous()
+    so = 3 * torch.arange(S + 1, device="cuda", dtype=torch.int32)
+    loss, counts, tokens, lse = m.moe_balance(x, ids, seq_offsets=so)
+    want = 3 * torch.nn.functional.one_hot(torch.arange(S, device="cuda") % E, E).int()
+    assert torch.equal(counts, want) and (tokens[:S] == 3).all() and tokens[S:].tolist() == [T, S]
+    # every p is 1/4, the loss 1; half steps as the oracle counts them, with |x - max| = 0
+    top = np.log(4.0)
+    lse_steps = 28 + 2 * top + 2 * top
+    assert abs(loss[0].item() - 1) <= (28 + 80 + 2) * E32 and (lse - top).abs().max().item() <= lse_steps * E32
+    assert abs(loss[1].item() - top ** 2) <= (2 * top * lse_steps + 66 * top ** 2) * E32
+    g = m.moe_balance_backward(torch.tensor([1.0, 0.0]).cuda(), x, counts, tokens, lse, 1, seq_offsets=so)
+    # E / (S 3) p_e (f_e - 1/4): f is 1 for one expert
+    ref = E / T * 0.25 * ((want[s] > 0).double() - 0.25)
+    steps = top + lse_steps + 8
+    assert ((g.double() - ref).abs() <= E / T * 0.25 * ((steps + 8) * 1.25 + 0.25 * (steps + 24)) * E32
+            + 2 * ref.abs() * E32).all()
+
+
 def test_rows_past_32_bit_offsets():
     """Logits of more than 2^32 bytes: the last tokens of a long batch (one sequence of their
     own) against the same tokens alone."""
