@@ -19,14 +19,21 @@
 // Quotients by 2^s and the differences are exact in fp32, so codes do not depend on
 // how they are computed, but for the rotation's own sums, whose order is fixed.
 //
-// All of it is bound by memory.  Along rows, a lane takes 8 values and 4 neighbouring
-// lanes a block, so that loads and stores of a wave are contiguous; transposed, a
-// workgroup takes 256 rows by 64 columns, a thread the 32 rows of one block in
-// two columns (its loads are 128 contiguous bytes of a row per 32 lanes), and the
-// codes are regrouped in LDS into 128 contiguous bytes of each output row.
+// Along rows, a lane takes 8 values and 4 neighbouring lanes a block, so that loads and
+// stores of a wave are contiguous; transposed, a workgroup takes 256 rows by 64 columns, a
+// thread the 32 rows of one block in two columns (its loads are 128 contiguous bytes of a row
+// per 32 lanes), and the codes are regrouped in LDS into 128 contiguous bytes of each output
+// row.
+//
+// Measured (MI355X; bytes at 5 TB/s in brackets): rows 8192 x 7168 bf16, rotated, 44 us [29],
+// plain 31; values 8192 x 7168 back to bf16 23 [29, part of them from the last-level cache];
+// transposed 16 x 1536 x 4096 fp32 108 [90], 4021 x 2048 bf16 rotated 8 [4], 4021 x 4096 rotated
+// and rounded at random 23 [11].  Bound by memory, but for the last, whose 24 instructions a
+// value take 10 us, in a launch that is one round of workgroups: they load, then compute.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "mx_device.h"
@@ -49,15 +56,19 @@ __device__ __forceinline__ int exponent4(uint32_t amax) {
   return E == 0 ? -127 : max(E - 129 + ((amax & 0x7fffffu) > 0x400000u ? 1 : 0), -127);
 }
 
-// Code of q = v / 2^s, |q| <= 6, with random byte r
-__device__ __forceinline__ uint32_t random4(float q, uint32_t r) {
-  const float x = fabsf(q);
-  // steps of 1/2 up to 2, of 1 up to 4, of 2 up to 6: u counts them from the range's start
-  const float u = x < 2.f ? 2.f * x : x < 4.f ? x - 2.f : 0.5f * x - 2.f;
-  const float lo = floorf(u);
-  uint32_t c = (uint32_t)lo + (x < 2.f ? 0u : x < 4.f ? 4u : 6u);
-  c += (u - lo) * 256.f > (float)r + 0.5f ? 1u : 0u;
-  return c | (__float_as_uint(q) >> 31) << 3;
+// Code of q = v / 2^s, |q| <= 6, with the complement n of its random byte (r = 255 - n).
+// From 1 on, the code's exponent and mantissa bit are the first of the fp32 bits, and those
+// behind them, 22 of them, hold (x - lo) / (hi - lo): it is above (r + 1/2) / 256 = (2 r + 1)
+// 2^13 / 2^22 where the bits carry once 2^22 - 1 - (2 r + 1) 2^13 = n 2^14 + 2^13 - 1 is added.
+// Below 1 codes are 1/2 apart: (1 + x) / 2 has the same bits behind codes 0 and 1, x rounded up
+// to 2^-20 first, which passes no multiple of 2^-10 and reaches none from below: being above
+// (r + 1/2) / 512 stays as it was.  (13 instructions; with floors and selections 24, and
+// 4021 x 4096 rotated, transposed and rounded at random 26 us.)
+__device__ __forceinline__ uint32_t random4(float q, uint32_t n) {
+  const float x = fabsf(q), small = fmaf(ceilf(x * 0x1p20f), 0x1p-21f, 0.5f);
+  const uint32_t bits = __float_as_uint(x < 1.0f ? small : x) + (n << 14) + ((4u << 22) + 8191u);
+  // 252 + code, + 4: the code modulo 8, and the sign
+  return (bits >> 22 & 7u) | (__float_as_uint(q) >> 28 & 8u);
 }
 
 template <int CTRL> __device__ __forceinline__ float quad(float v) {
@@ -175,7 +186,7 @@ __global__ __launch_bounds__(kThreadsQ) void k_mx4_rows(RowsArgs a) {
     uint32_t w = 0;
     if constexpr (RANDOM) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w |= random4(x[i] * inv, (rnd[j][i / 4] >> (8 * (i % 4))) & 255u) << (4 * i);
+      for (int i = 0; i < 8; ++i) w |= random4(x[i] * inv, (~rnd[j][i / 4] >> (8 * (i % 4))) & 255u) << (4 * i);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] *= inv;
@@ -216,42 +227,55 @@ __global__ __launch_bounds__(kThreadsQ) void k_mx4_cols(ColsArgs a) {
   const int pc = threadIdx.x & 31, rb = threadIdx.x >> 5;
   const int c = tc * kTileC + 2 * pc, r0 = tr * kTileR + 32 * rb;
   const int64_t sbase = batch * a.rows * a.ld, rbase = batch * a.rows * a.cols;
-  float v[2][32];
-  [[maybe_unused]] uint32_t rnd[2][8];
+  // both columns as they come: bf16 in one word, fp32 in two; two rows' random bytes in one
+  uint32_t raw[BF16 ? 1 : 2][32];
+  [[maybe_unused]] uint32_t rnd[16];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) rnd[0][i] = rnd[1][i] = 0;
+  for (int i = 0; i < 16; ++i) rnd[i] = 0;
+  // A tile that lies inside as a whole (the same for all threads) takes its loads without a
+  // branch around each, so that all are under way at once.
+  auto load = [&](auto inside) {
+    constexpr bool IN = decltype(inside)::value;
+    const int64_t o0 = sbase + (int64_t)r0 * a.ld + c, ro0 = rbase + (int64_t)r0 * a.cols + c;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    v[0][i] = v[1][i] = 0.f;
-    if (r0 + i >= a.rows || c >= a.cols) continue;
-    const int64_t o = sbase + (int64_t)(r0 + i) * a.ld + c, ro = rbase + (int64_t)(r0 + i) * a.cols + c;
-    const bool two = VEC || c + 1 < a.cols;
-    if constexpr (BF16) {
-      const uint16_t* p = (const uint16_t*)a.src + o;
-      const uint32_t w = VEC ? *(const uint32_t*)p : p[0] | (two ? (uint32_t)p[1] << 16 : 0u);
-      v[0][i] = __uint_as_float(w << 16);
-      v[1][i] = __uint_as_float(w & 0xffff0000u);
-    } else {
-      const float* p = (const float*)a.src + o;
-      if constexpr (VEC) {
-        const float2 w = *(const float2*)p;
-        v[0][i] = w.x;
-        v[1][i] = w.y;
+    for (int i = 0; i < 32; ++i) {
+      raw[0][i] = 0;
+      if constexpr (!BF16) raw[1][i] = 0;
+      if (!IN && (r0 + i >= a.rows || c >= a.cols)) continue;
+      const int64_t o = o0 + i * a.ld, ro = ro0 + (int64_t)i * a.cols;
+      const bool two = IN || VEC || c + 1 < a.cols;
+      if constexpr (BF16) {
+        const uint16_t* p = (const uint16_t*)a.src + o;
+        raw[0][i] = VEC ? *(const uint32_t*)p : p[0] | (two ? (uint32_t)p[1] << 16 : 0u);
       } else {
-        v[0][i] = p[0];
-        if (two) v[1][i] = p[1];
+        const uint32_t* p = (const uint32_t*)a.src + o;
+        if constexpr (VEC) {
+          const uint2 w = *(const uint2*)p;
+          raw[0][i] = w.x;
+          raw[1][i] = w.y;
+        } else {
+          raw[0][i] = p[0];
+          if (two) raw[1][i] = p[1];
+        }
+      }
+      if constexpr (RANDOM) {
+        const uint8_t* p = a.random + ro;
+        const uint32_t w = VEC ? *(const uint16_t*)p : p[0] | (two ? (uint32_t)p[1] << 8 : 0u);
+        rnd[i / 2] |= w << (16 * (i % 2));
       }
     }
-    if constexpr (RANDOM) {
-      const uint8_t* p = a.random + ro;
-      const uint32_t w = VEC ? *(const uint16_t*)p : p[0] | (two ? (uint32_t)p[1] << 8 : 0u);
-      rnd[0][i / 4] |= (w & 255u) << (8 * (i % 4));
-      rnd[1][i / 4] |= (w >> 8) << (8 * (i % 4));
-    }
-  }
-#pragma unroll
+  };
+  if ((tr + 1) * kTileR <= a.rows && (tc + 1) * kTileC <= a.cols) load(std::true_type());
+  else load(std::false_type());
+  // (one body for both columns: in one round of tiles a CU waits for its code, too; 4021 x 2048
+  // bf16 with two bodies 14 us, with one 8)
+#pragma unroll 1
   for (int h = 0; h < 2; ++h) {
-    float(&x)[32] = v[h];
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if constexpr (BF16) x[i] = __uint_as_float(raw[0][i] << (16 - 16 * h) & 0xffff0000u);
+      else x[i] = __uint_as_float(h ? raw[1][i] : raw[0][i]);
     if constexpr (ROTATE) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) x[i] *= a.signs[i];
@@ -282,7 +306,7 @@ __global__ __launch_bounds__(kThreadsQ) void k_mx4_cols(ColsArgs a) {
         w[g] = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          w[g] |= random4(y[i], (rnd[h][2 * g + i / 4] >> (8 * (i % 4))) & 255u) << (4 * i);
+          w[g] |= random4(y[i], ~rnd[4 * g + i / 2] >> (16 * (i % 2) + 8 * h) & 255u) << (4 * i);
       } else {
         w[g] = e2m1_codes(y);
       }
