@@ -22,7 +22,8 @@
 // the MFMA takes from lane g the scale of block g.  (A launch to quantize costs
 // 2.5 us.)
 //
-// mx4_linear: E2M1 activations, as codes or quantized on the way as mx4_quantize does.
+// mx4_linear: E2M1 activations, as codes or quantized on the way as mx4_quantize does: by the
+// lanes that multiply them, or for very few rows once, into LDS (launch_mx4_few).
 // Lane g of a row then holds block g of a chunk as a whole, as it does of the weights.
 #include <hip/hip_runtime.h>
 
@@ -39,11 +40,12 @@ typedef __bf16 v32bf __attribute__((ext_vector_type(32)));
 typedef uint32_t u32x4_a8 __attribute__((ext_vector_type(4), aligned(8)));
 
 constexpr int kAhead = 4;  // chunks in flight per wave
+constexpr int kAheadRows = 8;  // those without activations (kRows4)
 constexpr int W = 8;       // waves
 
 // activations: bf16 as given, E4M3 codes with scales, bf16 quantized here; E2M1 codes with
-// scales, bf16 quantized to E2M1 here
-enum Act { kBf16 = 0, kMx = 1, kQuant = 2, kMx4 = 3, kQuant4 = 4 };
+// scales, bf16 quantized to E2M1 here, by the lanes that multiply it or, in LDS, by all
+enum Act { kBf16 = 0, kMx = 1, kQuant = 2, kMx4 = 3, kQuant4 = 4, kRows4 = 5 };
 
 struct Chunk {
   uint4 a[4];         // kBf16, kQuant4: 32 values; kQuant: 2 x 16 values; kMx: a[0], a[1] codes; kMx4: a[0]
@@ -66,6 +68,7 @@ __device__ __forceinline__ void load_chunk(Chunk& f, const uint8_t* arow, const 
     f.b[0] = x[0]; f.b[1] = x[1]; f.b[2] = x[2]; f.b[3] = x[3]; f.b[4] = y.x; f.b[5] = y.y;
   }
   f.bs = *(const uint32_t*)(bsrow + 4 * c);
+  if (ACT == kRows4) return;
   if (arow == nullptr) return;  // a row past the tile: zeros, set once
   if (ACT == kMx4) {
     f.a[0] = *(const uint4*)(arow + 64 * (int64_t)c + 16 * g);
@@ -104,6 +107,17 @@ __device__ __forceinline__ uint32_t quant8_e2m1(const uint4& v, float inv) {
   for (int i = 0; i < 8; ++i) q[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) * inv;
   return e2m1_codes(q);
 }
+// largest magnitude (fp32 bits) of 8 bf16 values
+__device__ __forceinline__ uint32_t amax8(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) m = max(m, max((w[q] << 16) & 0x7fffffffu, w[q] & 0x7fff0000u));
+  return m;
+}
+template <int CTRL> __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true));
+}
 // largest magnitude (fp32 bits) of 16 bf16 values
 __device__ __forceinline__ uint32_t amax16(const uint4& lo, const uint4& hi) {
   const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -141,7 +155,7 @@ __device__ __forceinline__ void mul_chunk(v4f& acc, const Chunk& f, int g, int r
     }
     return;
   }
-  if (ACT == kMx4 || ACT == kQuant4) {
+  if (ACT == kMx4 || ACT == kQuant4 || ACT == kRows4) {
     uint4 q = f.a[0];
     int asc = (int)((f.as >> (8 * g)) & 0xffu);
     if (ACT == kQuant4) {
@@ -229,6 +243,8 @@ __device__ __forceinline__ Tile find_tile(const int32_t* offsets, int groups, in
 template <int ACT, int WF>
 __global__ __launch_bounds__(64 * W) void k_linear_few(FcArgs p) {
   __shared__ float part[W][16][kFewCols + 4];
+  extern __shared__ __attribute__((aligned(16))) uint8_t rows4[];  // kRows4: codes [rows, K / 2], scales [rows, K / 32]
+  constexpr int A = ACT == kRows4 ? kAheadRows : kAhead;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, r = lane & 15;
   const int nch = blockIdx.x % p.nchunks, ti = blockIdx.x / p.nchunks;
   const int N = p.N, K = p.K, col0 = nch * kFewCols;
@@ -264,24 +280,57 @@ __global__ __launch_bounds__(64 * W) void k_linear_few(FcArgs p) {
   const uint8_t* brow = p.w + (int64_t)t.expert * p.w_estride + wrow * ((int64_t)K * Fmt<WF>::BITS / 8);
   const uint8_t* bsrow = p.w_scale + (int64_t)t.expert * p.ws_estride + wrow * (K / 32);
   v4f acc = {0.f, 0.f, 0.f, 0.f};
-  Chunk f[kAhead];
+  Chunk f[A];
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
+  for (int u = 0; u < A; ++u) {
     f[u].as = 0x7f7f7f7fu;
 #pragma unroll
     for (int q = 0; q < 4; ++q) f[u].a[q] = make_uint4(0, 0, 0, 0);
+  }
+  // kRows4: pieces of 8 values of the tile's rows, one behind the other; the first two of a
+  // thread are requested before the weights, which they then need not wait for
+  const uint4* asrc = (const uint4*)p.a + (int64_t)t.p0 * (K / 8);
+  const int pieces = t.rows * (K / 8);
+  uint4 x[2] = {};
+  if (ACT == kRows4) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if ((int)threadIdx.x + 64 * W * u < pieces) x[u] = asrc[threadIdx.x + 64 * W * u];
   }
   // the wave's chunks: pairs w, w + W, ... of neighbouring chunks
   const int nchunk = K / 128;
   auto chunk = [&](int i) { return 2 * (w + W * (i >> 1)) + (i & 1); };
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u)
+  for (int u = 0; u < A; ++u)
     if (chunk(u) < nchunk) load_chunk<ACT, WF>(f[u], arow, asrow, brow, bsrow, chunk(u), g);
-  for (int i = 0; chunk(i) < nchunk; i += kAhead) {
+  uint8_t* scales4 = rows4 + t.rows * (K / 2);
+  if (ACT == kRows4) {
+    // (4 neighbouring lanes hold a block, and go on together: K % 128 == 0)
+    auto quantize = [&](int i, const uint4& v) {
+      const int s = block_exponent<1>(quad_max<0x4e>(quad_max<0xb1>(amax8(v))));
+      ((uint32_t*)rows4)[i] = quant8_e2m1(v, exp2_neg(s));
+      if ((i & 3) == 0) scales4[i >> 2] = (uint8_t)(s + 127);
+    };
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (chunk(i + u) < nchunk) mul_chunk<ACT, WF>(acc, f[u], g, r);
-      if (chunk(i + u + kAhead) < nchunk) load_chunk<ACT, WF>(f[u], arow, asrow, brow, bsrow, chunk(i + u + kAhead), g);
+    for (int u = 0; u < 2; ++u)
+      if ((int)threadIdx.x + 64 * W * u < pieces) quantize(threadIdx.x + 64 * W * u, x[u]);
+    for (int i = threadIdx.x + 2 * 64 * W; i < pieces; i += 64 * W) quantize(i, asrc[i]);
+    asm volatile("" ::: "memory");  // every piece is written
+    wait_lgkm0();
+    barrier();
+  }
+  for (int i = 0; chunk(i) < nchunk; i += A) {
+#pragma unroll
+    for (int u = 0; u < A; ++u) {
+      const int c = chunk(i + u);
+      if (c < nchunk) {
+        if (ACT == kRows4 && r < t.rows) {
+          f[u].a[0] = *(const uint4*)(rows4 + r * (K / 2) + 64 * c + 16 * g);
+          f[u].as = *(const uint32_t*)(scales4 + r * (K / 32) + 4 * c);
+        }
+        mul_chunk<ACT, WF>(acc, f[u], g, r);
+      }
+      if (chunk(i + u + A) < nchunk) load_chunk<ACT, WF>(f[u], arow, asrow, brow, bsrow, chunk(i + u + A), g);
     }
   }
   // weights first: the lane holds row r, columns 4g .. 4g + 3
@@ -303,16 +352,25 @@ __global__ __launch_bounds__(64 * W) void k_linear_few(FcArgs p) {
 }
 
 template <int ACT, int WF>
-void launch_few_t(const FcArgs& p, int ntiles, hipStream_t st) {
-  k_linear_few<ACT, WF><<<(unsigned)((int64_t)ntiles * p.nchunks), 64 * W, 0, st>>>(p);
+void launch_few_t(const FcArgs& p, int ntiles, hipStream_t st, unsigned lds = 0) {
+  k_linear_few<ACT, WF><<<(unsigned)((int64_t)ntiles * p.nchunks), 64 * W, lds, st>>>(p);
 }
+
+// Rows of bf16 up to which a workgroup quantizes them into LDS, once, in place of every lane what
+// it multiplies, as if there were 16 of them; and the LDS that this may take.  N = 4096, K =
+// 7168: one row 10.3 us -> 7.2 (from codes the same), 8 rows 12.6 -> 11.1, but 16 rows 14.4 -> 15.4;
+// 16 rows of 6 groups, 1024 x 2048, a few in each tile: 10.6 -> 6.8.
+constexpr int kRowsDense = 8, kRowsGrouped = 16, kRowsLds = 40 * 1024;
 
 }  // namespace
 
 hipError_t launch_mx4_few(const FcArgs& p, bool quant, hipStream_t st) {
   const int ntiles = p.dense_rows > 0 ? (p.dense_rows + 15) / 16 : p.max_tiles;
   if (ntiles == 0) return hipSuccess;
-  if (quant) launch_few_t<kQuant4, 1>(p, ntiles, st);
+  const int64_t rows = p.dense_rows > 0 ? p.dense_rows : p.group_rows, lds = rows * (p.K / 2 + p.K / 32);
+  const int most = p.dense_rows > 0 ? kRowsDense : kRowsGrouped;
+  if (quant && rows <= most && lds <= kRowsLds) launch_few_t<kRows4, 1>(p, ntiles, st, (unsigned)lds);
+  else if (quant) launch_few_t<kQuant4, 1>(p, ntiles, st);
   else launch_few_t<kMx4, 1>(p, ntiles, st);
   return hipGetLastError();
 }

@@ -40,9 +40,9 @@ inline mx_linear_problem_t as_mxfp8(const mx4_linear_problem_t& p) {
 // The smallest of the estimated times in microseconds, as linear_kind chooses
 // (linear_plan.h).  Over 82 measured shapes (1 to 76800 rows, dense and 8 to 384 groups) the
 // choice costs 0.8 % more than the best kernel each time, 19 % at most.
-//   few rows in place (a step of 1024 K): from codes 0.45 to 0.65, from bf16 0.68 to 1.23; twice
-//     that with groups (N = 4096, K = 7168: 1 row 7.9, 16 rows 9.5, 32 rows 15.5; from bf16
-//     9.7, 14.1, 25.7)
+//   few rows in place (a step of 1024 K): from codes 0.45 to 0.65, from bf16 to 0.75 up to 8 rows
+//     and to 1.23 from there on; twice that with groups (N = 4096, K = 7168: 1 row 7.2, 16 rows
+//     9.5, 32 rows 15.7; from bf16 7.2, 14.4, 25.7)
 //   tiles of 64, 128 and 256 rows: a stage of 256 K 0.6, 0.85 and 1.3 where few workgroups
 //     have an item and 0.76, 1.12 and 2.05 where all do, 15 and 8 % more for the smaller ones
 //     with groups, which share no weights; 1.4, 3.3 and 9 an item beside its stages.  N = 4096,
@@ -92,7 +92,8 @@ inline Mx4Plan mx4_plan(const mx4_linear_problem_t& p, bool has_a_scale) {
   const int64_t blocks = (p.N + kFewCols - 1) / kFewCols;
   if (most_tiles(q, kStreamRows) * blocks <= 1 << 20) {
     const double rows = std::min(c.per, 16.0) / 16.0;
-    const double t = (p.groups > 0 ? 2.0 : 1.0) * (has_a_scale ? 0.45 + 0.2 * rows : 0.68 + 0.55 * rows);
+    const double a = has_a_scale ? 0.2 * rows : p.M <= 8 ? 0.6 * rows : 0.23 + 0.55 * rows;
+    const double t = (p.groups > 0 ? 2.0 : 1.0) * (0.45 + a);
     const double steps = p.K <= 1024 ? 1.0 : std::ceil(p.K / 2048.0) * 2.0;
     take(Fc4::kFew, kStreamRows, c.time(16, 16, steps, t));
   }

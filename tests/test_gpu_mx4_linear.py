@@ -41,6 +41,7 @@ def _offsets(M, G, seed):
 # column blocks; tests/test_mx4_plan.py holds them against the choice
 CASES = [
     ("few", 16, 1, 8, 128, 0), ("few", 16, 1, 4096, 7168, 0), ("few", 16, 5, 264, 384, 0), ("few", 16, 16, 1032, 1152, 0),
+    ("few", 16, 8, 520, 4736, 0), ("few", 16, 8, 136, 10240, 0), ("few", 16, 2, 72, 16384, 0), ("few", 16, 16, 264, 2048, 6),
     ("few", 16, 33, 520, 640, 6), ("few", 16, 3, 72, 128, 2), ("few", 16, 20, 136, 896, 40), ("few", 16, 100, 40, 256, 1),
     ("tile", 64, 300, 2056, 512, 0), ("tile", 64, 700, 1032, 1152, 0), ("tile", 64, 4200, 2056, 640, 0),
     ("tile", 64, 700, 4104, 1152, 1), ("tile", 64, 4200, 1032, 512, 40), ("tile", 64, 1500, 1032, 2048, 6),
