@@ -464,7 +464,7 @@ __global__ __launch_bounds__(kFinishThreads) void k_balance_finish(BalanceArgs a
         give(&a.part_z[s], all.z);
       }
       give(&a.part[blockIdx.x], term);
-      __builtin_amdgcn_s_waitcnt(0);  // they have arrived, then this counts
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // they have arrived, then this counts
       last = __hip_atomic_fetch_add(a.arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
     }
   }

@@ -1,6 +1,43 @@
 // mx4_linear with many rows: tiles of 64 MSUB rows by 256 columns on the block-scaled
 // MFMA v_mfma_scale_f32_32x32x64_f8f6f4 with E2M1 on both sides (mxfp6-sm120 page,
 // "Execution model"; TokenSpeed SiTU page, "Supported contract": MxE2m1).
+//
+//   v[m, n] = sum_b 2^(sa[m, b] + sw[n, b] - 254) sum_{k in block b} a[m, k] w[n, k] + bias[n]
+//   out[m, n] = bf16(fn(v) mul[m, n] + residual[m, n])
+// The instruction applies both scales of a block of 32 to 64 k at a time and adds in fp32;
+// accumulators stay in registers from the first k to the epilogue.
+//
+// Bound.  With E2M1 on both sides the instruction takes 32 cycles, half of E4M3's, and moves
+// half the bytes, so that everything around it counts twice.  On values of any size registers
+// alone reach 5.8 to 6.2 PFLOP/s (the clock gives way to power; zeros reach 9.7).  A wave that
+// has its SIMD to itself pays 4.5 cycles for each instruction of its own beside its MFMAs; LDS
+// gives 128 bytes a cycle, of which copies and fragments take 3/4 of a 256-row tile's time and
+// all of a 128-row tile's.  What each choice is for:
+// - Four waves, one per SIMD, of 32 MSUB x 128 each: the largest pieces of the accumulator, so
+//   the fewest fragments (6 reads for 8 MFMAs with 128 rows, 8 for 16 with 256).  Eight waves
+//   spill (8192^3: 316 us for 304); two workgroups a CU of 128 rows, 128 k a stage, to have one's
+//   epilogue beside the other's products, fetch every scale line four times as often and rows
+//   by 64 bytes (469 us for 319).
+// - Stages of 256 k, rows of 128 bytes, a cache line; of 128 k: 279 us for 255 (256 rows).
+// - Two slots of stages, three where they fit (64 and 128 rows).  Scales travel in groups of
+//   two stages, 16 bytes a row; three slots of 128 rows leave room for two groups, which are
+//   enough where every item has an even number of stages (8192^3: 319 us -> 310; 65536 rows of
+//   128 experts, 1536 x 4096: 365 -> 338).
+// - Copies go from memory to LDS without registers, a stage's spread between the MFMAs of two
+//   steps; fragments are read a step ahead.  No branch stands among MFMAs: it would end the
+//   block that the compiler can interleave.
+// - Workgroups are persistent and walk patches of 4 row tiles by 8 column blocks per XCD, so
+//   that 32 of them share what they read in its L2 (copies alone, 8192^3: 239 us -> 214).
+// - The next item's copies are under way during an epilogue, and biases come with them: loaded
+//   in the epilogue they wait for every copy before them (512 rows of 384 experts, 7168 x 2048:
+//   474 us -> 377).
+//
+// Measured (MI355X, from codes): 8192 x 8192 x 8192 262 us with 256 rows, 4.2 PFLOP/s, 128 rows
+// 310, 64 rows 415; 8192 x 4096 x 7168 121, 143, 183; 65536 rows of 128 experts, 1536 x 4096, 289,
+// 307, 420, with SiLU and a second factor 367 (128 rows).  A 256-row K loop takes 2900 cycles a
+// stage where its MFMAs take 2050.  What is left: epilogues that the next item's products do
+// not overlap (about 4 us of a 128-row item's 25), the padding of a group's last tile, and a
+// launch's last round.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -26,7 +63,10 @@ template <int MSUB, int SLOTS_> struct Lay4 {
   static constexpr int TM = 64 * MSUB;
   static constexpr int NBUF = SLOTS_;
   static constexpr int SA = TM * ROW, SB = TN * ROW, STAGE = SA + SB;
-  static constexpr int GA = TM * 16, GROUP = GA + TN * 16;  // scales of two stages
+  // Scales travel in groups of two stages, 16 bytes a row.  While a stage is begun, the groups
+  // of the NBUF - 1 before it are in use: with three slots, of two groups if every item's
+  // stages pair up, else of up to three (64 rows have room for four).
+  static constexpr int GA = TM * 16, GROUP = GA + TN * 16;
   static constexpr int GBUFS = MSUB == 1 ? 4 : 2;
   static constexpr int SCALES = NBUF * STAGE;
   // Biases of the items that have a stage under way (K >= 512: two stages an item), 256
@@ -565,7 +605,7 @@ static void launch_fp4_t(const FcArgs& p, int grid, hipStream_t st) {
 hipError_t launch_linear_fp4(const FcArgs& p, int rows, int grid, hipStream_t st) {
   if (grid < 8) grid = 8;
   grid &= ~7;
-  const bool pairs = (p.K + 255) / 256 % 2 == 0;
+  const bool pairs = (p.K + 255) / 256 % 2 == 0;  // (Lay4: three slots of 128 rows)
   if (rows == 256) launch_fp4_t<4, 2>(p, grid, st);
   else if (rows == 128 && pairs) launch_fp4_t<2, 3>(p, grid, st);
   else if (rows == 128) launch_fp4_t<2, 2>(p, grid, st);

@@ -18,6 +18,10 @@ rather than to be fast:
                         FC2, routing-weighted combine and the shared expert.
 * ``oracle.dispatch`` -- rows sorted by expert and back, with their gradients,
                         and the gradient of the routing weights.
+* ``oracle.balance``  -- the router's balance loss, z-loss and counts per sequence, and
+                        their gradient.
+* ``oracle.mx4``     -- MXFP4 operands (transposed, rotated, stochastically rounded) and
+                        their product.
 
 Pins (tests/test_oracle_*.py) tie each function to something other than
 itself: hand-listed decode values, torch's own float8 codecs, brute-force
