@@ -623,7 +623,9 @@ __global__ __launch_bounds__(kThreadsB) void k_balance_grad(BalanceGradArgs a) {
 
 // ------------------------------------------------------------------- host --
 
-constexpr int kMaxChunks = 512;
+// Chunks of a loss of up to kChunkRows rows each; longer ones have more chunks, so that no sum
+// in fp32 has more than 64 rows (of 4 groups, at 64 lanes a row) and as many groups.
+constexpr int kMaxChunks = 512, kChunkRows = 256;
 
 // Lanes per row and pieces per lane: calls F with them as compile-time constants.  The loss
 // spends its time on what a row costs beside its values, reductions and a logarithm, so that
@@ -675,7 +677,7 @@ BalancePlan balance_plan(int32_t T, int32_t E, int32_t S) {
   BalancePlan f = {};
   f.one = T <= kOneTokens && S <= kOneSeqs;
   if (f.one) return f;
-  f.rows = (int)align_up(std::max<size_t>(((size_t)T + kMaxChunks - 1) / kMaxChunks, 1), 16);
+  f.rows = (int)std::min<size_t>(align_up(std::max<size_t>(((size_t)T + kMaxChunks - 1) / kMaxChunks, 1), 16), kChunkRows);
   f.chunks = (T + f.rows - 1) / f.rows;
   f.cols = f.chunks / S <= 64 ? 64 : 16;
   f.blocks = (E + f.cols - 1) / f.cols;

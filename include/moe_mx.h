@@ -227,10 +227,10 @@ moe_status_t moe_route_backward(const int32_t* topk_ids, const float* topk_w, co
  * Requires 0 <= T, 1 <= k <= E <= 1024, 1 <= S <= 2^20, T*k <= 2^30, S*E <= 2^27,
  * addresses that are multiples of the element size, and (moe_balance)
  * moe_balance_workspace_bytes(T, E, S) bytes, 256-byte aligned, whose contents need not be
- * set; calls that may run at the same time need one each.  T = 0 gives zeros.  Sums over a
- * few dozen rows are held in fp32, sums of those in fp64, in an order that sizes, row
- * distances and addresses (multiples of 16 bytes or not) fix: the same call repeats bit for
- * bit.
+ * set; calls that may run at the same time need one each.  T = 0 gives zeros.  Sums over up
+ * to 64 rows and up to 64 of those are held in fp32, the rest in fp64, in an order that
+ * sizes, row distances and addresses (multiples of 16 bytes or not) fix: the same call
+ * repeats bit for bit.
  */
 size_t moe_balance_workspace_bytes(int32_t T, int32_t E, int32_t S);
 moe_status_t moe_balance(const float* logits, int64_t logits_ld, const int32_t* topk_ids, const uint8_t* mask,

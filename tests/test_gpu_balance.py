@@ -260,6 +260,15 @@ def test_results_repeat_and_calls_at_once_and_captured():
             assert all(torch.equal(a, b) for a, b in zip(other, want[1 - i]))
 
 
+def test_more_chunks_than_a_short_batch_has():
+    """Rows past 512 chunks of 256: the sums in fp32 stay as short as the oracle's bound takes
+    them to be."""
+    T, E, k, S = 150001, 5, 2, 3
+    print_flush(f"moe_balance T={T}")
+    logits, ids, mask, off = _case(T, E, k, S, 31, masked=True)
+    _check(logits, ids, mask, off, S)
+
+
 def test_most_sequences():
     """2^20 sequences of 3 tokens, more than are held in LDS, each with an expert of its own."""
     from block_scaled_precision_amd import moe_mx as m
