@@ -286,41 +286,15 @@ __device__ __forceinline__ void finish(v16f (&acc)[MSUB][4], const Item4& it, in
   };
   const auto out = buffer(e.out), mul = buffer(e.mul), res = buffer(e.residual);
   const bool has_mul = e.mul != nullptr;
-  float bias[2][4][8];
-  if constexpr (BIAS) {
-    const int c = col % TN;
-    auto each_bias = [&](auto f) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f(bias[j >> 2][j & 3], c + 16 * j);
-    };
-    if (e.bias_kind == kBiasF32 || e.bias_kind == kBiasF32Any) {
-      each_bias([&](float (&b)[8], int i) {
-        *(float4*)b = *(const float4*)(biases + 4 * i);
-        *(float4*)(b + 4) = *(const float4*)(biases + 4 * i + 16);
-      });
-    } else if (e.bias_kind == kBiasBf16) {
-      each_bias([&](float (&b)[8], int i) {
-        const uint4 x = *(const uint4*)(biases + 2 * i);
-        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) b[k] = __uint_as_float(k & 1 ? v[k / 2] & 0xffff0000u : v[k / 2] << 16);
-      });
-    } else {
-      const uint8_t* first = biases + ((uint64_t)e.bias & 2);
-      each_bias([&](float (&b)[8], int i) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) b[k] = __uint_as_float((uint32_t) * (const uint16_t*)(first + 2 * (i + k)) << 16);
-      });
-    }
-  }
   const int rows = it.rows - 32 * wm - l32, cols = N - col;  // of this lane's first row and column on
   const int first = (int)(2 * ((uint32_t)(32 * wm + l32) * (uint32_t)N + col));
   auto at = [&](int h, int m, int q) {
     const int side = 64 * h + 16 * q < cols ? 0 : (int)kOutside;
     return ((64 * m < rows ? first + 128 * h + m * (128 * N) : (int)kOutside) | side) + 32 * q;
   };
-  // what a part takes in goes out AHEAD parts before it
-  constexpr int AHEAD = MSUB <= 2 ? 2 * MSUB : 1;
+  // what a part takes in goes out AHEAD parts before it: all of it with up to 128 rows, whose
+  // registers have room, two with 256 (8192^3 with a residual: one 314 us, two 296)
+  constexpr int AHEAD = MSUB <= 2 ? 2 * MSUB : 2;
   u32x4 nm[AHEAD][4], nr[AHEAD][4];
   auto request = [&](int slot, int h, int m) {
 #pragma unroll
@@ -329,13 +303,12 @@ __device__ __forceinline__ void finish(v16f (&acc)[MSUB][4], const Item4& it, in
       nr[slot][q] = __builtin_amdgcn_raw_buffer_load_b128(res, at(h, m, q), 0, 0);
     }
   };
-  if constexpr (IN && AHEAD > 1) {
+  if constexpr (IN) {
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) request(j, j / MSUB, j % MSUB);
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    if constexpr (IN && AHEAD == 1) request(0, h, 0);
     auto part = [&](int m, int slot) {
       float v[4][8];
       each(std::make_integer_sequence<int, MSUB>(), [&](auto M) {
@@ -348,10 +321,33 @@ __device__ __forceinline__ void finish(v16f (&acc)[MSUB][4], const Item4& it, in
         }
       });
       if constexpr (BIAS) {
+        const int c = col % TN + 64 * h;
+        if (e.bias_kind == kBiasF32 || e.bias_kind == kBiasF32Any) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+          for (int q = 0; q < 4; ++q) {
+            float b[8];
+            *(float4*)b = *(const float4*)(biases + 4 * (c + 16 * q));
+            *(float4*)(b + 4) = *(const float4*)(biases + 4 * (c + 16 * q) + 16);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[q][i] += bias[h][q][i];
+            for (int i = 0; i < 8; ++i) v[q][i] += b[i];
+          }
+        } else if (e.bias_kind == kBiasBf16) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint4 x = *(const uint4*)(biases + 2 * (c + 16 * q));
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              v[q][i] += __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+          }
+        } else {
+          const uint8_t* first = biases + ((uint64_t)e.bias & 2);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              v[q][i] += __uint_as_float((uint32_t) * (const uint16_t*)(first + 2 * (c + 16 * q + i)) << 16);
+        }
       }
       if (e.fn != MX_FN_NONE) {
 #pragma unroll
@@ -366,7 +362,11 @@ __device__ __forceinline__ void finish(v16f (&acc)[MSUB][4], const Item4& it, in
             v[q][i] *= has_mul ? __uint_as_float(i & 1 ? x & 0xffff0000u : x << 16) : 1.0f;
             v[q][i] += __uint_as_float(i & 1 ? y & 0xffff0000u : y << 16);
           }
-        if constexpr (AHEAD == 1) request(0, h, min(m + 1, MSUB - 1));
+        // (h, m) two parts on; behind the last one, that one again
+        if constexpr (MSUB > AHEAD) {
+          const int next = m + AHEAD < MSUB ? m + AHEAD : h ? MSUB - 1 : m + AHEAD - MSUB;
+          request(slot, m + AHEAD < MSUB ? h : 1, next);
+        }
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -386,7 +386,10 @@ __device__ __forceinline__ void finish(v16f (&acc)[MSUB][4], const Item4& it, in
       for (int m = 0; m < MSUB; ++m) part(m, h * MSUB + m);
     } else {
 #pragma unroll 1
-      for (int m = 0; m < MSUB; ++m) part(m, 0);
+      for (int m = 0; m < MSUB; m += AHEAD) {
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) part(m + j, j);
+      }
     }
   }
 }
