@@ -184,6 +184,15 @@ hipError_t launch_fc_mid(const FcArgs& p, bool fc1, int rows, int grid, hipStrea
 constexpr int kFp4Cols = 256;
 constexpr int kFp4K = 512;
 constexpr int64_t kFp4MaxN = (int64_t)1 << 22;
+// Tiles of 64 rows, dense: with p.ksplit > 1 an item takes one of as many ranges of K and
+// leaves fp32 sums in p.part, joined by launch_linear_join.  A range has fp4_range stages of
+// 256 K, an even number (scales come by two stages) of 4 or more (the copies are 3 ahead); the
+// last one what is left, 4 or more too.
+__host__ __device__ inline int fp4_range(int stages, int ranges) { return ((stages + ranges - 1) / ranges + 1) & ~1; }
+inline bool fp4_range_ok(int stages, int ranges) {
+  const int len = fp4_range(stages, ranges);
+  return len >= 4 && stages - len * (ranges - 1) >= 4;
+}
 hipError_t launch_linear_fp4(const FcArgs& p, int rows, int grid, hipStream_t st);
 
 }  // namespace moe_mx

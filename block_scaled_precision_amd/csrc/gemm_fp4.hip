@@ -32,6 +32,8 @@
 //   in the epilogue they wait for every copy before them (512 rows of 384 experts, 7168 x 2048:
 //   474 us -> 377).
 //
+// - Few dense items of 64 rows split K into ranges, whose fp32 sums a second launch joins.
+//
 // Measured (MI355X, from codes): 8192 x 8192 x 8192 262 us with 256 rows, 4.2 PFLOP/s, 128 rows
 // 310, 64 rows 415; 8192 x 4096 x 7168 121, 143, 183; 65536 rows of 128 experts, 1536 x 4096, 289,
 // 307, 420, with SiLU and a second factor 367 (128 rows).  A 256-row K loop takes 2900 cycles a
@@ -79,6 +81,7 @@ template <int MSUB, int SLOTS_> struct Lay4 {
 
 struct Item4 {
   int expert, p0, rows, nb;
+  int range, k0, kend;  // of the ranges of K; its stages
 };
 // The items of an XCD, q, q + Q, ... for its workgroup q: patches of kPatchM row tiles
 // by kPatchN column blocks one after the other, so that workgroups that run at the
@@ -87,10 +90,11 @@ struct Item4 {
 constexpr int kPatchM = 4, kPatchN = 8;
 struct Sched4 {
   int xcd, full, tail0, q, Q, NB, ntiles, nk, items;
+  int len;   // stages of a range of K
   bool odd;  // K % 256 == 128: the last stage is half of one
 };
 
-template <int TM>
+template <int TM, bool SPLIT>
 __device__ __forceinline__ Item4 item_at(const FcArgs& p, const Sched4& sc, int li) {
   const int j = sc.q + li * sc.Q, block = kPatchM * sc.NB;
   int u, t0;  // item within a run of blocks that begins with tile t0
@@ -107,6 +111,14 @@ __device__ __forceinline__ Item4 item_at(const FcArgs& p, const Sched4& sc, int 
   const int width = min(kPatchN, sc.NB - nb0), ti = __builtin_amdgcn_readfirstlane(t0 + u / width);
   Item4 it;
   it.nb = __builtin_amdgcn_readfirstlane(nb0 + u % width);
+  it.range = it.k0 = 0;
+  it.kend = sc.nk;
+  if (SPLIT) {
+    it.range = __builtin_amdgcn_readfirstlane(it.nb / p.nchunks);
+    it.nb = __builtin_amdgcn_readfirstlane(it.nb - it.range * p.nchunks);
+    it.k0 = it.range * sc.len;
+    it.kend = min(sc.nk, it.k0 + sc.len);
+  }
   if (p.dense_rows > 0) {
     it.expert = 0;
     it.p0 = TM * ti;
@@ -137,7 +149,7 @@ __device__ __forceinline__ void lds_copy16_b(v4i buffer, uint32_t off, uint32_t 
 
 // The copies of one wave: stages in order, each in COPIES parts that the caller
 // spreads between its MFMAs.
-template <int MSUB, int NBUF, bool BIAS> struct Copier {
+template <int MSUB, int NBUF, bool BIAS, bool SPLIT> struct Copier {
   using L = Lay4<MSUB, NBUF>;
   static constexpr int COPIES = L::ACOP + L::BCOP;
   const FcArgs& p;
@@ -146,6 +158,7 @@ template <int MSUB, int NBUF, bool BIAS> struct Copier {
   int w, lane;
   // cursor: items begun, stage of the last, LDS offsets of its stage and scale group
   int li = 0, ls, slot = 0, group = 0, bbuf = 0;
+  int k0, kend;  // the stages of its item
   // the item and stage that parts belong to
   v4i abuf, wbuf;
   const uint8_t *asb, *wsb;
@@ -158,7 +171,7 @@ template <int MSUB, int NBUF, bool BIAS> struct Copier {
   // (Rows 8 i + lane / 8; a wave's copies begin at an even i.)
   __device__ __forceinline__ int chunk(int i) const { return (lane & 7) ^ (lane >> 4 | (i & 1) << 2); }
   __device__ __forceinline__ void set_item() {
-    const Item4 it = item_at<L::TM>(p, sc, li);
+    const Item4 it = item_at<L::TM, SPLIT>(p, sc, li);
     const int K = p.K, kb = K / 2, ks = K / 32, n0 = it.nb * TN, last = p.N - 1 - n0;
     const int r8 = lane >> 3;
     abuf = buffer_of((const uint8_t*)p.a + (int64_t)it.p0 * kb);
@@ -175,6 +188,8 @@ template <int MSUB, int NBUF, bool BIAS> struct Copier {
     wsoff = (uint32_t)min(epi_row32(64 * w + lane), last) * (uint32_t)ks;
     bias_at = (int64_t)it.expert * p.N + n0;
     cols = last + 1;
+    k0 = it.k0;
+    kend = it.kend;
   }
   // Goes to the next stage.  Past the last stage of the last item that stage goes out
   // again, into a slot that nothing reads any more: without a branch around them the
@@ -189,7 +204,7 @@ template <int MSUB, int NBUF, bool BIAS> struct Copier {
       slot = slot == (L::NBUF - 1) * L::STAGE ? 0 : slot + L::STAGE;
       asm volatile("" : "+s"(slot));
     } else if (piece == 2) {
-      ls = min(ls + 1, sc.nk - 1);
+      ls = min(ls + 1, kend - 1);
       soff = ROW * ls;
       asm volatile("" : "+s"(ls), "+s"(soff));
     } else {
@@ -200,11 +215,11 @@ template <int MSUB, int NBUF, bool BIAS> struct Copier {
       asm volatile("" : "+v"(outside[0]), "+v"(outside[1]));
     }
   }
-  __device__ __forceinline__ bool ends_item() const { return ls == sc.nk - 1 && li < sc.items; }
+  __device__ __forceinline__ bool ends_item() const { return ls == kend - 1 && li < sc.items; }
   __device__ __forceinline__ void next_item() {
     set_item();
     ++li;
-    ls = -1;
+    ls = k0 - 1;
   }
   __device__ __forceinline__ bool scales() const { return (ls & 1) == 0; }
   // the stage's scale group, where it is the first of two
@@ -394,15 +409,41 @@ __device__ __forceinline__ void finish(v16f (&acc)[MSUB][4], const Item4& it, in
   }
 }
 
-template <int MSUB, int NBUF, bool IN, bool BIAS>
+// A range's sums in fp32, for launch_linear_join: 16 MSUB stores of every lane
+template <int MSUB>
+__device__ __forceinline__ void leave(v16f (&acc)[MSUB][4], const FcArgs& p, const Item4& it, int wm, int l32, int col) {
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  const auto out = __builtin_amdgcn_make_buffer_rsrc(p.part + ((int64_t)it.range * p.dense_rows + it.p0) * p.N, 0,
+                                                     (int)kOutside, 0x00020000);
+  const int rows = it.rows - 32 * wm - l32, cols = p.N - col;
+#pragma unroll
+  for (int m = 0; m < MSUB; ++m)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int h = j >> 2, q = j & 3;
+      const bool in = 64 * m < rows && 16 * j < cols;
+      const uint32_t at = in ? 4 * ((uint32_t)(32 * wm + l32 + 64 * m) * (uint32_t)p.N + col + 16 * j) : kOutside;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        u32x4 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = __float_as_uint(acc_read(acc[m][2 * h + k][4 * q + i]));
+        __builtin_amdgcn_raw_buffer_store_b128(o, out, (int)(at + 16 * k), 0, 0);
+      }
+    }
+}
+
+template <int MSUB, int NBUF, bool IN, bool BIAS, bool SPLIT>
 __global__ __launch_bounds__(kThreads4, 1) void k_linear_fp4(FcArgs p) {
   using L = Lay4<MSUB, NBUF>;
-  using C = Copier<MSUB, NBUF, BIAS>;
+  using C = Copier<MSUB, NBUF, BIAS, SPLIT>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[L::TOTAL];
   Sched4 sc;
   sc.nk = (p.K + 255) / 256;
   sc.odd = p.K % 256 != 0;
-  sc.NB = p.nchunks;
+  const int ranges = SPLIT ? p.ksplit : 1;
+  sc.len = SPLIT ? fp4_range(sc.nk, ranges) : sc.nk;
+  sc.NB = p.nchunks * ranges;  // (ranges count as column blocks)
   sc.ntiles = p.dense_rows > 0 ? (p.dense_rows + L::TM - 1) / L::TM : *p.num_tiles;
   sc.xcd = blockIdx.x & 7;
   sc.q = blockIdx.x >> 3;
@@ -489,6 +530,7 @@ __global__ __launch_bounds__(kThreads4, 1) void k_linear_fp4(FcArgs p) {
   constexpr Int<SLOTS> end;
 
   copy.next_item();
+  const int first = copy.k0;
   for (int s = 0; s < L::NBUF; ++s) {
     if (copy.ends_item()) copy.next_item();
 #pragma unroll
@@ -500,7 +542,7 @@ __global__ __launch_bounds__(kThreads4, 1) void k_linear_fp4(FcArgs p) {
   wait_vm_lgkm0<0>();
   barrier();
   {
-    const uint8_t* gs = smem + scales_at(0);
+    const uint8_t* gs = smem + scales_at(first);
 #pragma unroll
     for (int i = 0; i < READS; ++i) {
       read_scale(gs, i);
@@ -511,14 +553,14 @@ __global__ __launch_bounds__(kThreads4, 1) void k_linear_fp4(FcArgs p) {
   const uint8_t* st = smem;
   int slot = 0, bbuf = 0;
   for (int ci = 0; ci < sc.items; ++ci) {
-    const Item4 it = item_at<L::TM>(p, sc, ci);
+    const Item4 it = item_at<L::TM, SPLIT>(p, sc, ci);
 #pragma unroll
     for (int m = 0; m < MSUB; ++m)
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.f;
-    for (int ks = 0; ks < sc.nk; ++ks) {
+    for (int ks = it.k0; ks < it.kend; ++ks) {
       each(slots, [&](auto k) {
         mfma(i0, i0, k);
         among(k, reads, i0, mid, [&](int i) { read(1, st, off[1], i); });
@@ -531,7 +573,8 @@ __global__ __launch_bounds__(kThreads4, 1) void k_linear_fp4(FcArgs p) {
       pin();
       const bool behind = copy.scales(), first = copy.ls == 0;  // (of the stage begun last)
       if (copy.ends_item()) copy.next_item();
-      const int kn = ks + 1 == sc.nk ? 0 : ks + 1;
+      // (a range has more stages than the copies are ahead: they are in the next item)
+      const int kn = ks + 1 < it.kend ? ks + 1 : SPLIT ? copy.k0 : 0;
       uint32_t so = 0;
       __builtin_amdgcn_sched_barrier(0);
       each(slots, [&](auto k) {
@@ -555,8 +598,8 @@ __global__ __launch_bounds__(kThreads4, 1) void k_linear_fp4(FcArgs p) {
       // whole once every wave passes the barrier, and this one's slot is free
       // (behind the copies of the item's first stages the epilogue before it has left 8
       // MSUB stores, and the first stage has sent the second half of the last once more)
-      constexpr int kBehind = 8 * MSUB + rest;
-      const bool stored = ks == 0 && ci > 0;
+      constexpr int kBehind = (SPLIT ? 16 : 8) * MSUB + rest;
+      const bool stored = ks == it.k0 && ci > 0;
       if (L::NBUF == 2) {
         if (stored) wait_vm_lgkm0<kBehind>();
         else wait_vm_lgkm0<0>();
@@ -589,7 +632,8 @@ __global__ __launch_bounds__(kThreads4, 1) void k_linear_fp4(FcArgs p) {
 #pragma unroll
     for (int i = half; i < C::COPIES; ++i) copy.part(i);
     // the lane holds row 32 (wm + 2m) + l32 of the tile, eight columns of each piece
-    finish<MSUB, IN, BIAS>(acc, it, p.N, wm, l32, it.nb * TN + 128 * wn + 8 * g, smem + L::BIAS + bbuf);
+    if constexpr (SPLIT) leave<MSUB>(acc, p, it, wm, l32, it.nb * TN + 128 * wn + 8 * g);
+    else finish<MSUB, IN, BIAS>(acc, it, p.N, wm, l32, it.nb * TN + 128 * wn + 8 * g, smem + L::BIAS + bbuf);
     bbuf = bbuf == (L::BBUFS - 1) * 4 * TN ? 0 : bbuf + 4 * TN;
   }
   wait_vm_lgkm0<0>();  // no copy may land in LDS that is no longer this workgroup's
@@ -600,14 +644,19 @@ __global__ __launch_bounds__(kThreads4, 1) void k_linear_fp4(FcArgs p) {
 template <int MSUB, int NBUF>
 static void launch_fp4_t(const FcArgs& p, int grid, hipStream_t st) {
   const bool in = p.epi.mul || p.epi.residual, bias = p.epi.bias_kind != kBiasNone;
-  auto kernel = in ? (bias ? k_linear_fp4<MSUB, NBUF, true, true> : k_linear_fp4<MSUB, NBUF, true, false>)
-                   : (bias ? k_linear_fp4<MSUB, NBUF, false, true> : k_linear_fp4<MSUB, NBUF, false, false>);
+  auto kernel = in ? (bias ? k_linear_fp4<MSUB, NBUF, true, true, false> : k_linear_fp4<MSUB, NBUF, true, false, false>)
+                   : (bias ? k_linear_fp4<MSUB, NBUF, false, true, false> : k_linear_fp4<MSUB, NBUF, false, false, false>);
   kernel<<<grid, kThreads4, 0, st>>>(p);
 }
 
 hipError_t launch_linear_fp4(const FcArgs& p, int rows, int grid, hipStream_t st) {
   if (grid < 8) grid = 8;
   grid &= ~7;
+  if (p.ksplit > 1) {
+    if (rows != 64 || p.dense_rows <= 0 || !fp4_range_ok((p.K + 255) / 256, p.ksplit)) return hipErrorInvalidValue;
+    k_linear_fp4<1, 3, false, false, true><<<grid, kThreads4, 0, st>>>(p);
+    return hipGetLastError();
+  }
   const bool pairs = (p.K + 255) / 256 % 2 == 0;  // (Lay4: three slots of 128 rows)
   if (rows == 256) launch_fp4_t<4, 2>(p, grid, st);
   else if (rows == 128 && pairs) launch_fp4_t<2, 3>(p, grid, st);

@@ -75,5 +75,11 @@ extern "C" moe_status_t mx4_linear(const mx4_linear_problem_t* p, const mx_linea
     g.dense_rows = (int)M;
   }
   g.nchunks = (int)((p->N + kFp4Cols - 1) / kFp4Cols);
-  return launch_linear_fp4(g, f.rows, device_cus(), stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+  if (f.ksplit > 1) {
+    g.ksplit = f.ksplit;
+    g.part = (float*)(ws + f.part);
+  }
+  hipError_t e = launch_linear_fp4(g, f.rows, device_cus(), stream);
+  if (e == hipSuccess && f.ksplit > 1) e = launch_linear_join(g, stream);
+  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

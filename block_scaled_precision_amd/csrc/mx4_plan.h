@@ -5,7 +5,8 @@
 
 namespace moe_mx {
 
-// kFew: gemm_few.hip, E2M1 codes or bf16 quantized on the way; kTile: gemm_fp4.hip;
+// kFew: gemm_few.hip, E2M1 codes or bf16 quantized on the way; kTile: gemm_fp4.hip, for few
+// dense items in ranges of K;
 // kWiden: E4M3 codes of the E2M1 ones (every E2M1 value is an E4M3 value, with the same
 // scale) and mx_linear's kernels
 enum class Fc4 { kFew, kTile, kWiden };
@@ -13,10 +14,12 @@ enum class Fc4 { kFew, kTile, kWiden };
 struct Mx4Plan {
   Fc4 kind;
   int rows;               // kTile: M-tile height
+  int ksplit;             // kTile: ranges of K (0: one)
   int max_tiles;          // kFew, kTile, grouped: M-tiles there can be
   size_t codes, scales;   // E2M1 codes and scales of bf16 rows
   size_t wide;            // kWiden: E4M3 codes
   size_t tiles, ntiles;   // kTile, grouped: the tile list
+  size_t part;            // kTile, ranges of K: their sums
   size_t rest, rest_bytes;  // kWiden: mx_linear's own workspace
   size_t total;
 };
@@ -60,11 +63,12 @@ inline Mx4Plan mx4_plan(const mx4_linear_problem_t& p, bool has_a_scale) {
   const LinearCost c(q, true);
   Mx4Plan f = {};
   double best = -1.0;
-  auto take = [&](Fc4 kind, int rows, double us) {
+  auto take = [&](Fc4 kind, int rows, double us, int ksplit = 0) {
     if (best >= 0.0 && us >= best) return;
     best = us;
     f.kind = kind;
     f.rows = rows;
+    f.ksplit = ksplit;
   };
   const double before = p.groups > 0 ? 4.0 : 0.0;
   const double quant = has_a_scale ? 0.0 : 3.0 + (double)p.M * p.K * 2.53 / 4.5e6;
@@ -88,6 +92,15 @@ inline Mx4Plan mx4_plan(const mx4_linear_problem_t& p, bool has_a_scale) {
       const double tiles = rounds * (stages * t * (p.groups > 0 ? f4.group : 1.0) + f4.item);
       take(Fc4::kTile, 64 << i, 1.5 + std::max(tiles, weights) + before + quant);
     }
+    // ranges of K while all items have a workgroup of their own (K = 7168; 64-row tiles in one
+    // range, in several, widened: 33 x 4096 20 us, 13.1, 16.3; 100 x 4096 21, 15.8, 18.2; 64 x 1032
+    // 19, 11.8, 12.6; 500 x 520 19.5, 15.8, 18; 256 x 4096 23.5, 24.0)
+    const double items = c.tiles(64) * std::ceil(p.N / (double)kFp4Cols);
+    for (int s = 2; p.groups == 0 && s * items <= kLinearWgs && s <= 16; ++s)
+      if (fp4_range_ok((int)stages, s)) {
+        const double t = kFp4Cost[0].few + (kFp4Cost[0].all - kFp4Cost[0].few) * s * items / kLinearWgs;
+        take(Fc4::kTile, 64, 1.5 + fp4_range((int)stages, s) * t + kFp4Cost[0].item + c.join_time(s) + before + quant, s);
+      }
   }
   const int64_t blocks = (p.N + kFewCols - 1) / kFewCols;
   if (most_tiles(q, kStreamRows) * blocks <= 1 << 20) {
@@ -113,6 +126,7 @@ inline Mx4Plan mx4_plan(const mx4_linear_problem_t& p, bool has_a_scale) {
     f.tiles = room((size_t)f.max_tiles * sizeof(Tile));
     f.ntiles = room(4);
   }
+  if (f.ksplit > 1) f.part = room((size_t)f.ksplit * p.M * p.N * 4);
   if (f.kind == Fc4::kWiden) {
     f.wide = room((size_t)(p.M * p.K));
     f.rest_bytes = linear_plan(q, true).total;

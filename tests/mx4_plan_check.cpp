@@ -22,7 +22,7 @@ int main() {
       continue;
     }
     const Mx4Plan f = mx4_plan(p, scaled != 0);
-    const char* name = f.kind == Fc4::kFew ? "few" : f.kind == Fc4::kTile ? "tile" : "widen";
+    const char* name = f.kind == Fc4::kFew ? "few" : f.kind == Fc4::kWiden ? "widen" : f.ksplit > 1 ? "ranges" : "tile";
     std::printf("%s %d %d %zu\n", name, f.rows, f.max_tiles, f.total);
   }
   return 0;

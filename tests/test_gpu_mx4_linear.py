@@ -51,7 +51,9 @@ CASES = [
     ("tile", 128, 9000, 264, 1152, 40), ("tile", 128, 4200, 1032, 640, 1), ("tile", 128, 9300, 4104, 512, 3),
     ("tile", 256, 3000, 4104, 1920, 0), ("tile", 256, 6000, 2056, 2176, 0), ("tile", 256, 9300, 2568, 3200, 0),
     ("tile", 256, 1900, 4104, 1920, 1), ("tile", 256, 6000, 4104, 1664, 3),
-    ("widen", 0, 700, 1032, 128, 0), ("widen", 0, 64, 1032, 7168, 0), ("widen", 0, 1500, 520, 384, 0),
+    ("ranges", 64, 64, 1032, 7168, 0), ("ranges", 64, 300, 2056, 7168, 0), ("ranges", 64, 100, 4104, 7040, 0),
+    ("ranges", 64, 500, 520, 7168, 0),
+    ("widen", 0, 700, 1032, 128, 0), ("widen", 0, 1500, 520, 384, 0),
     ("widen", 0, 3000, 1032, 128, 6),
 ]
 IDS = [f"{k}{r}_{M}x{N}x{K}_g{G}" for k, r, M, N, K, G in CASES]
@@ -271,7 +273,7 @@ def test_longest_sum(M, N):
     _same_bits(m.mx4_linear(a, w, wsc, a_scale=asc), ref, "longest sum")
 
 
-AT_ONCE = [(5, 512, 1024, 0, False), (300, 2056, 640, 0, False), (700, 1032, 512, 4, True), (60, 4096, 1152, 0, False),
+AT_ONCE = [(100, 2056, 7168, 0, True), (5, 512, 1024, 0, False), (300, 2056, 640, 0, False), (700, 1032, 512, 4, True), (60, 4096, 1152, 0, False),
            (1500, 4104, 512, 5, False)]
 
 
