@@ -31,7 +31,6 @@
 // - The next item's copies are under way during an epilogue, and biases come with them: loaded
 //   in the epilogue they wait for every copy before them (512 rows of 384 experts, 7168 x 2048:
 //   474 us -> 377).
-//
 // - Few dense items of 64 rows split K into ranges, whose fp32 sums a second launch joins.
 //
 // Measured (MI355X, from codes): 8192 x 8192 x 8192 262 us with 256 rows, 4.2 PFLOP/s, 128 rows
