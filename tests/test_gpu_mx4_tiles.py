@@ -1,0 +1,94 @@
+"""mx4_linear's large tiles against float64, on a sample of rows and columns: every row of a first
+and of a ragged last tile and both sides of every group's ends, every column of a column block
+and of the ragged last one, and others at random.
+
+Bounds and exactness as in tests/test_gpu_mx4_linear.py.  The tiles' SiLU takes exp(-|v|) as t =
+exp2(-|v| log2 e), off by |v| + 2 half steps of fp32: at most 16 of f = |v| t / (1 + t) up to |v|
+= 14; past it f is below 1.2e-5 and the rest, (|v| + 2) E32 f < 1.3e-11, lies below the bound's dv
+= 2 (K + 1) E32 (sum |a w| + |bias|) >= 2 K E32 |v|.
+"""
+import numpy as np
+import pytest
+import torch
+
+from block_scaled_precision_amd import inputs as gen
+from oracle import mx4
+from tests.conftest import has_gpu
+from tests.helpers import print_flush
+from tests.test_gpu_linear import BF16, _bound, _np
+from tests.test_gpu_mx4_linear import _codes, _offsets
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not has_gpu(), reason="needs a GPU")]
+
+# (kernel, rows of its tiles, M, N, K, groups); tests/test_mx4_tiles_plan.py holds the lists of
+# this file against the choice.  K: stages of 256 even and odd in number, the last one whole and
+# half; fewer items than workgroups, and several for each.
+LARGE = [
+    ("tile", 128, 1500, 4104, 512, 0), ("tile", 128, 6000, 520, 640, 0), ("tile", 128, 6000, 520, 768, 0),
+    ("tile", 128, 6000, 520, 896, 0), ("tile", 128, 9000, 4104, 640, 0), ("tile", 128, 6000, 520, 512, 1),
+    ("tile", 128, 6000, 520, 768, 5), ("tile", 128, 8000, 264, 896, 40), ("tile", 128, 9300, 4104, 512, 3),
+    ("tile", 256, 3000, 4104, 1920, 0), ("tile", 256, 3000, 4104, 2048, 0), ("tile", 256, 5000, 1544, 2176, 0),
+    ("tile", 256, 5000, 1544, 2304, 0), ("tile", 256, 9300, 2568, 3200, 0), ("tile", 256, 5000, 1544, 2048, 1),
+    ("tile", 256, 5000, 1544, 2304, 5), ("tile", 256, 6000, 1032, 1920, 40), ("tile", 256, 6000, 4104, 1664, 3),
+    ("widen", 0, 3000, 1032, 128, 6), ("widen", 0, 1500, 520, 384, 0),
+]
+LARGE_IDS = [f"{k}{r}_{M}x{N}x{K}_g{G}" for k, r, M, N, K, G in LARGE]
+
+
+def _sample(M, N, tile, off, seed):
+    """Rows and columns to compare, ascending."""
+    rng = np.random.default_rng(seed)
+    tile = tile or 192
+    ends = [0, M] if off is None else [int(e) for e in off]
+    rows = {*range(min(tile, M)), *range((M - 1) // tile * tile, M), *rng.integers(0, M, 60).tolist()}
+    rows |= {r for e in ends for r in (e - 1, e) if 0 <= r < M}
+    block = 256 * int(rng.integers(0, max(N // 256, 1)))
+    cols = {*range(block, min(block + 256, N)), *range((N - 1) // 256 * 256, N), *rng.integers(0, N, 60).tolist()}
+    return np.array(sorted(rows)), np.array(sorted(cols))
+
+
+def _sampled_offsets(rows, off):
+    return None if off is None else np.searchsorted(rows, off)
+
+
+def _fn64(v, fn):
+    x = torch.from_numpy(v)
+    if fn == "silu":
+        return (x / (1 + torch.exp(-x))).numpy()
+    if fn == "gelu":
+        return (x * torch.special.erfc(-x / 2 ** 0.5) / 2).numpy()
+    return np.maximum(v, 0) ** 2 if fn == "relu2" else v
+
+
+@pytest.mark.parametrize("fn", ["none", "silu", "gelu", "relu2"])
+@pytest.mark.parametrize("kernel,tile,M,N,K,G", LARGE, ids=LARGE_IDS)
+def test_functions_factors_and_residuals(kernel, tile, M, N, K, G, fn):
+    """Every function with a bias of either type or none, a second factor, a residual, both."""
+    from block_scaled_precision_amd import moe_mx as m
+    print_flush(f"mx4_linear {fn} {kernel}{tile} M={M} N={N} K={K} G={G}")
+    a = gen.normal((M, K), 4, 25).to(BF16)
+    shape = (G, N) if G else (N,)
+    w, s = _codes(shape, K, 4, scales=(118, 123))
+    bias = gen.normal(shape, 4, 26)
+    mul, res = gen.normal((M, N), 4, 27).to(BF16), gen.normal((M, N), 4, 28).to(BF16)
+    off = _offsets(M, G, M + N)
+    rows, cols = _sample(M, N, tile, off, M)
+    part = _sampled_offsets(rows, off)
+    pick = np.ix_(rows, cols)
+    wn, sn = (t.numpy()[:, cols] if G else t.numpy()[cols] for t in (w, s))
+    v0, size, _ = mx4.mx4_linear(_np(a[rows]), wn, sn, offsets=part)
+    kw = dict(fn=fn, expert_offsets=None if off is None else torch.from_numpy(off).int().cuda())
+    a, w, s = a.cuda(), w.cuda(), s.cuda()
+    for b, mu, re in ((None, None, None), (bias, None, None), (bias.to(BF16), mul, None), (None, None, res),
+                      (bias, mul, res), (None, mul, res)):
+        got = m.mx4_linear(a, w, s, bias=None if b is None else b.cuda(), mul=None if mu is None else mu.cuda(),
+                           residual=None if re is None else re.cuda(), **kw)
+        assert torch.isfinite(got).all()
+        b64 = np.zeros((len(rows), len(cols)))
+        if b is not None:
+            b64 += np.repeat(_np(b)[:, cols], np.diff(part), axis=0) if G else _np(b)[cols]
+        mu64, re64 = (1.0 if mu is None else _np(mu)[pick]), (0.0 if re is None else _np(re)[pick])
+        ref = _fn64(v0 + b64, fn) * mu64 + re64
+        d = np.abs(_np(got.cpu()[pick]) - ref)
+        bound = _bound(fn, K, v0 + b64, size, b64, mu64, re64, ref)
+        assert (d <= bound).all(), f"{(d > bound).sum()} out of bounds, worst ratio {(d / bound).max():.2f}"
