@@ -11,6 +11,7 @@ import numpy as np
 import pytest
 import torch
 
+import tests.test_gpu_mx4_linear as lin
 from block_scaled_precision_amd import inputs as gen
 from oracle import mx, mx4
 from tests.conftest import has_gpu
@@ -118,3 +119,98 @@ def test_fp32_bias_and_relu2_are_bit_identical(kernel, tile, M, N, K, G):
     assert exact.mean() > 0.5 and (ref[exact] > 0).mean() > (0.1 if ref.size > 1000 else 0)
     bad = np.argwhere(exact & (got != mx.round_to_bf16(ref)))
     assert bad.size == 0, f"{len(bad)} of {exact.sum()} differ, first at {rows[bad[0][0]], cols[bad[0][1]]}"
+
+
+# (M, N, K) of 256-row tiles, without groups and with 5
+SCALED = [(3000, 4104, 1920), (3000, 4104, 2048), (5000, 1544, 2176), (5000, 1544, 2304)]
+
+
+@pytest.mark.parametrize("G", [0, 5])
+@pytest.mark.parametrize("M,N,K", SCALED)
+def test_every_code_meets_its_scales(M, N, K, G):
+    lin.test_every_code_meets_its_scales(M, N, K, G)
+
+
+@pytest.mark.parametrize("M,N,K", SCALED)
+def test_nan_scales_and_infinite_results(M, N, K):
+    lin.test_nan_scales_and_infinite_results(M, N, K)
+
+
+# (N, K, rows of each group), 256-row tiles: ends at, before and behind a tile's and a wave's
+COUNTS = [(1544, 1664, (256, 257, 255, 0, 1, 512, 3000, 719)), (1544, 2304, (0, 33, 4000, 95, 0, 1000)),
+          (4104, 1920, (2900,))]
+
+
+@pytest.mark.parametrize("N,K,counts", COUNTS, ids=str)
+def test_groups_are_bit_identical(N, K, counts):
+    lin.test_groups_are_bit_identical(N, K, list(counts))
+
+
+OUT_OF_ORDER = [(5000, 1544, 1664)]  # 4 groups
+
+
+@pytest.mark.parametrize("M,N,K", OUT_OF_ORDER)
+def test_offsets_out_of_order_or_range_stay_in_bounds(M, N, K):
+    from block_scaled_precision_amd import moe_mx as m
+    lin.test_offsets_out_of_order_or_range_stay_in_bounds(M, N, K)
+    a, (w, s) = _ints((M, K), 8, 20), _codes((4, N), K, 8)
+    buf = torch.full((3 * M, N), 9.0, dtype=BF16, device="cuda")
+    for off in ([0, M, 5, M, 80], [0, 1000, 3000, 5000, 10 ** 6], [-2 ** 31, 2 ** 31 - 1, 0, 5, 9]):
+        m.mx4_linear(a.cuda(), w.cuda(), s.cuda(), expert_offsets=torch.tensor(off, dtype=torch.int32).cuda(),
+                     out=buf[M:2 * M])
+        torch.cuda.synchronize()
+        assert (buf[:M] == 9.0).all() and (buf[2 * M:] == 9.0).all()
+
+
+ALIGNED = [(3000, 4104, 1920, 0), (5000, 1544, 2304, 5), (6000, 4104, 1664, 3)]
+
+
+@pytest.mark.parametrize("M,N,K,G", ALIGNED)
+def test_biases_of_any_alignment(M, N, K, G):
+    """Either type, from every address of the type; the bias differs in every column and group,
+    and NaN stands before and behind it."""
+    from block_scaled_precision_amd import moe_mx as m
+    shape = (G, N) if G else (N,)
+    (w, s), (a, asc) = _codes(shape, K, 50), _codes((M,), K, 51)
+    off = _offsets(M, G, M)
+    rows, cols = _sample(M, N, 256, off, M)
+    wn, sn = (t.numpy()[:, cols] if G else t.numpy()[cols] for t in (w, s))
+    v, _, _ = mx4.mx4_linear(a.numpy()[rows], wn, sn, a_scale=asc.numpy()[rows], offsets=_sampled_offsets(rows, off))
+    kw = dict(a_scale=asc.cuda(), expert_offsets=None if off is None else torch.from_numpy(off).int().cuda())
+    a, w, s, n = a.cuda(), w.cuda(), s.cuda(), max(G, 1) * N
+    values = ((torch.arange(n) * 37) % 509 - 254).float()
+    for dtype, step in ((torch.float32, 4), (BF16, 2)):
+        b = _np(values.to(dtype)).reshape(shape)
+        ref = v + (np.repeat(b[:, cols], np.diff(_sampled_offsets(rows, off)), axis=0) if G else b[cols])
+        for at in range(0, 16, step):
+            buf = torch.full((n + 16,), float("nan"), dtype=dtype, device="cuda")
+            view = buf[at // step:at // step + n]
+            view.copy_(values)
+            got = m.mx4_linear(a, w, s, bias=view.view(shape), **kw).cpu()
+            assert np.array_equal(_np(got[np.ix_(rows, cols)]), mx.round_to_bf16(ref)), f"{dtype} at {at}"
+
+
+IN_PLACE = [(9300, 2568, 3200, 0), (6000, 4104, 1664, 3), (9000, 4104, 640, 0)]
+
+
+@pytest.mark.parametrize("M,N,K,G", IN_PLACE)
+def test_out_may_be_factor_and_residual(M, N, K, G):
+    from block_scaled_precision_amd import moe_mx as m
+    w, s = (t.cuda() for t in _codes((G, N) if G else (N,), K, 9))
+    a, asc = (t.cuda() for t in _codes((M,), K, 10))
+    res = _ints((M, N), 9, 23).cuda()
+    off = _offsets(M, G, M)
+    kw = dict(a_scale=asc, expert_offsets=None if off is None else torch.from_numpy(off).int().cuda())
+    want = m.mx4_linear(a, w, s, residual=res, mul=res, **kw)
+    buf = res.clone()
+    m.mx4_linear(a, w, s, residual=buf, mul=buf, out=buf, **kw)
+    assert torch.equal(buf, want)
+
+
+# (M, N, K, groups, codes given)
+AT_ONCE = [(3000, 4104, 1920, 0, True), (5000, 1544, 2304, 5, False), (9300, 2568, 3200, 0, False), (9000, 4104, 640, 0, True)]
+
+
+def test_prepared_calls_at_once_and_captured(monkeypatch):
+    monkeypatch.setattr(lin, "AT_ONCE", AT_ONCE)
+    lin.test_prepared_calls_at_once_and_captured()

@@ -23,3 +23,30 @@ def test_functions_run_on_the_tiles_they_name():
             # several items for a workgroup, and at most one
             items = [-(-c[2] // rows) * -(-c[3] // 256) for c in own]
             assert max(items) > 256 > min(items), own
+
+
+def test_lists_of_256_row_tiles():
+    from tests import test_gpu_mx4_tiles as t
+    problems = [(M, N, K, G, codes) for M, N, K in t.SCALED for G in (0, 5) for codes in (False, True)]
+    problems += [(sum(c) + 5, N, K, len(c), codes) for N, K, c in t.COUNTS for codes in (False, True)]
+    problems += [(M, N, K, 4, False) for M, N, K in t.OUT_OF_ORDER]
+    problems += [(M, N, K, G, True) for M, N, K, G in t.ALIGNED]
+    wrong = [(q, p) for q, p in zip(problems, plans(problems)) if (p.kernel, p.rows) != ("tile", 256)]
+    assert not wrong, wrong
+    for some in ([(M, N, K, G, True) for M, N, K, G in t.IN_PLACE], t.AT_ONCE):
+        assert [p.rows for p in plans(some)] == [256] * (len(some) - 1) + [128], some
+
+
+def test_every_list_meets_every_tile_height():
+    """The shapes of each check in both files together."""
+    from tests import test_gpu_mx4_linear as lin
+    from tests import test_gpu_mx4_tiles as t
+    lists = {
+        "scales": [(M, N, K, G, True) for M, N, K in lin.PICKED + t.SCALED for G in (0, 5)],
+        "biases": [(M, N, K, G, True) for M, N, K, G in t.ALIGNED + [(3, 72, 256, 0), (300, 2056, 640, 0), (3000, 4104, 512, 0)]],
+        "at once": lin.AT_ONCE + t.AT_ONCE,
+        "functions": [(M, N, K, G, False) for _, _, M, N, K, G in lin.SOME + t.LARGE],
+    }
+    for name, problems in lists.items():
+        got = {p.rows for p in plans(problems) if p.kernel in ("tile", "ranges")}
+        assert got == {64, 128, 256}, (name, got)
