@@ -206,7 +206,8 @@ struct ColsArgs {
   const void* src;     // [batch, rows, cols], rows ld apart
   int rows, cols;
   int64_t ld;
-  int tiles_r, tiles_c;
+  int tiles_r, tiles_c;  // of this launch, from column tile first_c on
+  int first_c;
   const float* signs;
   const uint8_t* random;  // [batch, rows, cols]
   uint8_t* codes;      // [batch, cols, padded rows / 2]
@@ -222,7 +223,7 @@ __global__ __launch_bounds__(kThreadsQ) void k_mx4_cols(ColsArgs a) {
   // lane, a block apart per 32 lanes) spread over the banks
   __shared__ uint4 sc[kTileC][kTileR / 32 + 1];
   __shared__ uint8_t ss[kTileC][kTileR / 32];
-  const int tc = blockIdx.x % a.tiles_c, tr = blockIdx.x / a.tiles_c % a.tiles_r;
+  const int tc = a.first_c + blockIdx.x % a.tiles_c, tr = blockIdx.x / a.tiles_c % a.tiles_r;
   const int64_t batch = blockIdx.x / a.tiles_c / a.tiles_r;
   const int pc = threadIdx.x & 31, rb = threadIdx.x >> 5;
   const int c = tc * kTileC + 2 * pc, r0 = tr * kTileR + 32 * rb;
@@ -399,7 +400,9 @@ __global__ __launch_bounds__(kThreadsQ) void k_mx4_expand(const uint32_t* __rest
 
 // ------------------------------------------------------------------- host --
 
-constexpr int64_t kMaxDim = (int64_t)1 << 30;  // rows, columns
+constexpr int64_t kMaxDim = (int64_t)1 << 30;  // rows, columns, matrices
+// Workgroups of one launch, which has fewer than 2^32 threads; what has more takes several.
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23;
 bool aligned_to(const void* p, int64_t n) { return (uintptr_t)p % (uintptr_t)n == 0; }
 
 // F with the four choices as compile-time constants
@@ -449,30 +452,41 @@ extern "C" moe_status_t mx4_quantize(const void* src, moe_src_t src_dtype, int64
   if (!src || !codes || !scales || !aligned_to(src, es) || !aligned_to(codes, 16) || !aligned_to(scales, 4) ||
       !aligned_to(signs, 4))
     return MOE_ERR_INVALID_ARG;
+  const moe_status_t st = check_arch();
+  if (st != MOE_OK) return st;
   if (transpose) {
-    ColsArgs a = {src, (int)rows, (int)cols, src_ld, (int)((rows + kTileR - 1) / kTileR),
-                  (int)((cols + kTileC - 1) / kTileC), signs, random, codes, scales};
-    const double grid = (double)batch * a.tiles_r * a.tiles_c;
-    if (grid > 8388607.0) return MOE_ERR_UNSUPPORTED;
-    const moe_status_t st = check_arch();
-    if (st != MOE_OK) return st;
+    const int64_t tiles_r = (rows + kTileR - 1) / kTileR, tiles_c = (cols + kTileC - 1) / kTileC;
+    // matrices of a launch and column tiles (tiles_r <= 2^22)
+    const int64_t nb = std::max<int64_t>(kMaxBlocks / (tiles_r * tiles_c), 1), nc = std::min(tiles_c, kMaxBlocks / tiles_r);
+    const int64_t padded = (rows + 127) / 128 * 128;
     const bool vec = cols % 2 == 0 && src_ld % 2 == 0 && aligned_to(src, 2 * es) && (!random || aligned_to(random, 2));
-    for_choices(bf16, vec, signs != nullptr, random != nullptr, [&](auto B, auto V, auto R, auto S) {
-      k_mx4_cols<B.value, V.value, R.value, S.value><<<(unsigned)grid, kThreadsQ, 0, stream>>>(a);
-    });
+    for (int64_t b = 0; b < batch; b += nb)
+      for (int64_t c = 0; c < tiles_c; c += nc) {
+        const int64_t n = std::min(nc, tiles_c - c);
+        ColsArgs a = {(const char*)src + b * rows * src_ld * es, (int)rows, (int)cols, src_ld, (int)tiles_r, (int)n, (int)c,
+                      signs, random ? random + b * rows * cols : nullptr, codes + b * cols * (padded / 2),
+                      scales + b * cols * (padded / 32)};
+        const int64_t blocks = std::min(nb, batch - b) * tiles_r * n;
+        for_choices(bf16, vec, signs != nullptr, random != nullptr, [&](auto B, auto V, auto R, auto S) {
+          k_mx4_cols<B.value, V.value, R.value, S.value><<<(unsigned)blocks, kThreadsQ, 0, stream>>>(a);
+        });
+        if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
+      }
   } else {
-    RowsArgs a = {src, batch * rows, src_ld, (int)cols, (int)((cols + 127) / 128 * 16), signs, random, codes, scales};
-    const int64_t blocks = (a.rows * a.units + kThreadsQ * kUnits - 1) / (kThreadsQ * kUnits);
-    if (blocks > 8388607) return MOE_ERR_UNSUPPORTED;
-    const moe_status_t st = check_arch();
-    if (st != MOE_OK) return st;
+    const int64_t all = batch * rows, units = (cols + 127) / 128 * 16, nr = kMaxBlocks * (kThreadsQ * kUnits) / units;
     const bool vec = cols % 8 == 0 && src_ld * es % 16 == 0 && aligned_to(src, 16) &&
                      (!random || aligned_to(random, 8));
-    for_choices(bf16, vec, signs != nullptr, random != nullptr, [&](auto B, auto V, auto R, auto S) {
-      k_mx4_rows<B.value, V.value, R.value, S.value><<<(unsigned)blocks, kThreadsQ, 0, stream>>>(a);
-    });
+    for (int64_t r = 0; r < all; r += nr) {
+      RowsArgs a = {(const char*)src + r * src_ld * es, std::min(nr, all - r), src_ld, (int)cols, (int)units, signs,
+                    random ? random + r * cols : nullptr, codes + 4 * r * units, scales + r * units / 4};
+      const int64_t blocks = (a.rows * units + kThreadsQ * kUnits - 1) / (kThreadsQ * kUnits);
+      for_choices(bf16, vec, signs != nullptr, random != nullptr, [&](auto B, auto V, auto R, auto S) {
+        k_mx4_rows<B.value, V.value, R.value, S.value><<<(unsigned)blocks, kThreadsQ, 0, stream>>>(a);
+      });
+      if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
+    }
   }
-  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+  return MOE_OK;
 }
 
 extern "C" moe_status_t mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,

@@ -383,7 +383,8 @@ moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_tensors_t* 
  *   (mx4_linear_workspace_bytes).  For a weight's gradients: dX = dY W is mx4_linear of dY
  *   and W quantized transposed, dW = dY^T X that of dY and X both quantized transposed.
  * Requires 16-byte aligned codes, scales and random on a multiple of 4 bytes and 1, src and
- * dst on a multiple of their element size; rows, cols and batch up to 2^30.  Empty
+ * dst on a multiple of their element size; rows, cols and batch up to 2^30 and, with the
+ * distance of the rows, up to 1.4e14 elements from src's or dst's first to the last.  Empty
  * matrices are no-ops.
  */
 typedef struct {
