@@ -9,7 +9,8 @@
 //             v[i], v[i + d] <- v[i] + v[i + d], v[i] - v[i + d] at d = 1, 2, 4, 8, 16 in
 //             fp32, then one product with the factor.  Two operands rotated alike have
 //             the product they had: the rotation only spreads large values over their
-//             block.
+//             block.  32 magnitudes below 2^123 add up inside fp32; a block in which larger
+//             ones overflow gets the NaN scale.
 //   nearest   2^s the scale, s = floor(log2 max|v|) - 2; the code nearest to |v| / 2^s,
 //             ties to the even code, at most 6: as mx_quantize does
 //   random    s one more where 6 * 2^s < max|v|, so that nothing saturates; with lo <= x
@@ -69,6 +70,12 @@ __device__ __forceinline__ uint32_t random4(float q, uint32_t n) {
   const uint32_t bits = __float_as_uint(x < 1.0f ? small : x) + (n << 14) + ((4u << 22) + 8191u);
   // 252 + code, + 4: the code modulo 8, and the sign
   return (bits >> 22 & 7u) | (__float_as_uint(q) >> 28 & 8u);
+}
+
+// Scale code of a block; ROTATE: NaN where a rotation has left fp32 (amax infinite or NaN)
+template <bool ROTATE>
+__device__ __forceinline__ uint8_t scale_code(int s, uint32_t amax) {
+  return ROTATE && amax >= 0x7f800000u ? 255 : (uint8_t)(s + 127);
 }
 
 template <int CTRL> __device__ __forceinline__ float quad(float v) {
@@ -195,7 +202,7 @@ __global__ __launch_bounds__(kThreadsQ) void k_mx4_rows(RowsArgs a) {
     if (row[j] < a.rows) {
       const int64_t u = row[j] * a.units + (col[j] >> 3);
       *(uint32_t*)(a.codes + 4 * u) = w;
-      if ((threadIdx.x & 3) == 0) a.scales[u >> 2] = (uint8_t)(s + 127);
+      if ((threadIdx.x & 3) == 0) a.scales[u >> 2] = scale_code<ROTATE>(s, m);
     }
   }
 }
@@ -313,7 +320,7 @@ __global__ __launch_bounds__(kThreadsQ) void k_mx4_cols(ColsArgs a) {
       }
     }
     sc[2 * pc + h][rb] = make_uint4(w[0], w[1], w[2], w[3]);
-    ss[2 * pc + h][rb] = (uint8_t)(s + 127);
+    ss[2 * pc + h][rb] = scale_code<ROTATE>(s, m);
   }
   __syncthreads();
   const int padded = round_up128(a.rows);

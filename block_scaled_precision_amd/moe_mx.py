@@ -938,7 +938,8 @@ def mx4_quantize(src: torch.Tensor, transpose: bool = False, signs: torch.Tensor
     along the rows: (codes [.., cols, K/2], scales [.., cols, K/32]).
 
     signs [32] fp32 of +1 and -1 rotates every block of 32 by a Hadamard matrix (both
-    operands of a product alike); random, uint8 of src's shape, rounds stochastically and
+    operands of a product alike; a block whose sums leave fp32, which takes magnitudes of
+    2^123 and more, gets the NaN scale); random, uint8 of src's shape, rounds stochastically and
     saturates nothing; without it the nearest code is taken, as mx_quantize does."""
     return _plan_quantize4(src, transpose, signs, random, codes, scales, stream).launch(stream)
 

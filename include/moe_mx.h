@@ -362,7 +362,9 @@ moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_tensors_t* 
  *            rotated first: v <- H (signs * v) / sqrt(32) with the 32-point Hadamard matrix
  *            (butterflies at distance 1, 2, 4, 8, 16 in fp32, then the factor, rounded to
  *            fp32).  Operands rotated with the same signs have the product of the unrotated
- *            ones; a few large values no longer set the scale of their whole block.
+ *            ones; a few large values no longer set the scale of their whole block.  Blocks
+ *            of magnitudes below 2^123 always stay inside fp32; one whose sums overflow gets
+ *            scale 255 (NaN) and unspecified codes.
  *   random   [batch, rows, cols] bytes (rows cols apart), or NULL.
  *            Without: as mx_quantize with MX_E2M1: scale 2^s, s = floor(log2 amax) - 2 (at
  *            least -127), nearest code, ties to even, saturating.

@@ -55,13 +55,17 @@ def operand(src: np.ndarray, transpose: bool = False, signs=None, random=None):
     pad = [(0, 0)] * (v.ndim - 1) + [(0, -v.shape[-1] % K_STEP)]
     v = np.pad(v, pad)
     blocks = v.reshape(v.shape[:-1] + (-1, mx.BLOCK))
+    over = np.zeros(blocks.shape[:-1], dtype=bool)
     if signs is not None:
-        blocks = rotate(blocks, signs).astype(np.float64)
+        with np.errstate(over="ignore", invalid="ignore"):
+            blocks = rotate(blocks, signs).astype(np.float64)
+        over = ~np.isfinite(blocks).all(-1)  # left fp32: the NaN scale, codes unspecified
+        blocks[over] = 0.0
     if random is None:
         codes, scales = mx.quantize(blocks.reshape(v.shape), "e2m1")
     else:
         codes, scales = round_stochastically(blocks, np.pad(random, pad).reshape(blocks.shape).astype(np.int64))
-    return mx.pack(codes.reshape(v.shape), "e2m1"), scales
+    return mx.pack(codes.reshape(v.shape), "e2m1"), np.where(over, 255, scales).astype(np.uint8)
 
 
 def values(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
