@@ -34,9 +34,7 @@
 // there are many sequences -> 8.2, sums over lanes by register moves -> 7.
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
-#include <type_traits>
-
+#include "balance_plan.h"
 #include "copy_ring.h"
 #include "internal.h"
 
@@ -44,11 +42,7 @@ namespace moe_mx {
 
 namespace {
 
-constexpr int kThreadsB = 256;
 constexpr int kOneThreads = 1024;
-// Tokens up to which the loss takes one launch of one workgroup, for up to
-// kOneSeqs sequences
-constexpr int kOneTokens = 128, kOneSeqs = 4;
 constexpr float kNegInf = -__builtin_inff();
 
 typedef float v4 __attribute__((ext_vector_type(4)));
@@ -401,7 +395,6 @@ template <class T> __device__ __forceinline__ T take(T* p) {
 // One workgroup of 1024 threads per COLS experts and sequence, the other lanes along the
 // sequence's chunks.  All it does is wait: for the offsets, the
 // slots, the others and what those left, each once.
-constexpr int kFinishThreads = 1024;
 static_assert(kFinishThreads == 64 * kSumWaves && kOneThreads == 64 * kSumWaves, "block_sum");
 template <int COLS>
 __global__ __launch_bounds__(kFinishThreads) void k_balance_finish(BalanceArgs a) {
@@ -623,90 +616,6 @@ __global__ __launch_bounds__(kThreadsB) void k_balance_grad(BalanceGradArgs a) {
 
 // ------------------------------------------------------------------- host --
 
-// Chunks of a loss of up to kChunkRows rows each; longer ones have more chunks, so that no sum
-// in fp32 has more than 64 rows (of 4 groups, at 64 lanes a row) and as many groups.
-constexpr int kMaxChunks = 512, kChunkRows = 256;
-
-// Lanes per row and pieces per lane: calls F with them as compile-time constants.  The loss
-// spends its time on what a row costs beside its values, reductions and a logarithm, so that
-// 16 lanes a row, four rows a wave, take it as far as their registers reach (65536 x 128: 16
-// lanes 12.4 us, 32 lanes 15.5); the gradient moves more bytes and wants more loads under way.
-template <bool LOSS, class F>
-void for_row_shape(bool vec, int E, F f) {
-#define MOE_ROW_SHAPE(V, L, P) \
-  if (E <= V * L * P) return f(std::integral_constant<int, V>(), std::integral_constant<int, L>(), \
-                               std::integral_constant<int, P>())
-  if (vec && LOSS) {
-    MOE_ROW_SHAPE(4, 16, 1);
-    MOE_ROW_SHAPE(4, 16, 2);
-    MOE_ROW_SHAPE(4, 16, 3);
-    MOE_ROW_SHAPE(4, 16, 4);
-    MOE_ROW_SHAPE(4, 16, 6);
-    MOE_ROW_SHAPE(4, 32, 4);
-    MOE_ROW_SHAPE(4, 32, 6);
-    MOE_ROW_SHAPE(4, 32, 8);
-  } else if (vec) {
-    MOE_ROW_SHAPE(4, 16, 1);
-    MOE_ROW_SHAPE(4, 32, 1);
-    MOE_ROW_SHAPE(4, 16, 3);
-    MOE_ROW_SHAPE(4, 32, 2);
-    MOE_ROW_SHAPE(4, 32, 3);
-    MOE_ROW_SHAPE(4, 64, 2);
-    MOE_ROW_SHAPE(4, 64, 3);
-    MOE_ROW_SHAPE(4, 64, 4);
-  } else {
-    MOE_ROW_SHAPE(1, 16, 1);
-    MOE_ROW_SHAPE(1, 32, 1);
-    MOE_ROW_SHAPE(1, 64, 1);
-    MOE_ROW_SHAPE(1, 64, 2);
-    MOE_ROW_SHAPE(1, 64, 4);
-    MOE_ROW_SHAPE(1, 64, 8);
-    MOE_ROW_SHAPE(1, 64, 16);
-  }
-#undef MOE_ROW_SHAPE
-}
-
-struct BalancePlan {
-  bool one;
-  int rows, chunks;
-  int cols, blocks;  // experts of a workgroup of the second launch, workgroups per sequence
-  size_t sum_p, sum_c, sum_z, sum_n, part, part_z, arrived, total;
-};
-
-BalancePlan balance_plan(int32_t T, int32_t E, int32_t S) {
-  BalancePlan f = {};
-  f.one = T <= kOneTokens && S <= kOneSeqs;
-  if (f.one) return f;
-  f.rows = (int)std::min<size_t>(align_up(std::max<size_t>(((size_t)T + kMaxChunks - 1) / kMaxChunks, 1), 16), kChunkRows);
-  f.chunks = (T + f.rows - 1) / f.rows;
-  f.cols = f.chunks / S <= 64 ? 64 : 16;
-  f.blocks = (E + f.cols - 1) / f.cols;
-  const size_t slots = (size_t)f.chunks + S;
-  size_t o = 0;
-  auto take = [&](size_t bytes) {
-    const size_t r = o;
-    o = align_up(o + bytes, 256);
-    return r;
-  };
-  f.sum_p = take(slots * E * 4);
-  f.sum_c = take(slots * E * 4);
-  f.sum_z = take(slots * 4);
-  f.sum_n = take(slots * 4);
-  f.part = take((size_t)S * f.blocks * 8);
-  f.part_z = take((size_t)S * 8);
-  f.arrived = take(4);
-  f.total = o;
-  return f;
-}
-
-bool sizes_valid(int32_t T, int32_t E, int32_t k, int32_t S) {
-  return T >= 0 && E >= 1 && E <= kMaxExperts && k >= 1 && k <= E && S >= 1;
-}
-// (the second launch has S + S E / 64 workgroups of 1024 threads at most, and a launch fewer
-// than 2^32 threads)
-bool sizes_supported(int32_t T, int32_t E, int32_t k, int32_t S) {
-  return (int64_t)T * k <= (int64_t)1 << 30 && T <= 1 << 30 && S <= 1 << 20 && (int64_t)S * E <= (int64_t)1 << 27;
-}
 bool aligned_b(const void* p, uintptr_t n) { return (uintptr_t)p % n == 0; }
 bool matrix16(const float* p, int64_t ld, int32_t E) { return aligned_b(p, 16) && ld % 4 == 0 && E % 4 == 0; }
 moe_status_t launched_b() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
@@ -721,7 +630,7 @@ constexpr int64_t kStreamGrad = 16 << 20;
 using namespace moe_mx;
 
 extern "C" size_t moe_balance_workspace_bytes(int32_t T, int32_t E, int32_t S) {
-  if (!sizes_valid(T, E, 1, S) || !sizes_supported(T, E, 1, S)) return 0;
+  if (!balance_sizes_valid(T, E, 1, S) || !balance_sizes_supported(T, E, 1, S)) return 0;
   return balance_plan(T, E, S).total;
 }
 
@@ -729,8 +638,8 @@ extern "C" moe_status_t moe_balance(const float* logits, int64_t logits_ld, cons
                                     const uint8_t* mask, const int32_t* seq_offsets, int32_t T, int32_t E, int32_t k,
                                     int32_t S, float* loss, int32_t* counts, int32_t* tokens, float* lse,
                                     void* workspace, size_t workspace_bytes, hipStream_t stream) {
-  if (!sizes_valid(T, E, k, S) || (!seq_offsets && S != 1)) return MOE_ERR_INVALID_ARG;
-  if (!sizes_supported(T, E, k, S)) return MOE_ERR_UNSUPPORTED;
+  if (!balance_sizes_valid(T, E, k, S) || (!seq_offsets && S != 1)) return MOE_ERR_INVALID_ARG;
+  if (!balance_sizes_supported(T, E, k, S)) return MOE_ERR_UNSUPPORTED;
   if (!loss || !counts || !tokens || !aligned_b(loss, 4) || !aligned_b(counts, 4) || !aligned_b(tokens, 4) ||
       !aligned_b(seq_offsets, 4))
     return MOE_ERR_INVALID_ARG;
@@ -789,8 +698,8 @@ extern "C" moe_status_t moe_balance_backward(const float* dloss, const float* lo
                                              const int32_t* seq_offsets, int32_t T, int32_t E, int32_t k, int32_t S,
                                              const float* add, int64_t add_ld, float* dlogits, int64_t dlogits_ld,
                                              hipStream_t stream) {
-  if (!sizes_valid(T, E, k, S) || (!seq_offsets && S != 1)) return MOE_ERR_INVALID_ARG;
-  if (!sizes_supported(T, E, k, S)) return MOE_ERR_UNSUPPORTED;
+  if (!balance_sizes_valid(T, E, k, S) || (!seq_offsets && S != 1)) return MOE_ERR_INVALID_ARG;
+  if (!balance_sizes_supported(T, E, k, S)) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!dloss || !logits || !counts || !tokens || !lse || !dlogits || logits_ld < E || dlogits_ld < E ||
       (add && add_ld < E))
@@ -807,10 +716,8 @@ extern "C" moe_status_t moe_balance_backward(const float* dloss, const float* lo
   const bool stream_out = (int64_t)T * E * 4 >= kStreamGrad;
   for_row_shape<false>(vec, E, [&](auto V, auto L, auto P) {
     constexpr int G = kThreadsB / L.value;
-    // rows per group: one where that leaves the chip room, more once there are
-    // workgroups enough
-    a.per = (int)std::min<int64_t>(16, std::max<int64_t>(1, (int64_t)T / (G * 2048)));
-    const int64_t blocks = ((int64_t)T + (int64_t)G * a.per - 1) / ((int64_t)G * a.per);
+    a.per = balance_grad_rows(T, G);
+    const int64_t blocks = balance_grad_blocks(T, G);
     if (stream_out) k_balance_grad<V.value, L.value, P.value, true><<<(unsigned)blocks, kThreadsB, 0, stream>>>(a);
     else k_balance_grad<V.value, L.value, P.value, false><<<(unsigned)blocks, kThreadsB, 0, stream>>>(a);
   });
