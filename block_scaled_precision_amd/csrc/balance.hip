@@ -37,6 +37,7 @@
 #include "balance_plan.h"
 #include "copy_ring.h"
 #include "internal.h"
+#include "mx_device.h"
 
 namespace moe_mx {
 
@@ -57,16 +58,13 @@ __device__ __forceinline__ void lds_barrier() {
 
 // ------------------------------------------------------- rows in registers --
 
-template <int CTRL> __device__ __forceinline__ float dpp_mov(float v) {
-  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
-}
 // Reduction over a group of L neighbouring lanes; every lane gets the same bits.
 template <int L, class Op>
 __device__ __forceinline__ float group_reduce(float v, Op op) {
-  v = op(v, dpp_mov<0xb1>(v));   // quad_perm 1,0,3,2
-  v = op(v, dpp_mov<0x4e>(v));   // quad_perm 2,3,0,1
-  v = op(v, dpp_mov<0x141>(v));  // row_half_mirror
-  v = op(v, dpp_mov<0x140>(v));  // row_mirror
+  v = op(v, lane_move<0xb1>(v));   // quad_perm 1,0,3,2
+  v = op(v, lane_move<0x4e>(v));   // quad_perm 2,3,0,1
+  v = op(v, lane_move<0x141>(v));  // row_half_mirror
+  v = op(v, lane_move<0x140>(v));  // row_mirror
   if (L >= 32) v = op(v, __shfl_xor(v, 16));
   if (L >= 64) v = op(v, __shfl_xor(v, 32));
   return v;
@@ -348,14 +346,11 @@ __device__ __forceinline__ Sums operator+(const Sums& x, const Sums& y) {
 }
 // Sum over 16 neighbouring lanes, in each of them: by moves within the row of lanes, which
 // cost an instruction each where a shuffle costs a hundred cycles
-template <int CTRL> __device__ __forceinline__ int32_t moved(int32_t v) {
-  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true);
-}
 template <int CTRL> __device__ __forceinline__ double moved(double v) {
-  return __hiloint2double(moved<CTRL>(__double2hiint(v)), moved<CTRL>(__double2loint(v)));
+  return __hiloint2double(lane_move<CTRL>(__double2hiint(v)), lane_move<CTRL>(__double2loint(v)));
 }
 template <int CTRL> __device__ __forceinline__ Sums add_moved(const Sums& v) {
-  return v + Sums{moved<CTRL>(v.balance), moved<CTRL>(v.z), moved<CTRL>(v.n), moved<CTRL>(v.used)};
+  return v + Sums{moved<CTRL>(v.balance), moved<CTRL>(v.z), lane_move<CTRL>(v.n), lane_move<CTRL>(v.used)};
 }
 __device__ __forceinline__ Sums sum16(Sums v) {
   v = add_moved<0xb1>(v);      // quad_perm 1,0,3,2
@@ -616,8 +611,7 @@ __global__ __launch_bounds__(kThreadsB) void k_balance_grad(BalanceGradArgs a) {
 
 // ------------------------------------------------------------------- host --
 
-bool aligned_b(const void* p, uintptr_t n) { return (uintptr_t)p % n == 0; }
-bool matrix16(const float* p, int64_t ld, int32_t E) { return aligned_b(p, 16) && ld % 4 == 0 && E % 4 == 0; }
+bool matrix16(const float* p, int64_t ld, int32_t E) { return aligned(p, 16) && ld % 4 == 0 && E % 4 == 0; }
 moe_status_t launched_b() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 // Gradients from this size on are stored past the caches.
@@ -640,15 +634,15 @@ extern "C" moe_status_t moe_balance(const float* logits, int64_t logits_ld, cons
                                     void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (!balance_sizes_valid(T, E, k, S) || (!seq_offsets && S != 1)) return MOE_ERR_INVALID_ARG;
   if (!balance_sizes_supported(T, E, k, S)) return MOE_ERR_UNSUPPORTED;
-  if (!loss || !counts || !tokens || !aligned_b(loss, 4) || !aligned_b(counts, 4) || !aligned_b(tokens, 4) ||
-      !aligned_b(seq_offsets, 4))
+  if (!loss || !counts || !tokens || !aligned(loss, 4) || !aligned(counts, 4) || !aligned(tokens, 4) ||
+      !aligned(seq_offsets, 4))
     return MOE_ERR_INVALID_ARG;
-  if (T > 0 && (!logits || !topk_ids || !lse || logits_ld < E || !aligned_b(logits, 4) || !aligned_b(topk_ids, 4) ||
-                !aligned_b(lse, 4)))
+  if (T > 0 && (!logits || !topk_ids || !lse || logits_ld < E || !aligned(logits, 4) || !aligned(topk_ids, 4) ||
+                !aligned(lse, 4)))
     return MOE_ERR_INVALID_ARG;
   const BalancePlan f = balance_plan(T, E, S);
   if (f.total > 0 && (!workspace || workspace_bytes < f.total)) return MOE_ERR_WORKSPACE;
-  if (f.total > 0 && !aligned_b(workspace, 256)) return MOE_ERR_INVALID_ARG;
+  if (f.total > 0 && !aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
   const moe_status_t st = check_arch();
   if (st != MOE_OK) return st;
   BalanceArgs a = {};
@@ -706,7 +700,7 @@ extern "C" moe_status_t moe_balance_backward(const float* dloss, const float* lo
     return MOE_ERR_INVALID_ARG;
   for (const void* q : {(const void*)dloss, (const void*)logits, (const void*)counts, (const void*)tokens,
                         (const void*)lse, (const void*)seq_offsets, (const void*)add, (const void*)dlogits})
-    if (!aligned_b(q, 4)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(q, 4)) return MOE_ERR_INVALID_ARG;
   const moe_status_t st = check_arch();
   if (st != MOE_OK) return st;
   BalanceGradArgs a = {dloss, logits, logits_ld, counts, tokens, lse, seq_offsets, T, E, k, S, 1,

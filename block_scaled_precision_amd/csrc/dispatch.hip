@@ -379,7 +379,6 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_grad(const int32_t* 
 
 bool src_ok(moe_src_t d) { return d == MOE_SRC_BF16 || d == MOE_SRC_FP32; }
 int64_t elem_size(moe_src_t d) { return d == MOE_SRC_BF16 ? 2 : 4; }
-bool aligned(const void* p, int64_t n) { return (uintptr_t)p % (uintptr_t)n == 0; }
 // a row matrix that 16-byte pieces can walk
 bool pieces16(const void* p, int64_t ld, int64_t es) { return aligned(p, 16) && ld * es % 16 == 0; }
 

@@ -107,24 +107,20 @@ __device__ __forceinline__ uint32_t quant8_e2m1(const uint4& v, float inv) {
   for (int i = 0; i < 8; ++i) q[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) * inv;
   return e2m1_codes(q);
 }
-// largest magnitude (fp32 bits) of 8 bf16 values
+// largest magnitude (fp32 bits) of 2 N bf16 values
+template <int N> __device__ __forceinline__ uint32_t amax_bf16(const uint32_t (&w)[N]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int q = 0; q < N; ++q) m = max(m, max((w[q] << 16) & 0x7fffffffu, w[q] & 0x7fff0000u));
+  return m;
+}
 __device__ __forceinline__ uint32_t amax8(const uint4& v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) m = max(m, max((w[q] << 16) & 0x7fffffffu, w[q] & 0x7fff0000u));
-  return m;
+  return amax_bf16(w);
 }
-template <int CTRL> __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
-  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true));
-}
-// largest magnitude (fp32 bits) of 16 bf16 values
 __device__ __forceinline__ uint32_t amax16(const uint4& lo, const uint4& hi) {
   const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int q = 0; q < 8; ++q) m = max(m, max((w[q] << 16) & 0x7fffffffu, w[q] & 0x7fff0000u));
-  return m;
+  return amax_bf16(w);
 }
 
 template <int ACT, int WF>
@@ -307,7 +303,7 @@ __global__ __launch_bounds__(64 * W) void k_linear_few(FcArgs p) {
   if (ACT == kRows4) {
     // (4 neighbouring lanes hold a block, and go on together: K % 128 == 0)
     auto quantize = [&](int i, const uint4& v) {
-      const int s = block_exponent<1>(quad_max<0x4e>(quad_max<0xb1>(amax8(v))));
+      const int s = block_exponent<1>(quad_max(amax8(v)));
       ((uint32_t*)rows4)[i] = quant8_e2m1(v, exp2_neg(s));
       if ((i & 3) == 0) scales4[i >> 2] = (uint8_t)(s + 127);
     };

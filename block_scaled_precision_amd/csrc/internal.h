@@ -20,6 +20,7 @@ constexpr int kTokensPerRouteBlock = 64;  // tokens per block in the permutation
 constexpr int kMaxExperts = 1024;         // limit of the wave-level top-k / scan design
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+inline bool aligned(const void* p, int64_t n) { return (uintptr_t)p % (uintptr_t)n == 0; }
 
 // Checks that the current device is gfx950 (cached per device).
 moe_status_t check_arch();

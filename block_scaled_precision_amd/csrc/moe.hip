@@ -133,7 +133,6 @@ static int64_t grid_for(int64_t n, int64_t per_block, int64_t cap) {
 
 // ------------------------------------------------------------ layouts ----
 
-static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // Routed GEMMs run tiled (LDS-staged, M-tiles of up to kTiledRows rows) when the
 // activations are MXFP8, H and I are multiples of kTiledKMultiple and the
@@ -307,11 +306,11 @@ static moe_status_t validate(const moe_problem_t* p, const moe_tensors_t* t) {
     if (p->I_shared > 0 && (!t->ws1 || !t->ws1_scale || !t->ws2 || !t->ws2_scale)) return MOE_ERR_INVALID_ARG;
     const void* ptrs[] = {t->x, t->y, t->w1, t->w1_scale, t->w2, t->w2_scale};
     for (const void* q : ptrs)
-      if (!aligned16(q)) return MOE_ERR_INVALID_ARG;
+      if (!aligned(q, 16)) return MOE_ERR_INVALID_ARG;
     if (p->I_shared > 0) {
       const void* sp[] = {t->ws1, t->ws1_scale, t->ws2, t->ws2_scale};
       for (const void* q : sp)
-        if (!aligned16(q)) return MOE_ERR_INVALID_ARG;
+        if (!aligned(q, 16)) return MOE_ERR_INVALID_ARG;
     }
   }
   // valid, but outside what the kernels implement
@@ -375,7 +374,7 @@ extern "C" moe_status_t mx_quantize(const void* src, moe_src_t src_dtype, int64_
   if (src_dtype != MOE_SRC_BF16 && src_dtype != MOE_SRC_FP32) return MOE_ERR_INVALID_ARG;
   if (fmt != MX_E2M1 && fmt != MX_E3M2 && fmt != MX_E4M3) return MOE_ERR_INVALID_ARG;
   if (rows > 0 && (!src || !codes || !scales)) return MOE_ERR_INVALID_ARG;
-  if (rows > 0 && !aligned16(codes)) return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && !aligned(codes, 16)) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
   moe_status_t a = check_arch();
   if (a != MOE_OK) return a;
@@ -502,7 +501,7 @@ extern "C" moe_status_t mx_gemm(const void* a, const uint8_t* a_scale, int64_t M
   if (M > INT32_MAX || N > INT32_MAX || K > INT32_MAX || (double)M * N > 9.0e15) return MOE_ERR_INVALID_ARG;
   if (M > 0) {
     if (!a || !w || !w_scale || !c) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(a) || !aligned16(w) || !aligned16(c) || (a_scale && !aligned16(a_scale)))
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(c, 16) || (a_scale && !aligned(a_scale, 16)))
       return MOE_ERR_INVALID_ARG;
   }
   if (w_fmt == MX_E4M3 || N % 8 || K % 128) return MOE_ERR_UNSUPPORTED;
@@ -593,7 +592,7 @@ moe_status_t check_linear(const mx_linear_problem_t& p, const mx_linear_tensors_
     return MOE_ERR_INVALID_ARG;
   for (const void* q : {t.a, (const void*)t.a_scale, (const void*)t.w, (const void*)t.w_scale, t.mul, t.residual,
                         (const void*)t.out})
-    if (!aligned16(q)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(q, 16)) return MOE_ERR_INVALID_ARG;
   if (t.bias && (uintptr_t)t.bias % (p.bias_dtype == MOE_SRC_BF16 ? 2 : 4)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
@@ -604,8 +603,8 @@ FcArgs linear_args(const mx_linear_problem_t& p, const mx_linear_tensors_t& t, c
   g.epi.bias = t.bias;
   // (a bias row is N elements, N % 8 == 0: every row is as aligned as the first)
   g.epi.bias_kind = !t.bias ? kBiasNone
-                    : p.bias_dtype == MOE_SRC_FP32 ? (aligned16(t.bias) ? kBiasF32 : kBiasF32Any)
-                                                   : (aligned16(t.bias) ? kBiasBf16 : kBiasBf16Any);
+                    : p.bias_dtype == MOE_SRC_FP32 ? (aligned(t.bias, 16) ? kBiasF32 : kBiasF32Any)
+                                                   : (aligned(t.bias, 16) ? kBiasBf16 : kBiasBf16Any);
   g.epi.fn = p.fn;
   g.epi.mul = (const uint16_t*)t.mul;
   g.epi.residual = (const uint16_t*)t.residual;

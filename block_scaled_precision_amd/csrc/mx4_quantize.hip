@@ -78,12 +78,6 @@ __device__ __forceinline__ uint8_t scale_code(int s, uint32_t amax) {
   return ROTATE && amax >= 0x7f800000u ? 255 : (uint8_t)(s + 127);
 }
 
-template <int CTRL> __device__ __forceinline__ float quad(float v) {
-  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xf, 0xf, true));
-}
-template <int CTRL> __device__ __forceinline__ uint32_t quad(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
-}
 
 // ------------------------------------------------------------- along rows --
 
@@ -174,20 +168,19 @@ __global__ __launch_bounds__(kThreadsQ) void k_mx4_rows(RowsArgs a) {
       // distances 8 and 16: the neighbouring lanes
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float o = quad<0xb1>(x[i]);
+        const float o = lane_move<0xb1>(x[i]);
         x[i] = threadIdx.x & 1 ? o - x[i] : x[i] + o;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float o = quad<0x4e>(x[i]);
+        const float o = lane_move<0x4e>(x[i]);
         x[i] = (threadIdx.x & 2 ? o - x[i] : x[i] + o) * kHadamard;
       }
     }
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-    m = max(m, quad<0xb1>(m));
-    m = max(m, quad<0x4e>(m));
+    m = quad_max(m);
     const int s = exponent4<RANDOM>(m);
     const float inv = exp2_neg(s);
     uint32_t w = 0;
@@ -410,7 +403,6 @@ __global__ __launch_bounds__(kThreadsQ) void k_mx4_expand(const uint32_t* __rest
 constexpr int64_t kMaxDim = (int64_t)1 << 30;  // rows, columns, matrices
 // Workgroups of one launch, which has fewer than 2^32 threads; what has more takes several.
 constexpr int64_t kMaxBlocks = (int64_t)1 << 23;
-bool aligned_to(const void* p, int64_t n) { return (uintptr_t)p % (uintptr_t)n == 0; }
 
 // F with the four choices as compile-time constants
 template <class F>
@@ -456,8 +448,8 @@ extern "C" moe_status_t mx4_quantize(const void* src, moe_src_t src_dtype, int64
   const bool bf16 = src_dtype == MOE_SRC_BF16;
   const int64_t es = bf16 ? 2 : 4;
   if (batch == 0 || rows == 0) return MOE_OK;
-  if (!src || !codes || !scales || !aligned_to(src, es) || !aligned_to(codes, 16) || !aligned_to(scales, 4) ||
-      !aligned_to(signs, 4))
+  if (!src || !codes || !scales || !aligned(src, es) || !aligned(codes, 16) || !aligned(scales, 4) ||
+      !aligned(signs, 4))
     return MOE_ERR_INVALID_ARG;
   const moe_status_t st = check_arch();
   if (st != MOE_OK) return st;
@@ -466,7 +458,7 @@ extern "C" moe_status_t mx4_quantize(const void* src, moe_src_t src_dtype, int64
     // matrices of a launch and column tiles (tiles_r <= 2^22)
     const int64_t nb = std::max<int64_t>(kMaxBlocks / (tiles_r * tiles_c), 1), nc = std::min(tiles_c, kMaxBlocks / tiles_r);
     const int64_t padded = (rows + 127) / 128 * 128;
-    const bool vec = cols % 2 == 0 && src_ld % 2 == 0 && aligned_to(src, 2 * es) && (!random || aligned_to(random, 2));
+    const bool vec = cols % 2 == 0 && src_ld % 2 == 0 && aligned(src, 2 * es) && (!random || aligned(random, 2));
     for (int64_t b = 0; b < batch; b += nb)
       for (int64_t c = 0; c < tiles_c; c += nc) {
         const int64_t n = std::min(nc, tiles_c - c);
@@ -481,8 +473,8 @@ extern "C" moe_status_t mx4_quantize(const void* src, moe_src_t src_dtype, int64
       }
   } else {
     const int64_t all = batch * rows, units = (cols + 127) / 128 * 16, nr = kMaxBlocks * (kThreadsQ * kUnits) / units;
-    const bool vec = cols % 8 == 0 && src_ld * es % 16 == 0 && aligned_to(src, 16) &&
-                     (!random || aligned_to(random, 8));
+    const bool vec = cols % 8 == 0 && src_ld * es % 16 == 0 && aligned(src, 16) &&
+                     (!random || aligned(random, 8));
     for (int64_t r = 0; r < all; r += nr) {
       RowsArgs a = {(const char*)src + r * src_ld * es, std::min(nr, all - r), src_ld, (int)cols, (int)units, signs,
                     random ? random + r * cols : nullptr, codes + 4 * r * units, scales + r * units / 4};
@@ -504,10 +496,10 @@ extern "C" moe_status_t mx4_dequantize(const uint8_t* codes, const uint8_t* scal
   const bool bf16 = dst_dtype == MOE_SRC_BF16;
   const int64_t es = bf16 ? 2 : 4;
   if (rows == 0) return MOE_OK;
-  if (!codes || !scales || !dst || !aligned_to(codes, 4) || !aligned_to(dst, es)) return MOE_ERR_INVALID_ARG;
+  if (!codes || !scales || !dst || !aligned(codes, 4) || !aligned(dst, es)) return MOE_ERR_INVALID_ARG;
   const moe_status_t st = check_arch();
   if (st != MOE_OK) return st;
-  const bool vec = dst_ld * es % 16 == 0 && aligned_to(dst, 16);
+  const bool vec = dst_ld * es % 16 == 0 && aligned(dst, 16);
   const int64_t total = rows * (cols / 8);
   const unsigned blocks = (unsigned)std::min<int64_t>((total + kThreadsQ - 1) / kThreadsQ, 1 << 16);
 #define MX4_VALUES(B, V)                                                                                          \

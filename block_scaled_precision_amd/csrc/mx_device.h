@@ -141,13 +141,26 @@ __device__ __forceinline__ float act_mul(float g, float u) {
   return ACT == MOE_FN_SILU ? silu_mul_fast(g, u) : gated_act(ACT, g, u);
 }
 
-// Maximum over the 16 lanes of a DPP row (lanes 16r .. 16r+15).
+// The value of another lane of the DPP row (16 lanes) that CTRL names.
+template <int CTRL> __device__ __forceinline__ int32_t lane_move(int32_t v) {
+  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true);
+}
+template <int CTRL> __device__ __forceinline__ uint32_t lane_move(uint32_t v) {
+  return (uint32_t)lane_move<CTRL>((int32_t)v);
+}
+template <int CTRL> __device__ __forceinline__ float lane_move(float v) {
+  return __int_as_float(lane_move<CTRL>(__float_as_int(v)));
+}
+
+// Maximum over 4 neighbouring lanes, and over the 16 of a DPP row (lanes 16r .. 16r+15).
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, lane_move<0xb1>(v));    // quad_perm 1,0,3,2
+  return max(v, lane_move<0x4e>(v));  // quad_perm 2,3,0,1
+}
 __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xb1, 0xf, 0xf, true));   // quad_perm 1,0,3,2
-  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4e, 0xf, 0xf, true));   // quad_perm 2,3,0,1
-  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x124, 0xf, 0xf, true));  // row_ror 4
-  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x128, 0xf, 0xf, true));  // row_ror 8
-  return v;
+  v = quad_max(v);
+  v = max(v, lane_move<0x124>(v));    // row_ror 4
+  return max(v, lane_move<0x128>(v));  // row_ror 8
 }
 
 }  // namespace moe_mx
