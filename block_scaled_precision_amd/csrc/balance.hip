@@ -172,7 +172,7 @@ struct BalanceArgs {
   // slots chunk + sequence of the chunks' sums (a chunk and a sequence that meet
   // never share one with another pair, as both only go up), and what the
   // second launch leaves
-  int rows, chunks;       // rows per chunk, chunks
+  int rows;               // per chunk
   float* sum_p;           // [chunks + S, E]
   int32_t* sum_c;         // [chunks + S, E]
   float* sum_z;           // [chunks + S]
@@ -668,7 +668,6 @@ extern "C" moe_status_t moe_balance(const float* logits, int64_t logits_ld, cons
   }
   char* ws = (char*)workspace;
   a.rows = f.rows;
-  a.chunks = f.chunks;
   a.sum_p = (float*)(ws + f.sum_p);
   a.sum_c = (int32_t*)(ws + f.sum_c);
   a.sum_z = (float*)(ws + f.sum_z);

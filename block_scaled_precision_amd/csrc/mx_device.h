@@ -55,7 +55,7 @@ __device__ __forceinline__ int block_exponent(uint32_t amax_bits) {
   return s < -127 ? -127 : s;  // E <= 254 keeps s <= 127 - emax
 }
 
-// 2**-s as an exact fp32 (|s| <= 127 and s <= 125 in use, so always normal).
+// 2**-s as an exact fp32 (-127 <= s <= 126 in use, so always normal).
 __device__ __forceinline__ float exp2_neg(int s) { return __uint_as_float((uint32_t)(127 - s) << 23); }
 
 // Nearest element code of q (already divided by the block scale).
