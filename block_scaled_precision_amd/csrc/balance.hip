@@ -26,12 +26,15 @@
 //
 // Measured (MI355X, warm; bytes at 5 TB/s in brackets): 65536 x 256 and what is added to its
 // gradient 37 us [40]: bound by memory.  The loss is bound by what follows one after the
-// other, memory's latencies of about a microsecond in both launches: 65536 x 128 13 + 6
-// us [7], 8192 x 384 in 13 sequences 7.5 + 7 [2.6], 64 x 384 7 in one launch, of which a launch
-// that does nothing takes 2.  On the way there: the offsets through LDS and rows without regard
-// to sequences 9.0 -> 7.5 us (8192 x 384), 16 lanes a row and a cheaper exponential 15.5 -> 12.5
-// (65536 x 128), no fences in the second launch 16.6 -> 11.3, fewer workgroups in it where
-// there are many sequences -> 8.2, sums over lanes by register moves -> 7.
+// other: 65536 x 128 13 + 6 us [7], 8192 x 384 in 13 sequences 7.5 + 7 [2.6], 64 x 384 7 in one
+// launch, of which a launch that does nothing takes 2.  In the first launch of 65536 x 128 a wave
+// waits for half of its 23700 cycles, as a chunk's rows come in two batches, load, compute, load,
+// compute, and the 1625 vector instructions (25 a value) of the two waves of a SIMD take the
+// other half; in the second and in small calls it is memory's latencies of about a microsecond.
+// On the way there: the offsets through LDS and rows without regard to sequences 9.0 -> 7.5 us
+// (8192 x 384), 16 lanes a row and a cheaper exponential 15.5 -> 12.5 (65536 x 128), no fences in
+// the second launch 16.6 -> 11.3, fewer workgroups in it where there are many sequences -> 8.2,
+// sums over lanes by register moves -> 7.
 #include <hip/hip_runtime.h>
 
 #include "balance_plan.h"

@@ -10,9 +10,13 @@
 // Bound.  With E2M1 on both sides the instruction takes 32 cycles, half of E4M3's, and moves
 // half the bytes, so that everything around it counts twice.  On values of any size registers
 // alone reach 5.8 to 6.2 PFLOP/s (the clock gives way to power; zeros reach 9.7).  A wave that
-// has its SIMD to itself pays 4.5 cycles for each instruction of its own beside its MFMAs; LDS
-// gives 128 bytes a cycle, of which copies and fragments take 3/4 of a 256-row tile's time and
-// all of a 128-row tile's.  What each choice is for:
+// has its SIMD to itself pays for each instruction of its own beside its MFMAs, and that is what
+// bounds a stage of 256 k: 2680 cycles with 256 rows for 2048 of MFMAs, 1820 with 128 rows for
+// 1024, beside which it has 33 vector, 89 scalar, 29 LDS and 14 copy instructions, some 4.5
+// cycles each (counters; 26 of the scalar ones set M0 for the copies).  LDS is busy for a quarter
+// of the time, a quarter of that with conflicts.  Waits (first stages, epilogues, barriers) take
+// a fifth of a wave's time, an item's epilogue and what stands around it 10600 cycles with 128
+// rows.  What each choice is for:
 // - Four waves, one per SIMD, of 32 MSUB x 128 each: the largest pieces of the accumulator, so
 //   the fewest fragments (6 reads for 8 MFMAs with 128 rows, 8 for 16 with 256).  Eight waves
 //   spill (8192^3: 316 us for 304); two workgroups a CU of 128 rows, 128 k a stage, to have one's
@@ -34,11 +38,10 @@
 // - Few dense items of 64 rows split K into ranges, whose fp32 sums a second launch joins.
 //
 // Measured (MI355X, from codes): 8192 x 8192 x 8192 262 us with 256 rows, 4.2 PFLOP/s, 128 rows
-// 310, 64 rows 415; 8192 x 4096 x 7168 121, 143, 183; 65536 rows of 128 experts, 1536 x 4096, 289,
-// 307, 420, with SiLU and a second factor 367 (128 rows).  A 256-row K loop takes 2900 cycles a
-// stage where its MFMAs take 2050.  What is left: epilogues that the next item's products do
-// not overlap (about 4 us of a 128-row item's 25), the padding of a group's last tile, and a
-// launch's last round.
+// 310, 64 rows 415; 8192 x 4096 x 7168 119, 143, 183; 65536 rows of 128 experts, 1536 x 4096, 289,
+// 310, 420 and, 128 rows, with SiLU 338, with a second factor 350, with both 376.  What is left:
+// the instructions beside the MFMAs, epilogues that the next item's products do not overlap (about
+// 5 us of a 128-row item's 21), the padding of a group's last tile, and a launch's last round.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -274,8 +277,9 @@ __device__ __forceinline__ float acc_read(float a) {
   return v;
 }
 // silu of epilogue.h with the hardware's exponential: t is off by |v| + 2 half steps of fp32 for
-// a few, which v t, at most 0.28, leaves below half a step of 1 in the result.  (12 instructions
-// for 30; with silu and a second factor the rows of 128 experts took 446 us, now 392.)
+// a few, which v t, at most 0.28, leaves below half a step of 1 in the result; for v below -87.3
+// (results smaller than 1e-36) t may be 0.  (12 instructions for 30: 65536 rows of 128 experts,
+// with a second factor, took 446 us with it and 392 with this.)
 __device__ __forceinline__ void fn_of(int fn, float (&v)[8]) {
   if (fn == MX_FN_SILU) {
 #pragma unroll

@@ -42,7 +42,8 @@ inline mx_linear_problem_t as_mxfp8(const mx4_linear_problem_t& p) {
 
 // The smallest of the estimated times in microseconds, as linear_kind chooses
 // (linear_plan.h).  Over 82 measured shapes (1 to 76800 rows, dense and 8 to 384 groups) the
-// choice costs 0.8 % more than the best kernel each time, 19 % at most.
+// choice costs 0.7 % more than the best kernel each time, 19 % at most, but for the four of them
+// that take ranges of K, which were not among the kernels measured then.
 //   few rows in place (a step of 1024 K): from codes 0.45 to 0.65, from bf16 to 0.75 up to 8 rows
 //     and to 1.23 from there on; twice that with groups (N = 4096, K = 7168: 1 row 7.2, 16 rows
 //     9.5, 32 rows 15.7; from bf16 7.2, 14.4, 25.7)

@@ -26,11 +26,14 @@
 // per 32 lanes), and the codes are regrouped in LDS into 128 contiguous bytes of each output
 // row.
 //
-// Measured (MI355X; bytes at 5 TB/s in brackets): rows 8192 x 7168 bf16, rotated, 44 us [29],
-// plain 31; values 8192 x 7168 back to bf16 23 [29, part of them from the last-level cache];
+// Measured (MI355X; bytes at 5 TB/s in brackets): rows 8192 x 7168 bf16 31 us [29], rotated 40 [29]
+// (44 where nothing of src is in the last-level cache), at random 49 [41], both 64 [41]; values
+// 8192 x 7168 back to bf16 30 [29] (23 where the codes were just written), to fp32 54 [53];
 // transposed 16 x 1536 x 4096 fp32 108 [90], 4021 x 2048 bf16 rotated 8 [4], 4021 x 4096 rotated
-// and rounded at random 23 [11].  Bound by memory, but for the last, whose 24 instructions a
-// value take 10 us, in a launch that is one round of workgroups: they load, then compute.
+// and rounded at random 22 [11].  Bound by memory without rotation and random bytes; with them by
+// their vector instructions, 11 a value plain, 20 rotated, 35 with both, which are all that a SIMD
+// does along rows; transposed (30 a value) they are three quarters of a CU's time, in a launch that
+// is one round of workgroups, which load, then compute.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

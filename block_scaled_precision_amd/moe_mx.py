@@ -343,9 +343,9 @@ def _operator(planner):
 
 
 class OpCall:
-    """One operator call (moe_permute, moe_unpermute, their gradients,
-    moe_route_backward, mx_linear) with its arguments checked and marshalled and its
-    outputs allocated once, for loops that call it many times on the same
+    """One operator call (moe_permute, moe_unpermute, moe_balance, their gradients,
+    moe_route_backward, mx_linear, mx4_quantize, mx4_dequantize, mx4_linear) with its
+    arguments checked and marshalled and its outputs allocated once, for loops that call it many times on the same
     buffers (their contents may change between calls): each call then costs the
     host only the C call.  The stream is the current one at each call unless
     one is given.  Calling returns the operator's outputs, the same tensors each
