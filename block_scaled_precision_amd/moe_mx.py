@@ -973,7 +973,7 @@ def _plan_dequantize4(codes, scales, dtype=torch.bfloat16, out=None, stream=None
 def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values [.., rows, K] of E2M1 codes [.., rows, K/2] and scales [.., rows, K/32] as
-    bf16 or fp32 (exact in both)."""
+    bf16 or fp32 (exact in both; 2^128 and more is infinite, scale code 255 NaN)."""
     return _plan_dequantize4(codes, scales, dtype, out, stream).launch(stream)
 
 

@@ -373,8 +373,9 @@ moe_status_t mx_linear(const mx_linear_problem_t* p, const mx_linear_tensors_t* 
  *            256 (x - lo) / (hi - lo) > random + 1/2, else lo: with bytes spread evenly, x on
  *            average to within 1/512 of hi - lo.
  * mx4_dequantize -- dst [rows, cols] (bf16 or fp32, rows dst_ld apart) = the values of codes
- *   [rows, cols/2] with scales [rows, cols/32]; exact in both types but for 4 and 6 times
- *   2^127, which are infinite; a scale code of 255 gives NaN.  cols % 32 == 0.
+ *   [rows, cols/2] with scales [rows, cols/32]; exact in both types but for 2^128 and more
+ *   (4 and 6 times 2^126; 2, 3, 4 and 6 times 2^127), which are infinite; a scale code of 255
+ *   gives NaN.  cols % 32 == 0.
  * mx4_linear -- mx_linear with MXFP4 on both sides:
  *     v[m, n]   = sum_k A'[m, k] * W'[g, n, k] + bias[g, n]     (fp32 accumulation)
  *     out[m, n] = bf16_RNE(fn(v[m, n]) * mul[m, n] + residual[m, n])
