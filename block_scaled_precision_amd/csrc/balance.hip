@@ -9,9 +9,10 @@
 //   z       = 1 / n sum_t lse[t]^2
 //   dlogits[t, e] = d_balance E / (S' n_s) p_e (f_e - sum_j f_j p_j)
 //                   + d_z 2 / n lse[t] p_e,     f_e = counts[s, e] / (k n_s)
-// counts take no gradient (the choice of experts is piecewise constant), and since p =
-// exp(logit - lse), the gradient needs one pass over the logits and no second pass
-// over what the loss computed.
+// counts take no gradient (the choice of experts is piecewise constant), and since p is
+// exp(logit - lse) to within a factor of the row, the gradient needs one pass over the logits.
+// The factor (lse's rounding, 2^-24 |lse| and more, and all of log E where |lse| is 2^26)
+// goes with the sum of the row's exponentials, which is taken along with <f, p>.
 //
 // Both directions read the logits once (and write their gradient once).  A row is held in
 // registers by a group of 16, 32 or 64 neighbouring lanes, pieces of 16 bytes each where
@@ -585,16 +586,18 @@ __global__ __launch_bounds__(kThreadsB) void k_balance_grad(BalanceGradArgs a) {
             f[q * V + i] = e < a.E ? (float)a.counts[(int64_t)s * a.E + e] * per_k : 0.f;
           }
       }
-      float dot = 0.f;
+      float dot = 0.f, sum = 0.f;
 #pragma unroll
       for (int i = 0; i < P * V; ++i) {
         r.v[i] = expf(r.v[i] - l);
         dot = fmaf(f[i], r.v[i], dot);
+        sum += r.v[i];
       }
-      dot = group_reduce<L>(dot, Sum());
-      const float zl = kz * l;
+      const float inv = 1.0f / group_reduce<L>(sum, Sum());
+      dot = group_reduce<L>(dot, Sum()) * inv;
+      const float kp = ks * inv, zl = kz * inv * l;
 #pragma unroll
-      for (int i = 0; i < P * V; ++i) ad.v[i] = fmaf(r.v[i], fmaf(ks, f[i] - dot, zl), ad.v[i]);
+      for (int i = 0; i < P * V; ++i) ad.v[i] = fmaf(r.v[i], fmaf(kp, f[i] - dot, zl), ad.v[i]);
     }
 #pragma unroll
     for (int q = 0; q < P; ++q) {
