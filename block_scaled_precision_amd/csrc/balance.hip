@@ -595,9 +595,11 @@ __global__ __launch_bounds__(kThreadsB) void k_balance_grad(BalanceGradArgs a) {
       }
       const float inv = 1.0f / group_reduce<L>(sum, Sum());
       dot = group_reduce<L>(dot, Sum()) * inv;
-      const float kp = ks * inv, zl = kz * inv * l;
+      const float kp = ks * inv, kl = kz * inv;
+      // (kl p first: kl lse may be past fp32's range where p is small, or 0)
 #pragma unroll
-      for (int i = 0; i < P * V; ++i) ad.v[i] = fmaf(r.v[i], fmaf(kp, f[i] - dot, zl), ad.v[i]);
+      for (int i = 0; i < P * V; ++i)
+        ad.v[i] = fmaf(kl * r.v[i], l, fmaf(kp * r.v[i], f[i] - dot, ad.v[i]));
     }
 #pragma unroll
     for (int q = 0; q < P; ++q) {
