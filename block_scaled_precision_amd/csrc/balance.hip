@@ -593,7 +593,7 @@ __global__ __launch_bounds__(kThreadsB) void k_balance_grad(BalanceGradArgs a) {
         dot = fmaf(f[i], r.v[i], dot);
         sum += r.v[i];
       }
-      const float inv = 1.0f / group_reduce<L>(sum, Sum());
+      const float inv = __builtin_amdgcn_rcpf(group_reduce<L>(sum, Sum()));  // good to a step
       dot = group_reduce<L>(dot, Sum()) * inv;
       const float kp = ks * inv, kl = kz * inv;
       // (kl p first: kl lse may be past fp32's range where p is small, or 0)
