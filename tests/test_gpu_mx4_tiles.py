@@ -214,3 +214,23 @@ AT_ONCE = [(3000, 4104, 1920, 0, True), (5000, 1544, 2304, 5, False), (9300, 256
 def test_prepared_calls_at_once_and_captured(monkeypatch):
     monkeypatch.setattr(lin, "AT_ONCE", AT_ONCE)
     lin.test_prepared_calls_at_once_and_captured()
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 256, 128), (255, 256, 7168), (700, 1032, 128), (700, 1032, 1152), (1500, 4104, 512),
+                                   (3000, 4104, 1920)])
+def test_every_pair_of_scales(M, N, K):
+    """1 times 1 at the first and the last k, with every scale of a row against every scale of a
+    column: 2^-254 to 2^254, of which bf16 holds 2^-133 (a subnormal) to 2^127; from half of
+    its smallest number down they are 0, above its range infinite."""
+    from block_scaled_precision_amd import moe_mx as m
+    ra, rw = torch.arange(M) % 255, torch.arange(N) % 255
+    e = (ra[:, None] + rw - 254).numpy()
+    for k in (0, K - 1):
+        (a, asc), (w, wsc) = _codes((M,), K, 70), _codes((N,), K, 71)
+        for t, s, r in ((a, asc, ra), (w, wsc, rw)):
+            t.zero_()
+            t[:, k // 2] = 2 << 4 * (k % 2)
+            s[:, k // 32] = r.to(torch.uint8)
+        got = _np(m.mx4_linear(a.cuda(), w.cuda(), wsc.cuda(), a_scale=asc.cuda()))
+        want = np.where(e > 127, np.inf, np.where(e < -133, 0.0, np.ldexp(1.0, e)))
+        assert np.array_equal(got, want)
